@@ -306,6 +306,94 @@ int gmm_kmeans_iterate(const void* X, int32_t x_dtype, int64_t N, int32_t d, int
 /* Workspace bytes for the k-means entry points; 0 outside the limits. */
 size_t gmm_kmeans_workspace_bytes(int64_t N, int32_t d, int32_t K);
 
+/* ---------------------------------------------------------------------------
+ * Learned products around the mixture: the projection of wide rows to the
+ * features a mixture is fitted on (and any layer of a feature network), and
+ * the layer of experts that the mixture's posterior gates.
+ *
+ * These entry points keep the conventions above, with two differences. Their
+ * matrices (X, W, bias, P, W1, b1, W2, b2) all have the type x_dtype, whose
+ * products are accumulated in float. Widths are larger: 1 <= d_in, d_out, D,
+ * F <= 65536. */
+
+/* Activations. gelu is z * Phi(z) (the normal distribution function). */
+enum gmm_activation { GMM_ACT_NONE = 0, GMM_ACT_RELU = 1, GMM_ACT_GELU = 2, GMM_ACT_SILU = 3 };
+
+/* Linear layer with its epilogue:
+ *   z = X W^T + bias,   Y = act(z) + residual
+ * X is N x d_in, W is d_out x d_in, bias d_out; Y, residual and pre are
+ * N x d_out of y_dtype, which is x_dtype or GMM_F32. bias, residual and pre
+ * are nullable; pre receives z, which gmm_linear_backward needs unless act is
+ * GMM_ACT_NONE. All arithmetic is float, rounded once per output. Y may be
+ * residual itself; no other output may overlap an input. Where a row of X is
+ * a multiple of 16 bytes long, X and W must be 16-byte aligned (rows of other
+ * lengths may start at any element). N < 2^31. The workspace must hold
+ * gmm_linear_workspace_bytes(N, d_in, d_out, x_dtype, 0) bytes. */
+int gmm_linear(const void* X, int32_t x_dtype, int64_t N, int32_t d_in, const void* W, int32_t d_out,
+               const void* bias, int32_t act, const void* residual, void* Y, int32_t y_dtype, void* pre,
+               void* workspace, size_t ws_bytes, void* stream);
+
+/* Gradients of gmm_linear for dY (N x d_out of y_dtype) and the pre that the
+ * forward call wrote (may be NULL when act is GMM_ACT_NONE):
+ *   dZ = dY act'(pre),  dX = dZ W,  dW = dZ^T X,  db = sum_n dZ_n
+ * (the residual's gradient is dY). dX (N x d_in), dW (d_out x d_in) and db
+ * (d_out) have type x_dtype; each is nullable, and what only the others need
+ * may be NULL too (W without dX, X without dW). relu's slope at 0 is 0. The
+ * products take dZ rounded to x_dtype, as the matrix instructions do, and
+ * accumulate in float; db sums the unrounded dZ in float. Sums run in a fixed
+ * order. N = 0 gives dW = 0 and db = 0. Alignment of X and W as above. The
+ * workspace must hold gmm_linear_workspace_bytes(N, d_in, d_out, x_dtype, 1)
+ * bytes. */
+int gmm_linear_backward(const void* dY, int32_t y_dtype, const void* X, int32_t x_dtype, int64_t N, int32_t d_in,
+                        const void* W, int32_t d_out, const void* pre, int32_t act, void* dX, void* dW, void* db,
+                        void* workspace, size_t ws_bytes, void* stream);
+
+/* Workspace bytes for gmm_linear (backward = 0) or gmm_linear_backward
+ * (backward = 1); 0 for arguments outside the limits. */
+size_t gmm_linear_workspace_bytes(int64_t N, int32_t d_in, int32_t d_out, int32_t x_dtype, int32_t backward);
+
+/* Layer of experts gated by the mixture's posterior (a mixture of experts),
+ * for the few rows of a serving step: N <= 128. One expert per component; a
+ * row goes to the experts of its most probable components, as in
+ * gmm_assign_top2 and gmm_border_lists:
+ *   f = P x                              (features, P is d x D, d <= 128)
+ *   s_k = logw_k + log N(f | mu_k, diag var_k),  r = softmax_k(s)
+ *   picks: the `top` (1..8) largest s (ties go to the lower index); a pick
+ *     after the first is dropped when r < border_threshold, and a component
+ *     with s = -inf is never picked
+ *   w = r, or with renorm != 0 r / (sum of the kept picks' r)
+ *   y = residual + sum over picks of w (W2_k a + b2_k)
+ *   a = act(W1_k x + b1_k), or with glu != 0
+ *   a = act(g) u with [g; u] = W1_k x + b1_k (W1_k is 2F x D, g first)
+ * X, residual and Y are N x D; W1 is K x F x D (K x 2F x D with glu), b1
+ * K x F (K x 2F), W2 K x D x F, b2 K x D; b1, b2 and residual are nullable.
+ * idx (N x top int32) and resp (N x top float) receive the picks and their r,
+ * -1 and 0 for a dropped or missing one. The gate is computed in double
+ * precision; a is rounded to x_dtype between the two products. A row whose
+ * posterior is not a number (NaN or infinite features) has no picks and a y
+ * of NaN. Y may be X or residual itself. The workspace must hold
+ * gmm_expert_workspace_bytes(N, D, K, F, d, top, x_dtype) bytes. */
+int gmm_expert_layer(const void* X, int32_t x_dtype, int64_t N, int32_t D, const void* P, int32_t d, const float* mu,
+                     const float* var, const float* logw, int32_t K, int32_t top, float border_threshold,
+                     int32_t renorm, const void* W1, const void* b1, const void* W2, const void* b2, int32_t F,
+                     int32_t act, int32_t glu, const void* residual, void* Y, int32_t* idx, float* resp,
+                     void* workspace, size_t ws_bytes, void* stream);
+
+/* The experts of gmm_expert_layer for picks that the caller has (idx and wts
+ * of gmm_assign_top2, or any other gate's): idx N x top int32, wts N x top
+ * float combination weights. A pick outside [0, K) is skipped; a row may pick
+ * an expert more than once. The workspace must hold
+ * gmm_expert_workspace_bytes(N, D, K, F, 0, top, x_dtype) bytes. */
+int gmm_expert_rows(const void* X, int32_t x_dtype, int64_t N, int32_t D, const int32_t* idx, const float* wts,
+                    int32_t top, int32_t K, const void* W1, const void* b1, const void* W2, const void* b2, int32_t F,
+                    int32_t act, int32_t glu, const void* residual, void* Y, void* workspace, size_t ws_bytes,
+                    void* stream);
+
+/* Workspace bytes for gmm_expert_layer (d >= 1) or gmm_expert_rows (d = 0);
+ * 0 for arguments outside the limits. */
+size_t gmm_expert_workspace_bytes(int64_t N, int32_t D, int32_t K, int32_t F, int32_t d, int32_t top,
+                                  int32_t x_dtype);
+
 #ifdef __cplusplus
 }
 #endif

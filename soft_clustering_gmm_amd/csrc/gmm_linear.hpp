@@ -1,0 +1,73 @@
+// Internal declarations of the linear layer (gmm_linear, gmm_linear_backward).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace gmm {
+
+// One product C[m][n] = sum_k A(m, k) B(n, k) on 16-byte aligned operands.
+// An operand is "k-contiguous" (element (r, k) at p[r * ld + k]) or
+// "k-strided" (element (r, k) at p[k * ld + r]); ld * element size is a
+// multiple of 16. Elements of a k-contiguous operand between K and the next
+// multiple of 16 bytes are zero.
+struct ProductArgs {
+  const void* A;
+  const void* B;
+  int64_t lda, ldb;
+  int64_t M, K;
+  int N;
+  int tiles_m, tiles_n;  // output tiles of this launch
+  int splits;            // parts of the contraction (> 1: partial sums in `partial`)
+  int64_t split_k;       // k per part, a multiple of the k step
+  // epilogue (splits == 1): C = act(z + bias) + residual; pre receives z + bias
+  const void* bias;      // element type of the operands
+  const void* residual;  // type of C
+  void* C;
+  void* pre;             // type of C
+  int c_f32;             // C, residual and pre are float (else the operands' type)
+  int c_vec;             // rows of C, residual and pre allow 16-byte accesses
+  int b_vec;             // bias allows 16-byte loads
+  float* partial;        // [splits][M][N]
+};
+
+// Tile variants of the product kernel.
+enum { kTile256 = 0, kTile128 = 1, kTile64 = 2, kTileVariants = 3 };
+constexpr int kTileRows[kTileVariants] = {256, 128, 64};
+constexpr int kStepBytes = 128;  // bytes of k per step and operand row
+
+// Few rows: C[m][n] of at most kFewRows rows, operands of any alignment,
+// B (the weights) streamed once.
+constexpr int kFewRows = 64;
+
+struct FewArgs {
+  const void* A;  // [M][K]
+  const void* B;  // [N][K]
+  int M, N, K;
+  const void* bias;
+  const void* residual;
+  void* C;
+  void* pre;
+  int c_f32;
+};
+
+template <typename T>
+hipError_t launch_product(int variant, bool a_strided, bool b_strided, int act, const ProductArgs& p, hipStream_t s);
+template <typename T>
+hipError_t launch_few(int act, const FewArgs& p, hipStream_t s);
+// Rows of `cols` elements copied to rows of `ld` elements, zeros behind.
+template <typename T>
+hipError_t launch_pad(const T* src, T* dst, int64_t rows, int cols, int64_t ld, hipStream_t s);
+// Sum of the parts, then the epilogue of ProductArgs.
+template <typename T>
+hipError_t launch_reduce(int act, const ProductArgs& p, hipStream_t s);
+// dZ = dY act'(pre) in the operands' type, rows of ldz elements (zeros
+// behind), and per-chunk column sums of the unrounded dZ in db_part; dZ or
+// db_part may be null.
+template <typename T>
+hipError_t launch_dz(int act, const void* dY, const void* pre, int y_f32, int64_t rows, int cols, T* dZ, int64_t ldz,
+                     float* db_part, int64_t chunk_rows, hipStream_t s);
+template <typename T>
+hipError_t launch_db(const float* db_part, int64_t chunks, int cols, T* db, hipStream_t s);
+
+}  // namespace gmm

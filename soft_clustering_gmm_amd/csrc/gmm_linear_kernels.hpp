@@ -1,0 +1,564 @@
+// Kernels of the linear layer, instantiated once per element type
+// (gmm_linear_f32.hip, gmm_linear_f16.hip, gmm_linear_bf16.hip).
+#pragma once
+
+#include <type_traits>
+
+#include "gmm_linear.hpp"
+#include "gmm_product.hpp"
+
+namespace gmm {
+
+typedef __attribute__((address_space(3))) void* lds_ptr;
+
+__device__ __forceinline__ lds_ptr to_lds(const void* p) {
+  return reinterpret_cast<lds_ptr>(reinterpret_cast<uintptr_t>(p));
+}
+
+// ---------------------------------------------------------------------------
+// Tiled product. A block computes a BM x BN tile of C with WM x WN waves; a
+// step of the contraction brings kStepBytes of k of both operands into one
+// half of LDS, by loads that go to LDS directly, while the waves multiply the
+// other half. One barrier per step: it says both that the step's tiles have
+// arrived and that nobody reads the half that is filled next.
+//
+// The matrix instruction gets B's rows (n) as its first operand and A's rows
+// (m) as its second, so a lane's results are 4 consecutive n of one m; the
+// 16 instruction rows of tile i of a wave's NI tiles stand for
+//   n = (r / 4) * 4 NI + 4 i + r % 4,
+// so over the NI tiles a lane owns 4 NI consecutive n and stores whole
+// 16-byte pieces straight from its registers.
+//
+// LDS layouts, in 16-byte chunks, the chunk's place XORed with a key of its
+// row so that the fragment reads of a wave spread over the banks:
+//   k-contiguous: [row][8 chunks of k], key from the row;
+//   k-strided:    [k][BR / kPer chunks of rows], key from k.
+// ---------------------------------------------------------------------------
+
+template <int NI>
+__device__ __forceinline__ int key_rows_perm(int n) {  // rows in the order above
+  return (n & 3) | (((n / (4 * NI)) & 1) << 2);
+}
+__device__ __forceinline__ int key_rows(int r) { return r & 7; }  // rows in natural order
+// k-strided tiles of 2-byte elements: the transposing read takes, per 16
+// lanes, 4 values of k x 16 rows. Natural rows: 32 bytes of each k, moved
+// apart by the key. Permuted rows: 8 bytes every 4 NI elements of each k.
+__device__ __forceinline__ int key_k(int k) { return (k & 3) << 1; }
+template <int NI>
+__device__ __forceinline__ int key_k_perm(int k) {
+  return NI == 4 ? (k & 1) | ((k & 2) << 2) : (k & 1) << 2;
+}
+
+template <typename T, int BR, int NWAVES, bool STRIDED, bool PERM, int NI>
+struct Operand {
+  static constexpr int kPer = Frag<T>::kPer;
+  static constexpr int kStep = kStepBytes / (int)sizeof(T);  // k per step
+  static constexpr int kBytes = BR * kStepBytes;
+  static constexpr int kLoads = kBytes / 1024 / NWAVES;  // wave loads of 1 KB
+  static constexpr int kRowChunks = BR * (int)sizeof(T) / 16;  // k-strided: chunks per k
+
+  const char* base;   // element (first row of the tile, first k of the part)
+  int64_t step_bytes;  // from one step to the next
+  int64_t left;        // bytes from base to the operand's end (k-strided: to the end of the part's k range)
+  uint32_t off[kLoads];  // byte offset of this lane's chunk from base
+  int kchunk[kLoads];    // k-contiguous: first k of the lane's chunk within the step
+
+  __device__ __forceinline__ void init(const void* p, int64_t ld, int64_t r0, int64_t rows, int64_t k0, int64_t k1,
+                                       int wave, int lane) {
+    const int e = sizeof(T);
+    if (STRIDED) {
+      base = static_cast<const char*>(p) + (k0 * ld + r0) * e;
+      step_bytes = kStep * ld * e;
+      left = ((k1 - k0) * ld - r0) * e;
+    } else {
+      base = static_cast<const char*>(p) + (r0 * ld + k0) * e;
+      step_bytes = kStepBytes;
+      left = ((rows - r0) * ld - k0) * e;
+    }
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      const int ch = (wave * kLoads + j) * 64 + lane;  // chunk of the tile in LDS order
+      if (STRIDED) {
+        const int k = ch / kRowChunks, c = (ch % kRowChunks) ^ (PERM ? key_k_perm<NI>(k) : key_k(k));
+        off[j] = (uint32_t)(k * ld * e + 16 * c);
+        kchunk[j] = k;
+      } else {
+        const int r = ch / 8, c = (ch % 8) ^ (PERM ? key_rows_perm<NI>(r) : key_rows(r));
+        off[j] = (uint32_t)(r * ld * e + 16 * c);
+        kchunk[j] = c * kPer;
+      }
+    }
+  }
+
+  // Loads of the step that starts `k` into the part, of whose k `k_left` remain.
+  __device__ __forceinline__ void load(char* lds, int64_t step, int64_t k_left, int wave) {
+    const char* b = base + step * step_bytes;
+    int64_t n = left - step * step_bytes;
+    n = n < 0 ? 0 : n > 0x7fffffff ? 0x7fffffff : n;
+    // reads past the end give zeros
+    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(b), 0, (int)n, 0x00027000);
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      const uint32_t o = kchunk[j] < k_left ? off[j] : 0x80000000u;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, to_lds(lds + (wave * kLoads + j) * 1024), 16, (int)o, 0, 0, 0);
+    }
+  }
+
+  // Fragment of the 16 rows of tile i (of a wave whose rows start at w0), k
+  // chunks 4 kk + l / 16 of the step.
+  static __device__ __forceinline__ u32x4 frag(const char* lds, int w0, int i, int kk, int lane) {
+    const int r = lane & 15, g = lane >> 4;
+    if (!STRIDED) {
+      const int row = w0 + (PERM ? (r >> 2) * 4 * NI + 4 * i + (r & 3) : 16 * i + r);
+      const int c = (4 * kk + g) ^ (PERM ? key_rows_perm<NI>(row) : key_rows(row));
+      return *reinterpret_cast<const u32x4*>(lds + row * kStepBytes + 16 * c);
+    }
+    if constexpr (sizeof(T) == 4) {
+      const int row = w0 + (PERM ? (r >> 2) * 4 * NI + 4 * i + (r & 3) : 16 * i + r);
+      u32x4 v;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int k = 16 * kk + 4 * g + q;
+        const int c = (row >> 2) ^ (PERM ? key_k_perm<NI>(k) : key_k(k));
+        v[q] = *reinterpret_cast<const uint32_t*>(lds + (k * kRowChunks + c) * 16 + 4 * (row & 3));
+      }
+      return v;
+    } else {
+      // Two transposing reads: over 16 lanes, lane t gives the address of 4
+      // consecutive rows of k = t / 4, and receives 4 consecutive k of row t.
+      const int row = w0 + (PERM ? (r & 3) * 4 * NI + 4 * i : 16 * i + 4 * (r & 3));
+      u32x4 v;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int k = 32 * kk + 8 * g + 4 * h + (r >> 2);
+        const int c = (row >> 3) ^ (PERM ? key_k_perm<NI>(k) : key_k(k));
+        const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (__attribute__((address_space(3))) s16x4*)to_lds(lds + (k * kRowChunks + c) * 16 + 2 * (row & 7)));
+        const uint2 y = __builtin_bit_cast(uint2, x);
+        v[2 * h] = y.x;
+        v[2 * h + 1] = y.y;
+      }
+      return v;
+    }
+  }
+};
+
+// Loads / stores of W consecutive values of C's type as floats. `vec`: 16-byte
+// accesses are allowed; n is the number of values inside the row.
+template <typename T, int W>
+__device__ __forceinline__ void load_row(const void* p, int64_t at, int n, bool is_f32, bool vec, float* out) {
+  if (is_f32) {
+    const float* q = static_cast<const float*>(p) + at;
+    if (vec && n >= W) {
+#pragma unroll
+      for (int i = 0; i < W; i += 4) *reinterpret_cast<f32x4*>(out + i) = *reinterpret_cast<const f32x4*>(q + i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i) out[i] = i < n ? q[i] : 0.f;
+    }
+  } else {
+    const T* q = static_cast<const T*>(p) + at;
+    constexpr int P = 16 / sizeof(T);
+    if (vec && n >= W) {
+#pragma unroll
+      for (int i = 0; i < W; i += P) {
+        union {
+          u32x4 v;
+          T e[P];
+        } u;
+        u.v = *reinterpret_cast<const u32x4*>(q + i);
+#pragma unroll
+        for (int k = 0; k < P; ++k) out[i + k] = (float)u.e[k];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i) out[i] = i < n ? (float)q[i] : 0.f;
+    }
+  }
+}
+
+template <typename T, int W>
+__device__ __forceinline__ void store_row(void* p, int64_t at, int n, bool is_f32, bool vec, const float* v) {
+  if (is_f32) {
+    float* q = static_cast<float*>(p) + at;
+    if (vec && n >= W) {
+#pragma unroll
+      for (int i = 0; i < W; i += 4) *reinterpret_cast<f32x4*>(q + i) = f32x4{v[i], v[i + 1], v[i + 2], v[i + 3]};
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i)
+        if (i < n) q[i] = v[i];
+    }
+  } else {
+    T* q = static_cast<T*>(p) + at;
+    constexpr int P = 16 / sizeof(T);
+    if (vec && n >= W) {
+#pragma unroll
+      for (int i = 0; i < W; i += P) {
+        union {
+          u32x4 v;
+          T e[P];
+        } u;
+#pragma unroll
+        for (int k = 0; k < P; ++k) u.e[k] = (T)v[i + k];
+        *reinterpret_cast<u32x4*>(q + i) = u.v;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i)
+        if (i < n) q[i] = (T)v[i];
+    }
+  }
+}
+
+// z + bias -> pre, act(.) + residual -> C for W consecutive n of one row.
+template <typename T, int ACT, int W>
+__device__ __forceinline__ void finish_row(const ProductArgs& p, int64_t m, int n, float* z, const float* bias) {
+  const int64_t at = m * p.N + n;
+  const int left = p.N - n;
+#pragma unroll
+  for (int i = 0; i < W; ++i) z[i] += bias[i];
+  if (p.pre) store_row<T, W>(p.pre, at, left, p.c_f32, p.c_vec, z);
+#pragma unroll
+  for (int i = 0; i < W; ++i) z[i] = act_value<ACT>(z[i]);
+  if (p.residual) {
+    float r[W];
+    load_row<T, W>(p.residual, at, left, p.c_f32, p.c_vec, r);
+#pragma unroll
+    for (int i = 0; i < W; ++i) z[i] += r[i];
+  }
+  store_row<T, W>(p.C, at, left, p.c_f32, p.c_vec, z);
+}
+
+template <typename T, int BM, int BN, int WM, int WN, bool AS, bool BS, int ACT>
+__global__ void __launch_bounds__(64 * WM * WN)
+product_kernel(const ProductArgs p) {
+  constexpr int NW = WM * WN, TM = BM / WM, TN = BN / WN, MI = TM / 16, NI = TN / 16, W = 4 * NI;
+  using OA = Operand<T, BM, NW, AS, false, 1>;
+  using OB = Operand<T, BN, NW, BS, true, NI>;
+  constexpr int kHalf = OA::kBytes + OB::kBytes;
+  __shared__ __align__(1024) char lds[2 * kHalf];
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wm = wave / WN, wn = wave % WN;
+  // Tiles in groups of 8 tile rows, column by column within a group, so that
+  // the blocks an XCD runs together share rows of A and of B in its L2.
+  const int tiles = p.tiles_m * p.tiles_n;
+  const int part = blockIdx.x / tiles;
+  const int t = xcd_place(blockIdx.x - part * tiles, tiles);
+  constexpr int G = 8;
+  const int group = t / (G * p.tiles_n), first = group * G;
+  const int height = min(G, p.tiles_m - first), in = t - group * G * p.tiles_n;
+  const int tm = first + in % height, tn = in / height;
+  const int64_t m0 = (int64_t)tm * BM;
+  const int n0 = tn * BN;
+  const int64_t k0 = part * p.split_k, k1 = min(p.K, k0 + p.split_k);
+
+  OA a;
+  OB b;
+  a.init(p.A, p.lda, m0, p.M, k0, k1, wave, lane);
+  b.init(p.B, p.ldb, n0, p.N, k0, k1, wave, lane);
+
+  f32x4 acc[MI][NI];
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NI; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  const int64_t steps = (k1 - k0 + OA::kStep - 1) / OA::kStep;
+  a.load(lds, 0, k1 - k0, wave);
+  b.load(lds + OA::kBytes, 0, k1 - k0, wave);
+  for (int64_t s = 0; s < steps; ++s) {
+    const char* cur = lds + (s & 1) * kHalf;
+    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): this wave's part of the step has arrived
+    __syncthreads();
+    if (s + 1 < steps) {
+      char* nxt = lds + ((s + 1) & 1) * kHalf;
+      const int64_t k_left = k1 - k0 - (s + 1) * OA::kStep;
+      a.load(nxt, s + 1, k_left, wave);
+      b.load(nxt + OA::kBytes, s + 1, k_left, wave);
+    }
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      u32x4 fb[NI], fa[MI];
+#pragma unroll
+      for (int j = 0; j < NI; ++j) fb[j] = OB::frag(cur + OA::kBytes, wn * TN, j, kk, lane);
+#pragma unroll
+      for (int i = 0; i < MI; ++i) fa[i] = OA::frag(cur, wm * TM, i, kk, lane);
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < NI; ++j) acc[i][j] = Frag<T>::mma(fb[j], fa[i], acc[i][j]);
+    }
+  }
+
+  const int n = n0 + wn * TN + (lane >> 4) * W;
+  if (n >= p.N) return;
+  float bias[W];
+#pragma unroll
+  for (int i = 0; i < W; ++i) bias[i] = 0.f;
+  const bool whole = p.splits == 1;
+  if (whole && p.bias) load_row<T, W>(p.bias, n, p.N - n, false, p.b_vec, bias);
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    const int64_t m = m0 + wm * TM + 16 * i + (lane & 15);
+    if (m >= p.M) continue;
+    float z[W];
+#pragma unroll
+    for (int j = 0; j < NI; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) z[4 * j + q] = acc[i][j][q];
+    if (whole)
+      finish_row<T, ACT, W>(p, m, n, z, bias);
+    else
+      store_row<T, W>(p.partial, ((int64_t)part * p.M + m) * p.N + n, p.N - n, true, p.N % 4 == 0, z);
+  }
+}
+
+// C from the partial sums, in the order of the parts. One thread per 4 (or 1)
+// consecutive n.
+template <typename T, int ACT, int W>
+__global__ void __launch_bounds__(256) product_reduce_kernel(const ProductArgs p) {
+  const int per_row = (p.N + W - 1) / W;
+  const int64_t total = p.M * per_row, part = p.M * p.N;
+  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
+    const int64_t m = i / per_row;
+    const int n = (int)(i - m * per_row) * W;
+    float z[W], bias[W];
+#pragma unroll
+    for (int k = 0; k < W; ++k) z[k] = bias[k] = 0.f;
+    const float* q = p.partial + m * p.N + n;
+    for (int s = 0; s < p.splits; ++s) {
+      float v[W];
+      load_row<T, W>(q + s * part, 0, W, true, W == 4, v);
+#pragma unroll
+      for (int k = 0; k < W; ++k) z[k] += v[k];
+    }
+    if (p.bias) load_row<T, W>(p.bias, n, W, false, false, bias);
+    if (W == 1 || p.c_f32) {
+      finish_row<T, ACT, W>(p, m, n, z, bias);
+    } else {  // 4 values of 2 bytes: 8-byte rows, element accesses
+      ProductArgs e = p;
+      e.c_vec = 0;
+      finish_row<T, ACT, W>(e, m, n, z, bias);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Few rows. The weights are read once and everything else is small, so the
+// kernel is a stream over B: a block owns 16 rows of B, its waves split the
+// contraction, and every lane holds several 16-byte loads of B in flight. The
+// rows of A come from the caches, 16 at a time as the second operand.
+// ---------------------------------------------------------------------------
+template <typename T, int NW, int RT, int ACT>
+__global__ void __launch_bounds__(64 * NW) few_kernel(const FewArgs p) {
+  constexpr int P = Frag<T>::kPer, kStep = 4 * P, U = RT == 1 ? 8 : 4;
+  __shared__ float red[NW][RT][16][17];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
+  const int n0 = blockIdx.x * 16;
+  const int brow = min(n0 + r, p.N - 1);
+  const T* B = static_cast<const T*>(p.B) + (int64_t)brow * p.K + g * P;
+  const T* A[RT];
+#pragma unroll
+  for (int t = 0; t < RT; ++t)
+    A[t] = static_cast<const T*>(p.A) + (int64_t)min(16 * t + r, p.M - 1) * p.K + g * P;
+  f32x4 acc[RT];
+#pragma unroll
+  for (int t = 0; t < RT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int steps = (p.K + kStep - 1) / kStep, per = (steps + NW - 1) / NW;
+  const int s0 = wave * per, s1 = min(steps, s0 + per);
+  int s = s0;
+  for (; s + U <= s1 && (s + U) * kStep <= p.K; s += U) {
+    u32x4 fb[U], fa[U][RT];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      fb[u] = load16(B + (s + u) * kStep);
+#pragma unroll
+      for (int t = 0; t < RT; ++t) fa[u][t] = load16(A[t] + (s + u) * kStep);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int t = 0; t < RT; ++t) acc[t] = Frag<T>::mma(fb[u], fa[u][t], acc[t]);
+  }
+  for (; s < s1; ++s) {
+    const int left = p.K - s * kStep - g * P;
+    const u32x4 fb = load_frag<T>(B + s * kStep, left);
+#pragma unroll
+    for (int t = 0; t < RT; ++t) acc[t] = Frag<T>::mma(fb, load_frag<T>(A[t] + s * kStep, left), acc[t]);
+  }
+#pragma unroll
+  for (int t = 0; t < RT; ++t)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) red[wave][t][r][4 * g + q] = acc[t][q];
+  __syncthreads();
+  for (int i = threadIdx.x; i < 256 * RT; i += 64 * NW) {
+    const int n = i & 15, m = i >> 4;
+    if (m >= p.M || n0 + n >= p.N) continue;
+    float z = 0.f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) z += red[w][m >> 4][m & 15][n];
+    ProductArgs e;
+    e.N = p.N;
+    e.residual = p.residual;
+    e.C = p.C;
+    e.pre = p.pre;
+    e.c_f32 = p.c_f32;
+    e.c_vec = 0;
+    float bias = p.bias ? (float)static_cast<const T*>(p.bias)[n0 + n] : 0.f;
+    finish_row<T, ACT, 1>(e, m, n0 + n, &z, &bias);
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) pad_kernel(const T* src, T* dst, int64_t rows, int cols, int64_t ld) {
+  const int64_t total = rows * ld;
+  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
+    const int64_t r = i / ld;
+    const int c = (int)(i - r * ld);
+    dst[i] = c < cols ? src[r * cols + c] : (T)0.f;
+  }
+}
+
+// dZ and the column sums of a chunk of rows. A block owns 64 columns and one
+// chunk; its 4 waves take every fourth row.
+template <typename T, int ACT>
+__global__ void __launch_bounds__(256)
+dz_kernel(const void* dY, const void* pre, int y_f32, int64_t rows, int cols, T* dZ, int64_t ldz, float* db_part,
+          int64_t chunk_rows) {
+  __shared__ float red[4][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t c = blockIdx.x * 64ll + lane;
+  const int64_t r0 = blockIdx.y * chunk_rows, r1 = min(rows, r0 + chunk_rows);
+  float sum = 0.f;
+  for (int64_t r = r0 + wave; r < r1; r += 4) {
+    float v = 0.f;
+    if (c < cols) {
+      const int64_t at = r * cols + c;
+      v = y_f32 ? static_cast<const float*>(dY)[at] : (float)static_cast<const T*>(dY)[at];
+      if (ACT != GMM_ACT_NONE)
+        v *= act_slope<ACT>(y_f32 ? static_cast<const float*>(pre)[at] : (float)static_cast<const T*>(pre)[at]);
+    }
+    sum += v;
+    if (dZ && c < ldz) dZ[r * ldz + c] = (T)v;
+  }
+  if (!db_part) return;
+  red[wave][lane] = sum;
+  __syncthreads();
+  if (wave == 0 && c < cols)
+    db_part[blockIdx.y * (int64_t)cols + c] = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) db_kernel(const float* part, int64_t chunks, int cols, T* db) {
+  __shared__ float red[4][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int c = blockIdx.x * 64 + lane;
+  float sum = 0.f;
+  if (c < cols)
+    for (int64_t i = wave; i < chunks; i += 4) sum += part[i * cols + c];
+  red[wave][lane] = sum;
+  __syncthreads();
+  if (wave == 0 && c < cols) db[c] = (T)((red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]));
+}
+
+// --------------------------------------------------------------------------- launchers
+
+template <typename F>
+hipError_t with_act(int act, F&& f) {
+  if (act == GMM_ACT_RELU) return f(std::integral_constant<int, GMM_ACT_RELU>{});
+  if (act == GMM_ACT_GELU) return f(std::integral_constant<int, GMM_ACT_GELU>{});
+  if (act == GMM_ACT_SILU) return f(std::integral_constant<int, GMM_ACT_SILU>{});
+  return f(std::integral_constant<int, GMM_ACT_NONE>{});
+}
+
+template <typename T, bool AS, bool BS, int ACT>
+static void launch_tile(int variant, const ProductArgs& p, hipStream_t s) {
+  const dim3 grid(p.tiles_m * p.tiles_n * p.splits);
+  if (variant == kTile256)
+    product_kernel<T, 256, 256, 2, 4, AS, BS, ACT><<<grid, 512, 0, s>>>(p);
+  else if (variant == kTile128)
+    product_kernel<T, 128, 128, 2, 2, AS, BS, ACT><<<grid, 256, 0, s>>>(p);
+  else
+    product_kernel<T, 64, 64, 2, 2, AS, BS, ACT><<<grid, 256, 0, s>>>(p);
+}
+
+template <typename T>
+hipError_t launch_product(int variant, bool a_strided, bool b_strided, int act, const ProductArgs& p, hipStream_t s) {
+  if (!a_strided && !b_strided)
+    return with_act(act, [&](auto a) {
+      launch_tile<T, false, false, decltype(a)::value>(variant, p, s);
+      return hipGetLastError();
+    });
+  // the gradients' products have no activation
+  if (!a_strided)
+    launch_tile<T, false, true, GMM_ACT_NONE>(variant, p, s);
+  else
+    launch_tile<T, true, true, GMM_ACT_NONE>(variant, p, s);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch_few(int act, const FewArgs& p, hipStream_t s) {
+  return with_act(act, [&](auto a) {
+    constexpr int ACT = decltype(a)::value;
+    const dim3 grid((p.N + 15) / 16);
+    if (p.M <= 16)
+      few_kernel<T, 8, 1, ACT><<<grid, 512, 0, s>>>(p);
+    else
+      few_kernel<T, 8, 4, ACT><<<grid, 512, 0, s>>>(p);
+    return hipGetLastError();
+  });
+}
+
+static unsigned blocks_for(int64_t items) {
+  const int64_t b = (items + 255) / 256;
+  return (unsigned)(b < 16384 ? b : 16384);
+}
+
+template <typename T>
+hipError_t launch_pad(const T* src, T* dst, int64_t rows, int cols, int64_t ld, hipStream_t s) {
+  pad_kernel<T><<<blocks_for(rows * ld), 256, 0, s>>>(src, dst, rows, cols, ld);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch_reduce(int act, const ProductArgs& p, hipStream_t s) {
+  return with_act(act, [&](auto a) {
+    constexpr int ACT = decltype(a)::value;
+    if (p.N % 4 == 0)
+      product_reduce_kernel<T, ACT, 4><<<blocks_for(p.M * (p.N / 4)), 256, 0, s>>>(p);
+    else
+      product_reduce_kernel<T, ACT, 1><<<blocks_for(p.M * p.N), 256, 0, s>>>(p);
+    return hipGetLastError();
+  });
+}
+
+template <typename T>
+hipError_t launch_dz(int act, const void* dY, const void* pre, int y_f32, int64_t rows, int cols, T* dZ, int64_t ldz,
+                     float* db_part, int64_t chunk_rows, hipStream_t s) {
+  return with_act(act, [&](auto a) {
+    const int64_t w = dZ ? ldz : cols;
+    const dim3 grid((unsigned)((w + 63) / 64), (unsigned)((rows + chunk_rows - 1) / chunk_rows));
+    dz_kernel<T, decltype(a)::value><<<grid, 256, 0, s>>>(dY, pre, y_f32, rows, cols, dZ, ldz, db_part, chunk_rows);
+    return hipGetLastError();
+  });
+}
+
+template <typename T>
+hipError_t launch_db(const float* db_part, int64_t chunks, int cols, T* db, hipStream_t s) {
+  db_kernel<T><<<(cols + 63) / 64, 256, 0, s>>>(db_part, chunks, cols, db);
+  return hipGetLastError();
+}
+
+#define GMM_LINEAR_TYPE(T)                                                                                         \
+  template hipError_t launch_product<T>(int, bool, bool, int, const ProductArgs&, hipStream_t);                    \
+  template hipError_t launch_few<T>(int, const FewArgs&, hipStream_t);                                             \
+  template hipError_t launch_pad<T>(const T*, T*, int64_t, int, int64_t, hipStream_t);                             \
+  template hipError_t launch_reduce<T>(int, const ProductArgs&, hipStream_t);                                      \
+  template hipError_t launch_dz<T>(int, const void*, const void*, int, int64_t, int, T*, int64_t, float*, int64_t, \
+                                   hipStream_t);                                                                   \
+  template hipError_t launch_db<T>(const float*, int64_t, int, T*, hipStream_t);
+
+}  // namespace gmm

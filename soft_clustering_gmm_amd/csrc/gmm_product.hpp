@@ -1,0 +1,107 @@
+// Device code shared by the product kernels (the linear layer and the layer
+// of experts): element types, matrix instructions, activations.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/gmm.h"
+
+namespace gmm {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+// One 16-byte fragment holds kPer elements. The 64 lanes of a wave hold 16
+// rows x 4 groups of kPer consecutive k: lane l has row l % 16, group l / 16.
+// mma() multiplies such a fragment of A with one of B over those 4 kPer
+// values of k and adds to D: lane l has column l % 16 of B and rows
+// 4 (l / 16) + i of A. The single-precision instruction takes one k per lane
+// and group, so it runs once per element of the fragment; which k meet in
+// which instruction does not matter, as both fragments agree on it.
+template <typename T>
+struct Frag;
+
+template <>
+struct Frag<float> {
+  static constexpr int kPer = 4;
+  static __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
+    const f32x4 x = __builtin_bit_cast(f32x4, a), y = __builtin_bit_cast(f32x4, b);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(x[i], y[i], c, 0, 0, 0);
+    return c;
+  }
+};
+
+template <>
+struct Frag<_Float16> {
+  static constexpr int kPer = 8;
+  static __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0,
+                                                  0);
+  }
+};
+
+template <>
+struct Frag<__bf16> {
+  static constexpr int kPer = 8;
+  static __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                   0, 0);
+  }
+};
+
+// Activations in single precision. gelu is the exact one, z Phi(z).
+// exp(-z) of a far negative z is +inf, and the quotients then give 0 as they
+// should. A NaN z stays NaN.
+template <int ACT>
+__device__ __forceinline__ float act_value(float z) {
+  if (ACT == GMM_ACT_RELU) return z < 0.f ? 0.f : z;  // keeps a NaN
+  if (ACT == GMM_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+  if (ACT == GMM_ACT_SILU) return z / (1.f + __expf(-z));
+  return z;
+}
+
+template <int ACT>
+__device__ __forceinline__ float act_slope(float z) {
+  if (ACT == GMM_ACT_RELU) return z > 0.f ? 1.f : z == z ? 0.f : z;
+  if (ACT == GMM_ACT_GELU)
+    return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + 0.39894228040143268f * z * __expf(-0.5f * z * z);
+  if (ACT == GMM_ACT_SILU) {
+    const float q = 1.f / (1.f + __expf(-z));
+    return q * (1.f + z * (1.f - q));
+  }
+  return 1.f;
+}
+
+// 16 bytes from an address of any alignment (the hardware's unaligned loads).
+__device__ __forceinline__ u32x4 load16(const void* p) {
+  u32x4 v;
+  __builtin_memcpy(&v, p, 16);
+  return v;
+}
+
+// The kPer elements at p[0..], zero from n on (n <= 0: all zero, p not read).
+template <typename T>
+__device__ __forceinline__ u32x4 load_frag(const T* p, int n) {
+  if (n >= Frag<T>::kPer) return load16(p);
+  union {
+    u32x4 v;
+    T e[Frag<T>::kPer];
+  } u;
+#pragma unroll
+  for (int i = 0; i < Frag<T>::kPer; ++i) u.e[i] = i < n ? p[i] : (T)0.f;
+  return u.v;
+}
+
+// Block b of `total` in launch order -> its place in an order in which the
+// blocks that one XCD runs (every eighth) are neighbours and share its L2.
+__device__ __forceinline__ int xcd_place(int b, int total) {
+  const int q = total >> 3, r = total & 7, x = b & 7, i = b >> 3;
+  return x < r ? x * (q + 1) + i : r * (q + 1) + (x - r) * q + i;
+}
+
+}  // namespace gmm

@@ -18,6 +18,7 @@ LIB_PATH = os.path.join(_HERE, "libgmm_mi355x.so")
 
 GMM_F32, GMM_F16, GMM_BF16 = 0, 1, 2
 REGIME_AUTO, REGIME_SINGLE, REGIME_TWOPASS, REGIME_SMALLK = 0, 1, 2, 3
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_SILU = 0, 1, 2, 3
 STATS_FP32, STATS_SPLIT_BF16, STATS_AUTO = 0, 1, 2  # STATS_AUTO is the default
 
 EXPORTS = (
@@ -27,6 +28,8 @@ EXPORTS = (
     "gmm_border_lists", "gmm_border_lists_workspace_bytes",
     "gmm_kmeans_assign", "gmm_kmeans_update", "gmm_kmeans_iterate", "gmm_kmeans_workspace_bytes",
     "gmm_plan_info", "gmm_estep_stats_static",
+    "gmm_linear", "gmm_linear_backward", "gmm_linear_workspace_bytes",
+    "gmm_expert_layer", "gmm_expert_rows", "gmm_expert_workspace_bytes",
     "gmm_peak_mfma", "gmm_peak_mfma_flops", "gmm_peak_hbm_read", "gmm_peak_coissue",
 )
 PEAK_FP32, PEAK_FP64 = 0, 1
@@ -94,6 +97,19 @@ def _load() -> ctypes.CDLL:
     L.gmm_peak_coissue.argtypes = [I32, I64, I32, P, P]
     L.gmm_estep_stats_static.restype = ctypes.c_int
     L.gmm_estep_stats_static.argtypes = [P, I32, I64, I32, P, P, P, I32, P, P, P, P, P, P]
+    L.gmm_linear.restype = ctypes.c_int
+    L.gmm_linear.argtypes = [P, I32, I64, I32, P, I32, P, I32, P, P, I32, P, P, SZ, P]
+    L.gmm_linear_backward.restype = ctypes.c_int
+    L.gmm_linear_backward.argtypes = [P, I32, P, I32, I64, I32, P, I32, P, I32, P, P, P, P, SZ, P]
+    L.gmm_linear_workspace_bytes.restype = SZ
+    L.gmm_linear_workspace_bytes.argtypes = [I64, I32, I32, I32, I32]
+    L.gmm_expert_layer.restype = ctypes.c_int
+    L.gmm_expert_layer.argtypes = [P, I32, I64, I32, P, I32, P, P, P, I32, I32, F32, I32, P, P, P, P, I32, I32, I32, P,
+                                   P, P, P, P, SZ, P]
+    L.gmm_expert_rows.restype = ctypes.c_int
+    L.gmm_expert_rows.argtypes = [P, I32, I64, I32, P, P, I32, I32, P, P, P, P, I32, I32, I32, P, P, P, SZ, P]
+    L.gmm_expert_workspace_bytes.restype = SZ
+    L.gmm_expert_workspace_bytes.argtypes = [I64, I32, I32, I32, I32, I32, I32]
     return L
 
 
@@ -132,6 +148,9 @@ def _xtype(X: torch.Tensor) -> int:
     if X.dtype == torch.bfloat16:
         return GMM_BF16
     raise ValueError(f"X must be float32, float16 or bfloat16, got {X.dtype}")
+
+
+_DTYPES = {torch.float32: GMM_F32, torch.float16: GMM_F16, torch.bfloat16: GMM_BF16}
 
 
 def _need(t: torch.Tensor, name: str, dtype, shape, device):
@@ -379,6 +398,147 @@ def kmeans_iterate(X, C, iters: int, *, ws=None):
     _check("gmm_kmeans_iterate", lib().gmm_kmeans_iterate(
         _ptr(X), _xtype(X), N, d, K, iters, _ptr(C), _ptr(hist), _ptr(ws), ws.numel(), _stream(dev)))
     return hist[:iters]
+
+
+def _matrix(t, name):
+    if t.dim() != 2 or t.device.type != "cuda" or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous 2-d GPU tensor")
+    return t.shape
+
+
+def _optional(t, name, dtype, shape, device):
+    if t is not None:
+        _need(t, name, dtype, shape, device)
+
+
+def _scratch(ws, nbytes, device, what):
+    if ws is not None:
+        return ws
+    if nbytes == 0:
+        raise ValueError(f"unsupported {what}")
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def linear_workspace(N: int, d_in: int, d_out: int, dtype, device, *, backward: bool = False) -> torch.Tensor:
+    """A device workspace for linear (or linear_backward) with operands of this torch dtype."""
+    nb = int(lib().gmm_linear_workspace_bytes(N, d_in, d_out, _DTYPES[dtype], int(backward)))
+    return _scratch(None, nb, device, f"N={N} d_in={d_in} d_out={d_out}")
+
+
+def linear(X, W, *, bias=None, act: int = ACT_NONE, residual=None, out_dtype=None, want_pre: bool = False, ws=None):
+    """Y = act(X W^T + bias) + residual; returns (Y, pre), pre = X W^T + bias or None.
+
+    X N x d_in, W d_out x d_in and bias d_out share one type; Y, residual and pre are N x d_out of out_dtype
+    (X's type, the default, or float32)."""
+    N, d_in = _matrix(X, "X")
+    dev, xt = X.device, _xtype(X)
+    d_out = W.shape[0]
+    _need(W, "W", X.dtype, (d_out, d_in), dev)
+    _optional(bias, "bias", X.dtype, (d_out,), dev)
+    out_dtype = X.dtype if out_dtype is None else out_dtype
+    if out_dtype not in (X.dtype, torch.float32):
+        raise ValueError(f"out_dtype must be {X.dtype} or float32, got {out_dtype}")
+    _optional(residual, "residual", out_dtype, (N, d_out), dev)
+    with torch.cuda.device(dev):
+        Y = torch.empty(N, d_out, dtype=out_dtype, device=dev)
+        pre = torch.empty(N, d_out, dtype=out_dtype, device=dev) if want_pre else None
+        if ws is None:
+            ws = linear_workspace(N, d_in, d_out, X.dtype, dev)
+        _check("gmm_linear", lib().gmm_linear(
+            _ptr(X), xt, N, d_in, _ptr(W), d_out, _ptr(bias), act, _ptr(residual), _ptr(Y), _DTYPES[out_dtype],
+            _ptr(pre), _ptr(ws), ws.numel(), _stream(dev)))
+    return Y, pre
+
+
+def linear_backward(dY, X, W, *, pre=None, act: int = ACT_NONE, want_dx: bool = True, want_dw: bool = True,
+                    want_db: bool = True, ws=None):
+    """Gradients of linear: (dX, dW, db) in X's type, None for what is not wanted. pre is linear's second result
+    (not needed with ACT_NONE). The residual's gradient is dY."""
+    N, d_in = _matrix(X, "X")
+    dev, xt = X.device, _xtype(X)
+    d_out = W.shape[0]
+    _need(W, "W", X.dtype, (d_out, d_in), dev)
+    if dY.dtype not in (X.dtype, torch.float32):
+        raise ValueError(f"dY must be {X.dtype} or float32, got {dY.dtype}")
+    _need(dY, "dY", dY.dtype, (N, d_out), dev)
+    if pre is None and act != ACT_NONE:
+        raise ValueError("pre is needed with an activation")
+    _optional(pre, "pre", dY.dtype, (N, d_out), dev)
+    with torch.cuda.device(dev):
+        dX = torch.empty_like(X) if want_dx else None
+        dW = torch.empty_like(W) if want_dw else None
+        db = torch.empty(d_out, dtype=X.dtype, device=dev) if want_db else None
+        if ws is None:
+            ws = linear_workspace(N, d_in, d_out, X.dtype, dev, backward=True)
+        _check("gmm_linear_backward", lib().gmm_linear_backward(
+            _ptr(dY), _DTYPES[dY.dtype], _ptr(X), xt, N, d_in, _ptr(W), d_out, _ptr(pre), act, _ptr(dX), _ptr(dW),
+            _ptr(db), _ptr(ws), ws.numel(), _stream(dev)))
+    return dX, dW, db
+
+
+def expert_workspace(N: int, D: int, K: int, F: int, d: int, top: int, dtype, device) -> torch.Tensor:
+    """A device workspace for expert_layer (d >= 1 features) or expert_rows (d = 0)."""
+    nb = int(lib().gmm_expert_workspace_bytes(N, D, K, F, d, top, _DTYPES[dtype]))
+    return _scratch(None, nb, device, f"N={N} D={D} K={K} F={F} d={d} top={top}")
+
+
+def _experts_args(X, W1, W2, b1, b2, glu, residual):
+    N, D = _matrix(X, "X")
+    _xtype(X)
+    dev, t = X.device, X.dtype
+    if W2.dim() != 3:
+        raise ValueError("W2 must be K x D x F")
+    K, F = W2.shape[0], W2.shape[2]
+    up = 2 * F if glu else F
+    _need(W1, "W1", t, (K, up, D), dev)
+    _need(W2, "W2", t, (K, D, F), dev)
+    _optional(b1, "b1", t, (K, up), dev)
+    _optional(b2, "b2", t, (K, D), dev)
+    _optional(residual, "residual", t, (N, D), dev)
+    return N, D, K, F, dev
+
+
+def expert_layer(X, P, mu, var, logw, W1, W2, *, b1=None, b2=None, act: int = ACT_SILU, glu: bool = True,
+                 top: int = 2, border_threshold: float = 0.0, renorm: bool = False, residual=None, ws=None):
+    """Layer of experts gated by the mixture's posterior at P x, for at most 128 rows: returns
+    (Y[N,D], idx[N,top] int32, resp[N,top] float32)."""
+    N, D, K, F, dev = _experts_args(X, W1, W2, b1, b2, glu, residual)
+    d = P.shape[0]
+    _need(P, "P", X.dtype, (d, D), dev)
+    _need(mu, "mu", torch.float32, (K, d), dev)
+    _need(var, "var", torch.float32, (K, d), dev)
+    _need(logw, "logw", torch.float32, (K,), dev)
+    with torch.cuda.device(dev):
+        if ws is None:
+            ws = expert_workspace(N, D, K, F, d, top, X.dtype, dev)
+        Y = torch.empty(N, D, dtype=X.dtype, device=dev)
+        idx = torch.empty(N, top, dtype=torch.int32, device=dev)
+        resp = torch.empty(N, top, dtype=torch.float32, device=dev)
+        _check("gmm_expert_layer", lib().gmm_expert_layer(
+            _ptr(X), _xtype(X), N, D, _ptr(P), d, _ptr(mu), _ptr(var), _ptr(logw), K, top, float(border_threshold),
+            int(renorm), _ptr(W1), _ptr(b1), _ptr(W2), _ptr(b2), F, act, int(glu), _ptr(residual), _ptr(Y), _ptr(idx),
+            _ptr(resp), _ptr(ws), ws.numel(), _stream(dev)))
+    return Y, idx, resp
+
+
+def expert_rows(X, idx, wts, W1, W2, *, b1=None, b2=None, act: int = ACT_SILU, glu: bool = True, residual=None,
+                ws=None):
+    """The experts of expert_layer for given picks (idx N x top int32, wts N x top float32, for instance those of
+    assign_top2): returns Y[N,D]. A pick outside [0, K) is skipped."""
+    N, D, K, F, dev = _experts_args(X, W1, W2, b1, b2, glu, residual)
+    if idx.dim() != 2:
+        raise ValueError("idx must be N x top")
+    top = idx.shape[1]
+    _need(idx, "idx", torch.int32, (N, top), dev)
+    _need(wts, "wts", torch.float32, (N, top), dev)
+    with torch.cuda.device(dev):
+        if ws is None:
+            ws = expert_workspace(N, D, K, F, 0, top, X.dtype, dev)
+        Y = torch.empty(N, D, dtype=X.dtype, device=dev)
+        _check("gmm_expert_rows", lib().gmm_expert_rows(
+            _ptr(X), _xtype(X), N, D, _ptr(idx), _ptr(wts), top, K, _ptr(W1), _ptr(b1), _ptr(W2), _ptr(b2), F, act,
+            int(glu), _ptr(residual), _ptr(Y), _ptr(ws), ws.numel(), _stream(dev)))
+    return Y
 
 
 def peak_mfma(precision: int, trips: int, blocks: int, out: torch.Tensor) -> float:
