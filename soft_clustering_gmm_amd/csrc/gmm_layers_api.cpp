@@ -34,27 +34,43 @@ static int with_type(int t, F&& f) {
 }
 
 // Tile variant and split of the contraction for an M x N x K product: the
-// least of a simple time model.
+// least of a time model, whose us per step were fitted to measurements on an
+// MI355X (2-byte elements: 256-row tiles 1263 TFLOP/s at 8192 x 16384 x 4096
+// against 1075 with 128-row tiles; 128-row tiles 26.6 us at 2048^3 against 29.9
+// with 64-row and 52.9 with 256-row ones; single precision: 64-row tiles 76 us
+// at 4096 x 1024 x 1024 against 80 and 104).
 struct Cut {
   int variant, splits;
   int64_t split_k;
 };
 
 static Cut choose_cut(int64_t M, int64_t N, int64_t K, int e) {
-  // Blocks resident on the chip, and us of one k step of all of them.
-  static const double kSlots[kTileVariants] = {256, 512, 1024};
-  static const double kStepUs[kTileVariants] = {1.0, 0.65, 0.5};
+  struct Rate {
+    int per_cu;         // blocks that a CU holds
+    double one, full;   // us of a step with one block on a CU, and with all
+  };
+  static const Rate kRates[2][kTileVariants] = {{{1, 1.7, 1.7}, {2, 0.7, 1.02}, {4, 0.5, 0.82}},
+                                                {{1, 7.5, 7.5}, {2, 2.4, 3.8}, {4, 0.8, 2.1}}};
+  constexpr int kCus = 256;
+  constexpr double kFixedUs = 3., kReduceUs = 3., kBytesPerUs = 3e6;
   const int64_t step = kStepBytes / e, steps = std::max<int64_t>(ceil_div(K, step), 1);
   Cut best{};
   double best_us = 1e30;
   for (int v = 0; v < kTileVariants; ++v) {
+    const Rate& r = kRates[e == 4][v];
     const int64_t tiles = ceil_div(M, kTileRows[v]) * ceil_div(N, kTileRows[v]);
     for (int64_t want = 1; want <= std::min<int64_t>(steps, 256); want *= 2) {
       const int64_t per = ceil_div(steps, want), parts = ceil_div(steps, per);
-      if (parts > 1 && (double)parts * M * N * 4 > 1e9) break;
-      const double rounds = (double)ceil_div(tiles * parts, (int64_t)kSlots[v]);
-      double us = rounds * (per * kStepUs[v] * (e == 4 ? 8 : 1) + 2.);
-      if (parts > 1) us += 4. + 8e-6 * parts * M * N / 4;
+      const double moved = parts > 1 ? 8. * parts * M * N : 0.;  // partial sums, written and read
+      if (moved > 2e9) break;
+      const int64_t blocks = tiles * parts, rounds = blocks / (kCus * r.per_cu), rest = blocks % (kCus * r.per_cu);
+      double us = rounds * (per * r.full + kFixedUs);
+      if (rest) {
+        const int64_t on_cu = ceil_div(rest, kCus);
+        const double share = r.per_cu > 1 ? double(on_cu - 1) / (r.per_cu - 1) : 0.;
+        us += per * (r.one + share * (r.full - r.one)) + kFixedUs;
+      }
+      if (parts > 1) us += kReduceUs + moved / kBytesPerUs;
       if (us < best_us) {
         best_us = us;
         best = Cut{v, (int)parts, per * step};

@@ -19,8 +19,14 @@ __device__ __forceinline__ lds_ptr to_lds(const void* p) {
 // Tiled product. A block computes a BM x BN tile of C with WM x WN waves; a
 // step of the contraction brings kStepBytes of k of both operands into one
 // half of LDS, by loads that go to LDS directly, while the waves multiply the
-// other half. One barrier per step: it says both that the step's tiles have
-// arrived and that nobody reads the half that is filled next.
+// other half.
+//
+// The loop is pipelined in registers too: a step has two half steps of k, and
+// the fragments of the next half step are read from LDS between the matrix
+// instructions of the present one. The barrier stands between the half steps,
+// where every wave holds its last fragments of the old step in registers: it
+// says that the next step's tiles have arrived and that the old half of LDS
+// may be filled again, and matrix instructions follow it at once.
 //
 // The matrix instruction gets B's rows (n) as its first operand and A's rows
 // (m) as its second, so a lane's results are 4 consecutive n of one m; the
@@ -34,6 +40,25 @@ __device__ __forceinline__ lds_ptr to_lds(const void* p) {
 //   k-contiguous: [row][8 chunks of k], key from the row;
 //   k-strided:    [k][BR / kPer chunks of rows], key from k.
 // ---------------------------------------------------------------------------
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+
+// One kilobyte per wave, 16 bytes a lane, from a buffer straight into LDS at
+// `lds` (the same for the whole wave); offsets past the buffer's end give
+// zeros. Written out because the compiler makes every transposing LDS read
+// wait for such loads in flight, which would undo the double buffering; the
+// kernel's own waits are in step_barrier(). Nothing is returned in registers.
+__device__ __forceinline__ void load_to_lds(uint32_t lds, uint32_t offset, i32x4 buffer) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               :
+               : "s"(lds), "v"(offset), "s"(buffer));
+}
+
+// Every load of this wave has arrived in LDS and its LDS reads are done; then
+// the block's barrier. `lds` ties the tile's memory to it.
+__device__ __forceinline__ void step_barrier(const void* lds) {
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" : : "v"(to_lds(lds)) : "memory");
+}
 
 template <int NI>
 __device__ __forceinline__ int key_rows_perm(int n) {  // rows in the order above
@@ -57,11 +82,22 @@ struct Operand {
   static constexpr int kLoads = kBytes / 1024 / NWAVES;  // wave loads of 1 KB
   static constexpr int kRowChunks = BR * (int)sizeof(T) / 16;  // k-strided: chunks per k
 
-  const char* base;   // element (first row of the tile, first k of the part)
-  int64_t step_bytes;  // from one step to the next
-  int64_t left;        // bytes from base to the operand's end (k-strided: to the end of the part's k range)
+  const char* base;      // element (first row of the tile, first k of the part)
+  int64_t step_bytes;    // from one step to the next
+  int64_t left;          // bytes from base to the operand's end (k-strided: to the end of the part's k range)
   uint32_t off[kLoads];  // byte offset of this lane's chunk from base
-  int kchunk[kLoads];    // k-contiguous: first k of the lane's chunk within the step
+
+  static __device__ __forceinline__ int key(int k) {
+    return PERM ? key_k_perm<NI>(k) : key_k(k);
+  }
+
+  // First k, within the step, of the chunk that this lane brings in load j.
+  static __device__ __forceinline__ int chunk_k(int j, int wave, int lane) {
+    const int ch = (wave * kLoads + j) * 64 + lane;
+    if (STRIDED) return ch / kRowChunks;
+    const int r = ch / 8;
+    return ((ch % 8) ^ (PERM ? key_rows_perm<NI>(r) : key_rows(r))) * kPer;
+  }
 
   __device__ __forceinline__ void init(const void* p, int64_t ld, int64_t r0, int64_t rows, int64_t k0, int64_t k1,
                                        int wave, int lane) {
@@ -79,29 +115,28 @@ struct Operand {
     for (int j = 0; j < kLoads; ++j) {
       const int ch = (wave * kLoads + j) * 64 + lane;  // chunk of the tile in LDS order
       if (STRIDED) {
-        const int k = ch / kRowChunks, c = (ch % kRowChunks) ^ (PERM ? key_k_perm<NI>(k) : key_k(k));
+        const int k = ch / kRowChunks, c = (ch % kRowChunks) ^ key(k);
         off[j] = (uint32_t)(k * ld * e + 16 * c);
-        kchunk[j] = k;
       } else {
-        const int r = ch / 8, c = (ch % 8) ^ (PERM ? key_rows_perm<NI>(r) : key_rows(r));
-        off[j] = (uint32_t)(r * ld * e + 16 * c);
-        kchunk[j] = c * kPer;
+        off[j] = (uint32_t)((ch / 8) * ld * e + chunk_k(j, wave, lane) * e);
       }
     }
   }
 
-  // Loads of the step that starts `k` into the part, of whose k `k_left` remain.
-  __device__ __forceinline__ void load(char* lds, int64_t step, int64_t k_left, int wave) {
-    const char* b = base + step * step_bytes;
+  // Loads of step `step` of the part, of whose k `k_left` remain.
+  __device__ __forceinline__ void load(uint32_t lds, int64_t step, int64_t k_left, int wave, int lane) const {
+    const uintptr_t b = reinterpret_cast<uintptr_t>(base) + step * step_bytes;
     int64_t n = left - step * step_bytes;
     n = n < 0 ? 0 : n > 0x7fffffff ? 0x7fffffff : n;
-    // reads past the end give zeros
-    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(b), 0, (int)n, 0x00027000);
+    i32x4 buffer;
+    buffer[0] = (int)(uint32_t)b;
+    buffer[1] = (int)((uint32_t)(b >> 32) & 0xffff);
+    buffer[2] = (int)n;
+    buffer[3] = 0x00027000;
+    const int left_here = (int)(k_left < kStep ? k_left : kStep);
 #pragma unroll
-    for (int j = 0; j < kLoads; ++j) {
-      const uint32_t o = kchunk[j] < k_left ? off[j] : 0x80000000u;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, to_lds(lds + (wave * kLoads + j) * 1024), 16, (int)o, 0, 0, 0);
-    }
+    for (int j = 0; j < kLoads; ++j)
+      load_to_lds(lds + (wave * kLoads + j) * 1024, chunk_k(j, wave, lane) < left_here ? off[j] : 0x80000000u, buffer);
   }
 
   // Fragment of the 16 rows of tile i (of a wave whose rows start at w0), k
@@ -119,7 +154,7 @@ struct Operand {
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int k = 16 * kk + 4 * g + q;
-        const int c = (row >> 2) ^ (PERM ? key_k_perm<NI>(k) : key_k(k));
+        const int c = (row >> 2) ^ key(k);
         v[q] = *reinterpret_cast<const uint32_t*>(lds + (k * kRowChunks + c) * 16 + 4 * (row & 3));
       }
       return v;
@@ -131,7 +166,7 @@ struct Operand {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int k = 32 * kk + 8 * g + 4 * h + (r >> 2);
-        const int c = (row >> 3) ^ (PERM ? key_k_perm<NI>(k) : key_k(k));
+        const int c = (row >> 3) ^ key(k);
         const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
             (__attribute__((address_space(3))) s16x4*)to_lds(lds + (k * kRowChunks + c) * 16 + 2 * (row & 7)));
         const uint2 y = __builtin_bit_cast(uint2, x);
@@ -158,13 +193,13 @@ __device__ __forceinline__ void load_row(const void* p, int64_t at, int n, bool 
     }
   } else {
     const T* q = static_cast<const T*>(p) + at;
-    constexpr int P = 16 / sizeof(T);
-    if (vec && n >= W) {
+    constexpr int P = W * sizeof(T) < 16 ? 1 : 16 / sizeof(T);
+    if (P > 1 && vec && n >= W) {
 #pragma unroll
       for (int i = 0; i < W; i += P) {
         union {
           u32x4 v;
-          T e[P];
+          T e[16 / sizeof(T)];
         } u;
         u.v = *reinterpret_cast<const u32x4*>(q + i);
 #pragma unroll
@@ -191,13 +226,13 @@ __device__ __forceinline__ void store_row(void* p, int64_t at, int n, bool is_f3
     }
   } else {
     T* q = static_cast<T*>(p) + at;
-    constexpr int P = 16 / sizeof(T);
-    if (vec && n >= W) {
+    constexpr int P = W * sizeof(T) < 16 ? 1 : 16 / sizeof(T);
+    if (P > 1 && vec && n >= W) {
 #pragma unroll
       for (int i = 0; i < W; i += P) {
         union {
           u32x4 v;
-          T e[P];
+          T e[16 / sizeof(T)];
         } u;
 #pragma unroll
         for (int k = 0; k < P; ++k) u.e[k] = (T)v[i + k];
@@ -230,8 +265,46 @@ __device__ __forceinline__ void finish_row(const ProductArgs& p, int64_t m, int 
   store_row<T, W>(p.C, at, left, p.c_f32, p.c_vec, z);
 }
 
+// A block's tile and part of the contraction. Tiles go in groups of 8 tile
+// rows, column by column within a group, so that the blocks an XCD runs
+// together share rows of A and of B in its L2.
+struct Place {
+  int part, n0;
+  int64_t m0, k0, k1;
+};
+__device__ __forceinline__ Place tile_place(const ProductArgs& p, int bm, int bn) {
+  const int tiles = p.tiles_m * p.tiles_n;
+  Place at;
+  at.part = blockIdx.x / tiles;
+  const int t = xcd_place(blockIdx.x - at.part * tiles, tiles);
+  constexpr int G = 8;
+  const int group = t / (G * p.tiles_n), first = group * G;
+  const int height = min(G, p.tiles_m - first), in = t - group * G * p.tiles_n;
+  at.m0 = (int64_t)(first + in % height) * bm;
+  at.n0 = in / height * bn;
+  at.k0 = at.part * p.split_k;
+  at.k1 = min(p.K, at.k0 + p.split_k);
+  return at;
+}
+
+// One row of a lane's results (4 NI consecutive n) to C or the partial sums.
+template <typename T, int ACT, int NI>
+__device__ __forceinline__ void finish_tile(const ProductArgs& p, int part, int64_t m, int n, const f32x4* acc,
+                                            const float* bias) {
+  constexpr int W = 4 * NI;
+  float z[W];
+#pragma unroll
+  for (int j = 0; j < NI; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) z[4 * j + q] = acc[j][q];
+  if (p.splits == 1)
+    finish_row<T, ACT, W>(p, m, n, z, bias);
+  else
+    store_row<T, W>(p.partial, ((int64_t)part * p.M + m) * p.N + n, p.N - n, true, p.N % 4 == 0, z);
+}
+
 template <typename T, int BM, int BN, int WM, int WN, bool AS, bool BS, int ACT>
-__global__ void __launch_bounds__(64 * WM * WN)
+__global__ void __launch_bounds__(64 * WM * WN, 2)
 product_kernel(const ProductArgs p) {
   constexpr int NW = WM * WN, TM = BM / WM, TN = BN / WN, MI = TM / 16, NI = TN / 16, W = 4 * NI;
   using OA = Operand<T, BM, NW, AS, false, 1>;
@@ -239,25 +312,15 @@ product_kernel(const ProductArgs p) {
   constexpr int kHalf = OA::kBytes + OB::kBytes;
   __shared__ __align__(1024) char lds[2 * kHalf];
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN;
-  // Tiles in groups of 8 tile rows, column by column within a group, so that
-  // the blocks an XCD runs together share rows of A and of B in its L2.
-  const int tiles = p.tiles_m * p.tiles_n;
-  const int part = blockIdx.x / tiles;
-  const int t = xcd_place(blockIdx.x - part * tiles, tiles);
-  constexpr int G = 8;
-  const int group = t / (G * p.tiles_n), first = group * G;
-  const int height = min(G, p.tiles_m - first), in = t - group * G * p.tiles_n;
-  const int tm = first + in % height, tn = in / height;
-  const int64_t m0 = (int64_t)tm * BM;
-  const int n0 = tn * BN;
-  const int64_t k0 = part * p.split_k, k1 = min(p.K, k0 + p.split_k);
+  const Place at = tile_place(p, BM, BN);
+  const int64_t k0 = at.k0, k1 = at.k1;
 
   OA a;
   OB b;
-  a.init(p.A, p.lda, m0, p.M, k0, k1, wave, lane);
-  b.init(p.B, p.ldb, n0, p.N, k0, k1, wave, lane);
+  a.init(p.A, p.lda, at.m0, p.M, k0, k1, wave, lane);
+  b.init(p.B, p.ldb, at.n0, p.N, k0, k1, wave, lane);
 
   f32x4 acc[MI][NI];
 #pragma unroll
@@ -265,82 +328,120 @@ product_kernel(const ProductArgs p) {
 #pragma unroll
     for (int j = 0; j < NI; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  const int64_t steps = (k1 - k0 + OA::kStep - 1) / OA::kStep;
-  a.load(lds, 0, k1 - k0, wave);
-  b.load(lds + OA::kBytes, 0, k1 - k0, wave);
-  for (int64_t s = 0; s < steps; ++s) {
-    const char* cur = lds + (s & 1) * kHalf;
-    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): this wave's part of the step has arrived
-    __syncthreads();
-    if (s + 1 < steps) {
-      char* nxt = lds + ((s + 1) & 1) * kHalf;
-      const int64_t k_left = k1 - k0 - (s + 1) * OA::kStep;
-      a.load(nxt, s + 1, k_left, wave);
-      b.load(nxt + OA::kBytes, s + 1, k_left, wave);
+  const int steps = (int)((k1 - k0 + OA::kStep - 1) / OA::kStep);
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)reinterpret_cast<uintptr_t>(to_lds(lds)));
+  auto load = [&](int s) {
+    const uint32_t at = lds0 + (s & 1) * kHalf;
+    const int64_t k_left = k1 - k0 - (int64_t)s * OA::kStep;
+    a.load(at, s, k_left, wave, lane);
+    b.load(at + OA::kBytes, s, k_left, wave, lane);
+  };
+  // Half of A's tiles of a half step, and B's tiles, in two sets of registers.
+  constexpr int HI = MI / 2;
+  u32x4 fa[2][HI], fb[2][NI];
+  auto read_a = [&](int s, int kk, int h) {
+#pragma unroll
+    for (int i = 0; i < HI; ++i)
+      fa[h][i] = OA::frag(lds + (s & 1) * kHalf, wm * TM, h * HI + i, kk, lane);
+  };
+  auto read_b = [&](int s, int kk) {
+#pragma unroll
+    for (int j = 0; j < NI; ++j) fb[kk][j] = OB::frag(lds + (s & 1) * kHalf + OA::kBytes, wn * TN, j, kk, lane);
+  };
+  auto multiply = [&](int kk, int h) {
+    Frag<T>::template mma_tiles<HI, NI>(fb[kk], fa[h], acc + h * HI);
+  };
+  // The reads of one phase, one before every few of its matrix instructions.
+  constexpr int kPerA = !AS ? 1 : sizeof(T) == 4 ? 4 : 2, kPerB = !BS ? 1 : sizeof(T) == 4 ? 4 : 2;
+  constexpr int kMma = HI * NI * (sizeof(T) == 4 ? 4 : 1);
+  auto interleave = [&](auto with_b) {
+    constexpr int reads = HI * kPerA + (decltype(with_b)::value ? NI * kPerB : 0);
+    constexpr int between = kMma / reads > 1 ? kMma / reads : 1;
+#pragma unroll
+    for (int i = 0; i < reads; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, between, 0);
     }
-#pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      u32x4 fb[NI], fa[MI];
-#pragma unroll
-      for (int j = 0; j < NI; ++j) fb[j] = OB::frag(cur + OA::kBytes, wn * TN, j, kk, lane);
-#pragma unroll
-      for (int i = 0; i < MI; ++i) fa[i] = OA::frag(cur, wm * TM, i, kk, lane);
-#pragma unroll
-      for (int i = 0; i < MI; ++i)
-#pragma unroll
-        for (int j = 0; j < NI; ++j) acc[i][j] = Frag<T>::mma(fb[j], fa[i], acc[i][j]);
-    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  load(0);
+  step_barrier(lds);
+  if (steps > 1) load(1);
+  read_a(0, 0, 0);
+  read_b(0, 0);
+  __builtin_amdgcn_sched_barrier(0);
+  for (int s = 0; s < steps; ++s) {
+    read_a(s, 0, 1);
+    multiply(0, 0);
+    interleave(std::false_type{});
+    read_a(s, 1, 0);
+    read_b(s, 1);
+    multiply(0, 1);
+    interleave(std::true_type{});
+    read_a(s, 1, 1);
+    multiply(1, 0);
+    interleave(std::false_type{});
+    step_barrier(lds);
+    if (s + 2 < steps) load(s + 2);
+    __builtin_amdgcn_sched_barrier(0);
+    read_a(s + 1, 0, 0);  // after the last step: what an earlier step left, not used
+    read_b(s + 1, 0);
+    multiply(1, 1);
+    interleave(std::true_type{});
   }
 
-  const int n = n0 + wn * TN + (lane >> 4) * W;
+  const int n = at.n0 + wn * TN + (lane >> 4) * W;
   if (n >= p.N) return;
   float bias[W];
 #pragma unroll
   for (int i = 0; i < W; ++i) bias[i] = 0.f;
-  const bool whole = p.splits == 1;
-  if (whole && p.bias) load_row<T, W>(p.bias, n, p.N - n, false, p.b_vec, bias);
+  if (p.splits == 1 && p.bias) load_row<T, W>(p.bias, n, p.N - n, false, p.b_vec, bias);
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
-    const int64_t m = m0 + wm * TM + 16 * i + (lane & 15);
-    if (m >= p.M) continue;
-    float z[W];
-#pragma unroll
-    for (int j = 0; j < NI; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) z[4 * j + q] = acc[i][j][q];
-    if (whole)
-      finish_row<T, ACT, W>(p, m, n, z, bias);
-    else
-      store_row<T, W>(p.partial, ((int64_t)part * p.M + m) * p.N + n, p.N - n, true, p.N % 4 == 0, z);
+    const int64_t m = at.m0 + wm * TM + 16 * i + (lane & 15);
+    if (m < p.M) finish_tile<T, ACT, NI>(p, at.part, m, n, acc[i], bias);
   }
 }
 
-// C from the partial sums, in the order of the parts. One thread per 4 (or 1)
-// consecutive n.
+// C from the partial sums. A block takes 64 groups of W consecutive n, and its
+// 4 waves a quarter of the parts each: few outputs of many parts would
+// otherwise be few threads with one long chain of loads each.
 template <typename T, int ACT, int W>
 __global__ void __launch_bounds__(256) product_reduce_kernel(const ProductArgs p) {
+  __shared__ float red[4][64][W + 1];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int per_row = (p.N + W - 1) / W;
   const int64_t total = p.M * per_row, part = p.M * p.N;
-  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
-    const int64_t m = i / per_row;
+  const int quarter = (p.splits + 3) / 4, s0 = wave * quarter, s1 = min(p.splits, s0 + quarter);
+  for (int64_t i0 = blockIdx.x * 64ll; i0 < total; i0 += gridDim.x * 64ll) {
+    const int64_t i = i0 + lane, m = i / per_row;
     const int n = (int)(i - m * per_row) * W;
     float z[W], bias[W];
 #pragma unroll
     for (int k = 0; k < W; ++k) z[k] = bias[k] = 0.f;
-    const float* q = p.partial + m * p.N + n;
-    for (int s = 0; s < p.splits; ++s) {
-      float v[W];
-      load_row<T, W>(q + s * part, 0, W, true, W == 4, v);
+    if (i < total) {
+      const float* q = p.partial + m * p.N + n;
+      for (int s = s0; s < s1; ++s) {
+        float v[W];
+        load_row<float, W>(q + s * part, 0, W, true, W == 4, v);
 #pragma unroll
-      for (int k = 0; k < W; ++k) z[k] += v[k];
+        for (int k = 0; k < W; ++k) z[k] += v[k];
+      }
     }
-    if (p.bias) load_row<T, W>(p.bias, n, W, false, false, bias);
-    if (W == 1 || p.c_f32) {
-      finish_row<T, ACT, W>(p, m, n, z, bias);
-    } else {  // 4 values of 2 bytes: 8-byte rows, element accesses
-      ProductArgs e = p;
-      e.c_vec = 0;
-      finish_row<T, ACT, W>(e, m, n, z, bias);
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < W; ++k) red[wave][lane][k] = z[k];
+    __syncthreads();
+    // each wave finishes 16 of the groups
+    const int mine = wave * 16 + lane;
+    const int64_t at = i0 + mine, row = at / per_row;
+    if (lane < 16 && at < total) {
+      const int col = (int)(at - row * per_row) * W;
+#pragma unroll
+      for (int k = 0; k < W; ++k)
+        z[k] = (red[0][mine][k] + red[1][mine][k]) + (red[2][mine][k] + red[3][mine][k]);
+      if (p.bias) load_row<T, W>(p.bias, col, W, false, false, bias);
+      finish_row<T, ACT, W>(p, row, col, z, bias);
     }
   }
 }
@@ -421,46 +522,68 @@ __global__ void __launch_bounds__(256) pad_kernel(const T* src, T* dst, int64_t 
   }
 }
 
-// dZ and the column sums of a chunk of rows. A block owns 64 columns and one
-// chunk; its 4 waves take every fourth row.
-template <typename T, int ACT>
+// dZ and the column sums of a chunk of rows. A thread owns V consecutive
+// columns (V * 16 bits or more in one access where the rows allow it), 256 / CG
+// rows go at a time; the rows' sums meet in LDS at the end.
+template <typename T, int ACT, int V, int CG>
 __global__ void __launch_bounds__(256)
 dz_kernel(const void* dY, const void* pre, int y_f32, int64_t rows, int cols, T* dZ, int64_t ldz, float* db_part,
           int64_t chunk_rows) {
-  __shared__ float red[4][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t c = blockIdx.x * 64ll + lane;
+  constexpr int RG = 256 / CG;
+  __shared__ float red[RG][CG * V];
+  const int cg = threadIdx.x % CG, rg = threadIdx.x / CG;
+  const int64_t c = ((int64_t)blockIdx.x * CG + cg) * V;
   const int64_t r0 = blockIdx.y * chunk_rows, r1 = min(rows, r0 + chunk_rows);
-  float sum = 0.f;
-  for (int64_t r = r0 + wave; r < r1; r += 4) {
-    float v = 0.f;
-    if (c < cols) {
-      const int64_t at = r * cols + c;
-      v = y_f32 ? static_cast<const float*>(dY)[at] : (float)static_cast<const T*>(dY)[at];
-      if (ACT != GMM_ACT_NONE)
-        v *= act_slope<ACT>(y_f32 ? static_cast<const float*>(pre)[at] : (float)static_cast<const T*>(pre)[at]);
+  const int left = (int)min((int64_t)V, cols - c);  // of this thread's columns
+  float sum[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) sum[i] = 0.f;
+  if (c < cols) {
+    for (int64_t r = r0 + rg; r < r1; r += RG) {
+      float v[V], z[V];
+      load_row<T, V>(dY, r * cols + c, left, y_f32, V > 1, v);
+      if (ACT != GMM_ACT_NONE) {
+        load_row<T, V>(pre, r * cols + c, left, y_f32, V > 1, z);
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] *= act_slope<ACT>(z[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) sum[i] += v[i];
+      if (dZ) store_row<T, V>(dZ, r * ldz + c, left, false, V > 1, v);
     }
-    sum += v;
-    if (dZ && c < ldz) dZ[r * ldz + c] = (T)v;
+  } else if (dZ && c < ldz) {  // the rows' padding (V = 1: rows of whole pieces have none)
+    for (int64_t r = r0 + rg; r < r1; r += RG) dZ[r * ldz + c] = (T)0.f;
   }
   if (!db_part) return;
-  red[wave][lane] = sum;
+#pragma unroll
+  for (int i = 0; i < V; ++i) red[rg][cg * V + i] = sum[i];
   __syncthreads();
-  if (wave == 0 && c < cols)
-    db_part[blockIdx.y * (int64_t)cols + c] = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+  for (int i = threadIdx.x; i < CG * V; i += 256) {
+    const int64_t col = (int64_t)blockIdx.x * CG * V + i;
+    float t = 0.f;
+#pragma unroll
+    for (int g = 0; g < RG; ++g) t += red[g][i];
+    if (col < cols) db_part[blockIdx.y * (int64_t)cols + col] = t;
+  }
 }
 
+// Column sums of the chunks' sums: 16 columns a block, 16 chunks at a time.
 template <typename T>
 __global__ void __launch_bounds__(256) db_kernel(const float* part, int64_t chunks, int cols, T* db) {
-  __shared__ float red[4][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int c = blockIdx.x * 64 + lane;
+  __shared__ float red[16][17];
+  const int x = threadIdx.x & 15, y = threadIdx.x >> 4;
+  const int c = blockIdx.x * 16 + x;
   float sum = 0.f;
   if (c < cols)
-    for (int64_t i = wave; i < chunks; i += 4) sum += part[i * cols + c];
-  red[wave][lane] = sum;
+    for (int64_t i = y; i < chunks; i += 16) sum += part[i * cols + c];
+  red[y][x] = sum;
   __syncthreads();
-  if (wave == 0 && c < cols) db[c] = (T)((red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]));
+  if (y == 0 && c < cols) {
+    sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) sum += red[i][x];
+    db[c] = (T)sum;
+  }
 }
 
 // --------------------------------------------------------------------------- launchers
@@ -528,27 +651,43 @@ hipError_t launch_reduce(int act, const ProductArgs& p, hipStream_t s) {
   return with_act(act, [&](auto a) {
     constexpr int ACT = decltype(a)::value;
     if (p.N % 4 == 0)
-      product_reduce_kernel<T, ACT, 4><<<blocks_for(p.M * (p.N / 4)), 256, 0, s>>>(p);
+      product_reduce_kernel<T, ACT, 4><<<blocks_for(p.M * (p.N / 4) * 4), 256, 0, s>>>(p);
     else
-      product_reduce_kernel<T, ACT, 1><<<blocks_for(p.M * p.N), 256, 0, s>>>(p);
+      product_reduce_kernel<T, ACT, 1><<<blocks_for(p.M * p.N * 4), 256, 0, s>>>(p);
     return hipGetLastError();
   });
+}
+
+template <typename T, int ACT, int V>
+static void launch_dz_columns(const void* dY, const void* pre, int y_f32, int64_t rows, int cols, T* dZ, int64_t ldz,
+                              float* db_part, int64_t chunk_rows, hipStream_t s) {
+  const int64_t groups = ((dZ ? ldz : cols) + V - 1) / V;
+  const unsigned y = (unsigned)((rows + chunk_rows - 1) / chunk_rows);
+  if (groups > 16)
+    dz_kernel<T, ACT, V, 64><<<dim3((unsigned)((groups + 63) / 64), y), 256, 0, s>>>(dY, pre, y_f32, rows, cols, dZ,
+                                                                                  ldz, db_part, chunk_rows);
+  else  // narrow rows: more of them at a time
+    dz_kernel<T, ACT, V, 16><<<dim3(1, y), 256, 0, s>>>(dY, pre, y_f32, rows, cols, dZ, ldz, db_part, chunk_rows);
 }
 
 template <typename T>
 hipError_t launch_dz(int act, const void* dY, const void* pre, int y_f32, int64_t rows, int cols, T* dZ, int64_t ldz,
                      float* db_part, int64_t chunk_rows, hipStream_t s) {
+  constexpr int P = 16 / sizeof(T);
+  const bool vec = cols % P == 0 && ((reinterpret_cast<uintptr_t>(dY) | reinterpret_cast<uintptr_t>(pre)) & 15) == 0;
   return with_act(act, [&](auto a) {
-    const int64_t w = dZ ? ldz : cols;
-    const dim3 grid((unsigned)((w + 63) / 64), (unsigned)((rows + chunk_rows - 1) / chunk_rows));
-    dz_kernel<T, decltype(a)::value><<<grid, 256, 0, s>>>(dY, pre, y_f32, rows, cols, dZ, ldz, db_part, chunk_rows);
+    constexpr int ACT = decltype(a)::value;
+    if (vec)
+      launch_dz_columns<T, ACT, P>(dY, pre, y_f32, rows, cols, dZ, ldz, db_part, chunk_rows, s);
+    else
+      launch_dz_columns<T, ACT, 1>(dY, pre, y_f32, rows, cols, dZ, ldz, db_part, chunk_rows, s);
     return hipGetLastError();
   });
 }
 
 template <typename T>
 hipError_t launch_db(const float* db_part, int64_t chunks, int cols, T* db, hipStream_t s) {
-  db_kernel<T><<<(cols + 63) / 64, 256, 0, s>>>(db_part, chunks, cols, db);
+  db_kernel<T><<<(cols + 15) / 16, 256, 0, s>>>(db_part, chunks, cols, db);
   return hipGetLastError();
 }
 

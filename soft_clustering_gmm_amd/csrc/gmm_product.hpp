@@ -25,6 +25,15 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 template <typename T>
 struct Frag;
 
+// acc[i][j] += the product of fb[j] and fa[i], for all tiles.
+template <typename T, int MI, int NI>
+__device__ __forceinline__ void mma_each(const u32x4* fb, const u32x4* fa, f32x4 (*acc)[NI]) {
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NI; ++j) acc[i][j] = Frag<T>::mma(fb[j], fa[i], acc[i][j]);
+}
+
 template <>
 struct Frag<float> {
   static constexpr int kPer = 4;
@@ -33,6 +42,19 @@ struct Frag<float> {
 #pragma unroll
     for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(x[i], y[i], c, 0, 0, 0);
     return c;
+  }
+  // One element at a time over all tiles: the four products of a tile wait for
+  // each other.
+  template <int MI, int NI>
+  static __device__ __forceinline__ void mma_tiles(const u32x4* fb, const u32x4* fa, f32x4 (*acc)[NI]) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < NI; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(__builtin_bit_cast(f32x4, fb[j])[q],
+                                                           __builtin_bit_cast(f32x4, fa[i])[q], acc[i][j], 0, 0, 0);
   }
 };
 
@@ -43,6 +65,10 @@ struct Frag<_Float16> {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0,
                                                   0);
   }
+  template <int MI, int NI>
+  static __device__ __forceinline__ void mma_tiles(const u32x4* fb, const u32x4* fa, f32x4 (*acc)[NI]) {
+    mma_each<_Float16, MI, NI>(fb, fa, acc);
+  }
 };
 
 template <>
@@ -52,26 +78,57 @@ struct Frag<__bf16> {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
                                                    0, 0);
   }
+  template <int MI, int NI>
+  static __device__ __forceinline__ void mma_tiles(const u32x4* fb, const u32x4* fa, f32x4 (*acc)[NI]) {
+    mma_each<__bf16, MI, NI>(fb, fa, acc);
+  }
 };
 
-// Activations in single precision. gelu is the exact one, z Phi(z).
-// exp(-z) of a far negative z is +inf, and the quotients then give 0 as they
-// should. A NaN z stays NaN.
+// Activations in single precision. A NaN z stays NaN.
+//
+// gelu is z Phi(z). The tail of the normal distribution is taken from Abramowitz
+// and Stegun, Handbook of Mathematical Functions, 7.1.26:
+//   erfc(x) = (a1 t + ... + a5 t^5) exp(-x^2),  t = 1 / (1 + p x),  x >= 0,
+// within 1.5e-7, which is 0.75e-7 of Phi: below half a step of single precision
+// next to 1. With x = |z| / sqrt 2 the exponential is also the density's, which
+// the slope needs. It takes a third of erff's instructions.
+struct Normal {
+  float cdf, e;  // Phi(z), exp(-z^2 / 2)
+};
+__device__ __forceinline__ Normal normal_of(float z) {
+  const float x = fabsf(z) * 0.70710678118654752f;
+  const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, x, 1.f));
+  const float e = __builtin_amdgcn_exp2f(-0.72134752044448170f * z * z);
+  float q = fmaf(1.061405429f, t, -1.453152027f);
+  q = fmaf(q, t, 1.421413741f);
+  q = fmaf(q, t, -0.284496736f);
+  q = fmaf(q, t, 0.254829592f);
+  const float tail = 0.5f * q * t * e;
+  return {z < 0.f ? tail : 1.f - tail, e};
+}
+
+// 1 / (1 + exp(-z)): a far negative z gives 1 / inf = 0.
+__device__ __forceinline__ float logistic(float z) {
+  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504088896341f * z));
+}
+
 template <int ACT>
 __device__ __forceinline__ float act_value(float z) {
-  if (ACT == GMM_ACT_RELU) return z < 0.f ? 0.f : z;  // keeps a NaN
-  if (ACT == GMM_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
-  if (ACT == GMM_ACT_SILU) return z / (1.f + __expf(-z));
+  if (ACT == GMM_ACT_RELU) return z < 0.f ? 0.f : z;
+  if (ACT == GMM_ACT_GELU) return z * normal_of(z).cdf;
+  if (ACT == GMM_ACT_SILU) return z * logistic(z);
   return z;
 }
 
 template <int ACT>
 __device__ __forceinline__ float act_slope(float z) {
   if (ACT == GMM_ACT_RELU) return z > 0.f ? 1.f : z == z ? 0.f : z;
-  if (ACT == GMM_ACT_GELU)
-    return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + 0.39894228040143268f * z * __expf(-0.5f * z * z);
+  if (ACT == GMM_ACT_GELU) {
+    const Normal n = normal_of(z);
+    return fmaf(0.39894228040143268f * z, n.e, n.cdf);
+  }
   if (ACT == GMM_ACT_SILU) {
-    const float q = 1.f / (1.f + __expf(-z));
+    const float q = logistic(z);
     return q * (1.f + z * (1.f - q));
   }
   return 1.f;
