@@ -8,6 +8,16 @@ namespace gmm {
 
 constexpr int kMaxLayerRows = 128;  // rows of one call
 constexpr int kMaxTop = 8;          // picks per row
+constexpr int kMaxPicks = kMaxLayerRows * kMaxTop;
+// Up to so many rows the second product gathers a row's experts itself (one
+// matrix instruction's columns are the rows of the call).
+constexpr int kGatherRows = 16;
+constexpr int kScoresInLds = 4096;  // components whose scores the gate keeps on chip
+constexpr int kGateParts = 8;       // parts of the features' contraction
+
+// Entries of ExpertArgs::count: experts with picks, picks in the lists, rows
+// whose gate is done.
+enum { kExperts = 0, kPlaces = 1, kRowsDone = 2, kCounts = 3 };
 
 // A layer's arguments and the pointers into its workspace.
 struct ExpertArgs {
@@ -23,21 +33,25 @@ struct ExpertArgs {
   int32_t* idx;         // [T][top]
   float* resp;          // [T][top]
   const int32_t* in_idx;
-  const float* in_wts;
+  const float* in_wts;  // combination weights
   // experts
   const void *W1, *b1, *W2, *b2;
   // workspace
-  double* feats;        // [T][d]
-  double* scores;       // [T][K]
-  float* wts;           // [T][top] combination weights
+  double* feats;        // [kGateParts][T][d]
+  double* consts;       // [K]
+  double* scores;       // [T][K], K > kScoresInLds
+  float* wts;           // [T][top] combination weights of the gate
   int32_t* bad;         // [T] rows whose gate is not a number
   int32_t* place;       // [T * top] place of a pick in the order by expert, -1: none
   int32_t* row_of;      // [T * top] row of the pick at a place
+  int32_t* ord;         // [T * top] which of the experts with picks the place belongs to
+  float* weight;        // [T * top] combination weight of the pick at a place
+  float* scale;         // [T] largest weight of a row (1 if that is 0)
   int32_t* expert;      // [T * top] experts with picks, increasing
   int32_t* first;       // [T * top + 1] their first places
-  int32_t* count;       // [1] how many experts have picks
+  int32_t* count;       // [kCounts]
   void* h;              // [T * top][F] in the operands' type
-  float* out;           // [T * top][D]
+  float* out;           // [T * top][D], more than kGatherRows rows
 };
 
 template <typename T>

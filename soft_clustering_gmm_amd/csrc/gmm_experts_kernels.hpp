@@ -14,152 +14,83 @@ namespace gmm {
 // throughout, since a pick is decided by the difference of two scores.
 // ---------------------------------------------------------------------------
 
-// f[t][j] = P_j . x_t, one wave per feature and 4 rows.
-template <typename T>
-__global__ void __launch_bounds__(256) gate_features_kernel(const ExpertArgs p) {
-  constexpr int P = Frag<T>::kPer, R = 4;
-  const int lane = threadIdx.x & 63, j = blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int t0 = blockIdx.y * R;
-  if (j >= p.d) return;
-  const T* w = static_cast<const T*>(p.proj) + (int64_t)j * p.D;
-  const T* x[R];
-#pragma unroll
-  for (int r = 0; r < R; ++r) x[r] = static_cast<const T*>(p.X) + (int64_t)min(t0 + r, p.T - 1) * p.D;
-  double sum[R] = {0., 0., 0., 0.};
-  for (int k = lane * P; k < p.D; k += 64 * P) {
-    union U {
-      u32x4 v;
-      T e[P];
-    } a, b;
-    a.v = load_frag<T>(w + k, p.D - k);
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      b.v = load_frag<T>(x[r] + k, p.D - k);
-#pragma unroll
-      for (int i = 0; i < P; ++i) sum[r] = fma((double)(float)a.e[i], (double)(float)b.e[i], sum[r]);
-    }
+typedef double f64x4 __attribute__((ext_vector_type(4)));
+
+typedef double f64x4 __attribute__((ext_vector_type(4)));
+
+// c_k = logw_k - 1/2 (d log 2 pi + sum_j log var_kj), 16 components a block of
+// 256 threads, 16 lanes each. The sum is the logarithm of the product of the
+// mantissas (at least 2^-128) and the sum of the exponents: one logarithm a
+// component.
+__device__ __forceinline__ void gate_constants(const ExpertArgs& p, int block) {
+  const int l16 = threadIdx.x & 15, k = block * 16 + (threadIdx.x >> 4);
+  if (k >= p.K) return;
+  double mant = 1.;
+  int e = 0;
+  for (int j = l16; j < p.d; j += 16) {
+    int ej;
+    mant *= frexp((double)p.var[(int64_t)k * p.d + j], &ej);
+    e += ej;
   }
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-#pragma unroll
-    for (int o = 32; o; o >>= 1) sum[r] += __shfl_xor(sum[r], o);
-    if (lane == 0 && t0 + r < p.T) p.feats[(int64_t)(t0 + r) * p.d + j] = sum[r];
+  for (int o = 8; o; o >>= 1) {
+    mant *= __shfl_xor(mant, o);
+    e += __shfl_xor(e, o);
   }
+  const double log2pi = 1.8378770664093454836, ln2 = 0.69314718055994530942;
+  if (l16 == 0) p.consts[k] = (double)p.logw[k] - 0.5 * (p.d * log2pi + (log(mant) + e * ln2));
 }
 
-struct Best {
-  double s;
-  int k;
-};
-__device__ __forceinline__ bool better(double s, int k, const Best& b) { return s > b.s || (s == b.s && k < b.k); }
-
-// Scores of one row against all components, then its picks. One wave scores a
-// component at a time, two features per lane; sum_j log var_j is taken as the
-// logarithm of the product of the mantissas (at least 2^-128) and the sum of
-// the exponents, one logarithm a component.
-template <int NW>
-__global__ void __launch_bounds__(64 * NW) gate_pick_kernel(const ExpertArgs p) {
-  __shared__ Best wave_best[NW];
-  __shared__ double wave_sum[NW];
-  __shared__ int odd;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, t = blockIdx.x;
-  const int j0 = lane, j1 = lane + 64;
-  const double* f = p.feats + (int64_t)t * p.d;
-  const double f0 = j0 < p.d ? f[j0] : 0., f1 = j1 < p.d ? f[j1] : 0.;
-  double* sc = p.scores + (int64_t)t * p.K;
-  if (threadIdx.x == 0) odd = 0;
-  __syncthreads();
-  for (int k = wave; k < p.K; k += NW) {
-    const float *mu = p.mu + (int64_t)k * p.d, *var = p.var + (int64_t)k * p.d;
-    double q = 0., m = 1.;
-    int e = 0;
-    if (j0 < p.d) {
-      const double v = var[j0], u = f0 - mu[j0];
-      q = u * u / v;
-      m = frexp(v, &e);
-    }
-    if (j1 < p.d) {
-      const double v = var[j1], u = f1 - mu[j1];
-      int e1;
-      q += u * u / v;
-      m *= frexp(v, &e1);
-      e += e1;
-    }
-#pragma unroll
-    for (int o = 32; o; o >>= 1) {
-      q += __shfl_xor(q, o);
-      m *= __shfl_xor(m, o);
-      e += __shfl_xor(e, o);
-    }
-    if (lane == 0) {
-      const double log2pi = 1.8378770664093454836, ln2 = 0.69314718055994530942;
-      const double s = (double)p.logw[k] - 0.5 * (p.d * log2pi + (log(m) + e * ln2) + q);
-      sc[k] = s;
-      if (!(s < INFINITY)) odd = 1;  // NaN or +inf: the posterior is not a number
-    }
+// f[t][j] = P_j . x_t on the double-precision matrix instruction, in
+// kGateParts parts of the contraction that the next kernel adds up: a row or
+// two alone would leave most of the chip idle. A block owns 16 features, 16
+// rows and a part, its 4 waves split that again. Every lane loads 16 bytes of
+// its row, and element i of all lanes meets in instruction i. The blocks after
+// those compute the components' constants.
+template <typename T>
+__global__ void __launch_bounds__(256) gate_features_kernel(const ExpertArgs p) {
+  constexpr int P = Frag<T>::kPer, kStep = 4 * P, U = 4, NW = 4;
+  __shared__ double red[NW][16][17];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
+  const int tiles_j = (p.d + 15) / 16, tiles_t = (p.T + 15) / 16;
+  if (blockIdx.x >= tiles_j * tiles_t * kGateParts) {
+    gate_constants(p, blockIdx.x - tiles_j * tiles_t * kGateParts);
+    return;
   }
-  __threadfence_block();
-  __syncthreads();
-
-  Best last{INFINITY, -1};
-  double lse = 0., kept = 0.;
-  double r_of[kMaxTop];
-  int k_of[kMaxTop];
-  bool bad = odd != 0;
+  const int z = blockIdx.x / (tiles_j * tiles_t), in = blockIdx.x - z * tiles_j * tiles_t;
+  const int j0 = in % tiles_j * 16, t0 = in / tiles_j * 16;
+  if (blockIdx.x == 0 && threadIdx.x == 0) p.count[kRowsDone] = 0;
+  const T* w = static_cast<const T*>(p.proj) + (int64_t)min(j0 + r, p.d - 1) * p.D + g * P;
+  const T* x = static_cast<const T*>(p.X) + (int64_t)min(t0 + r, p.T - 1) * p.D + g * P;
+  const int steps = (p.D + kStep - 1) / kStep, per = (steps + NW * kGateParts - 1) / (NW * kGateParts);
+  const int s0 = (z * NW + wave) * per, s1 = min(steps, s0 + per);
+  f64x4 acc = {0., 0., 0., 0.};
+  for (int s = s0; s < s1; s += U) {
+    union V {
+      u32x4 v;
+      T e[P];
+    } a[U], b[U];
 #pragma unroll
-  for (int pick = 0; pick < kMaxTop; ++pick) {
-    if (pick >= p.top) break;
-    Best b{-INFINITY, INT_MAX};
-    for (int k = threadIdx.x; k < p.K; k += 64 * NW) {
-      const double s = sc[k];
-      // after the last pick in the order (score down, index up)
-      if ((s < last.s || (s == last.s && k > last.k)) && better(s, k, b)) b = Best{s, k};
+    for (int u = 0; u < U; ++u) {
+      const int left = s + u < s1 ? p.D - (s + u) * kStep - g * P : 0;
+      a[u].v = load_frag<T>(w + (s + u) * kStep, left);
+      b[u].v = load_frag<T>(x + (s + u) * kStep, left);
     }
 #pragma unroll
-    for (int o = 32; o; o >>= 1) {
-      const double s = __shfl_xor(b.s, o);
-      const int k = __shfl_xor(b.k, o);
-      if (better(s, k, b)) b = Best{s, k};
-    }
-    if (lane == 0) wave_best[wave] = b;
-    __syncthreads();
-    b = wave_best[0];
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-    for (int w = 1; w < NW; ++w)
-      if (better(wave_best[w].s, wave_best[w].k, b)) b = wave_best[w];
-    if (pick == 0) {  // the normaliser
-      double z = 0.;
-      for (int k = threadIdx.x; k < p.K; k += 64 * NW) z += exp(sc[k] - b.s);
-#pragma unroll
-      for (int o = 32; o; o >>= 1) z += __shfl_xor(z, o);
-      if (lane == 0) wave_sum[wave] = z;
-      __syncthreads();
-      z = 0.;
-#pragma unroll
-      for (int w = 0; w < NW; ++w) z += wave_sum[w];
-      bad = bad || !(b.s > -INFINITY);
-      lse = b.s + log(z);
-    }
-    __syncthreads();
-    // components of weight zero (score -inf) are no picks
-    const bool some = !bad && b.k != INT_MAX && b.s > -INFINITY;
-    const double r = some ? exp(b.s - lse) : 0.;
-    const bool keep = some && (pick == 0 || r >= (double)p.threshold);
-    k_of[pick] = keep ? b.k : -1;
-    r_of[pick] = keep ? r : 0.;
-    kept += r_of[pick];
-    last = b;
+      for (int i = 0; i < P; ++i)
+        acc = __builtin_amdgcn_mfma_f64_16x16x4f64((double)(float)a[u].e[i], (double)(float)b[u].e[i], acc, 0, 0, 0);
   }
-  if (threadIdx.x == 0) {
-    p.bad[t] = bad;
 #pragma unroll
-    for (int pick = 0; pick < kMaxTop; ++pick) {
-      if (pick >= p.top) break;
-      const int at = t * p.top + pick;
-      p.idx[at] = k_of[pick];
-      p.resp[at] = (float)r_of[pick];
-      p.wts[at] = (float)(p.renorm && k_of[pick] >= 0 ? r_of[pick] / kept : r_of[pick]);
-    }
+  for (int q = 0; q < 4; ++q) red[wave][r][4 * q + g] = acc[q];  // row r, feature 4 q + g
+  __syncthreads();
+  const int j = threadIdx.x & 15, t = threadIdx.x >> 4;
+  if (j0 + j < p.d && t0 + t < p.T) {
+    double f = 0.;
+#pragma unroll
+    for (int v = 0; v < NW; ++v) f += red[v][t][j];
+    p.feats[((int64_t)z * p.T + t0 + t) * p.d + j0 + j] = f;
   }
 }
 
@@ -191,11 +122,11 @@ __device__ __forceinline__ void expert_rows_part(const ExpertArgs& p, const T* B
   for (; s + U <= s1 && (s + U) * kStep <= K; s += U) {
     u32x4 fb[U], fa[U][RT];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      fb[u] = load16(B + (s + u) * kStep);
+    for (int u = 0; u < U; ++u) fb[u] = load16(B + (s + u) * kStep);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int t = 0; t < RT; ++t) fa[u][t] = load16(A[t] + (s + u) * kStep);
-    }
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -230,8 +161,12 @@ __device__ __forceinline__ void expert_rows_part(const ExpertArgs& p, const T* B
       if (b1) z += (float)b1[at];
       if (GLU && b1) u += (float)b1[at + p.F];
       z = act_value<ACT>(z);
+      if (GLU) z *= u;
+      // The gathering product adds a row's experts up as it goes, so their
+      // weights come in here, as parts of the row's largest.
+      if (p.T <= kGatherRows) z *= p.weight[place] / p.scale[p.row_of[place]];
       // rounded to the operands' type: what the second product's matrix instruction takes
-      static_cast<T*>(p.h)[place * p.F + n0 + n] = (T)(GLU ? z * u : z);
+      static_cast<T*>(p.h)[place * p.F + n0 + n] = (T)z;
     } else {
       p.out[place * p.D + n0 + n] = z;
     }
@@ -243,8 +178,8 @@ template <typename T, int NW, int RT, bool UP, bool GLU, int ACT>
 __global__ void __launch_bounds__(64 * NW) expert_kernel(const ExpertArgs p) {
   __shared__ float red[NW * RT * 16 * 17];
   const int a = blockIdx.y;
-  if (a >= *p.count) return;
-  const int e = p.expert[a], first = p.first[a], rows = p.first[a + 1] - first;
+  const int count = p.count[kExperts], e = p.expert[a], first = p.first[a], rows = p.first[a + 1] - first;
+  if (a >= count) return;  // all four loaded at once
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
   const int K = UP ? p.D : p.F, N = UP ? (GLU ? 2 * p.F : p.F) : p.D;
   int brow;
@@ -276,41 +211,123 @@ __global__ void __launch_bounds__(256) expert_combine_kernel(const ExpertArgs p)
     if (place < 0) continue;
     float o = p.out[(int64_t)place * p.D + c];
     if (p.b2) o += (float)static_cast<const T*>(p.b2)[(int64_t)p.in_idx[pick] * p.D + c];
-    y += p.in_wts[pick] * o;
+    y += p.weight[place] * o;
   }
   if (p.bad && p.bad[t]) y = NAN;
   static_cast<T*>(p.Y)[at] = (T)y;
 }
 
+// The second product and the sum over a row's experts for at most 16 rows: the
+// columns of the matrix instruction are the rows of the call, and a block runs
+// `cols` columns of Y (at most 16; fewer where that fills the chip) through all
+// experts with picks, one long contraction over (expert, k) that its waves
+// split evenly. Column t of an expert that row t did not pick is zero; the
+// weights are in h already, as parts of the row's largest, which stands before
+// the whole sum.
+template <typename T, int NW>
+__global__ void __launch_bounds__(64 * NW) expert_gather_kernel(const ExpertArgs p, int cols) {
+  constexpr int P = Frag<T>::kPer, kStep = 4 * P, U = 8, kMost = kGatherRows * kMaxTop;
+  static_assert(64 * NW >= kMost, "one thread per pick");
+  __shared__ float red[NW][16][17];
+  __shared__ int16_t at[kMost][16];  // [expert][row]: place of the row's pick, -1: none
+  __shared__ int expert[kMost];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4, i = threadIdx.x;
+  const int n0 = blockIdx.x * cols, count = p.count[kExperts], places = p.count[kPlaces];
+  int e = 0, ord = 0, row_of = 0;
+  if (i < p.T * p.top) {  // all loaded at once, whatever the counts
+    e = p.expert[i];
+    ord = p.ord[i];
+    row_of = p.row_of[i];
+  }
+  for (int q = i; q < kMost * 8; q += 64 * NW) reinterpret_cast<int*>(at)[q] = -1;
+  __syncthreads();
+  if (i < count) expert[i] = e;
+  if (i < places) at[ord][row_of] = (int16_t)i;
+  __syncthreads();
+  const int spe = (p.F + kStep - 1) / kStep, total = count * spe, per = (total + NW - 1) / NW;
+  const int t0 = wave * per, t1 = min(total, t0 + per);
+  const int64_t brow = min(n0 + r % cols, p.D - 1);
+  const T *W2 = static_cast<const T*>(p.W2), *h = static_cast<const T*>(p.h);
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  int a = t0 / spe, s = t0 - a * spe;  // the expert and the step in it
+  for (int t = t0; t < t1; t += U) {
+    u32x4 fb[U], fa[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      fb[u] = fa[u] = u32x4{0, 0, 0, 0};
+      if (t + u < t1) {
+        const int k = s * kStep + g * P, place = at[a][r];
+        fb[u] = load_frag<T>(W2 + ((int64_t)expert[a] * p.D + brow) * p.F + k, p.F - k);
+        if (place >= 0) fa[u] = load_frag<T>(h + (int64_t)place * p.F + k, p.F - k);
+        if (++s == spe) {
+          s = 0;
+          ++a;
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) acc = Frag<T>::mma(fb[u], fa[u], acc);
+  }
+#pragma unroll
+  for (int q = 0; q < 4; ++q) red[wave][r][4 * g + q] = acc[q];
+  __syncthreads();
+  if (i < 256) {
+    const int n = i & 15, c = n0 + n, row = i >> 4;
+    if (row >= p.T || n >= cols || c >= p.D) return;
+    float z = 0.f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) z += red[w][row][n];
+    float y = p.scale[row] * z;
+    if (p.b2)
+      for (int q = row * p.top; q < (row + 1) * p.top; ++q)
+        if (p.place[q] >= 0)
+          y += p.weight[p.place[q]] * (float)static_cast<const T*>(p.b2)[(int64_t)p.in_idx[q] * p.D + c];
+    const int64_t to = (int64_t)row * p.D + c;
+    if (p.residual) y += (float)static_cast<const T*>(p.residual)[to];
+    if (p.bad && p.bad[row]) y = NAN;
+    static_cast<T*>(p.Y)[to] = (T)y;
+  }
+}
+
 // --------------------------------------------------------------------------- launchers
+
+hipError_t launch_gate_picks(const ExpertArgs& p, hipStream_t s);
 
 template <typename T>
 hipError_t launch_gate(const ExpertArgs& p, hipStream_t s) {
-  gate_features_kernel<T><<<dim3((p.d + 3) / 4, (p.T + 3) / 4), 256, 0, s>>>(p);
-  gate_pick_kernel<8><<<p.T, 512, 0, s>>>(p);
-  return hipGetLastError();
+  const int blocks = (p.d + 15) / 16 * ((p.T + 15) / 16) * kGateParts + (p.K + 15) / 16;
+  gate_features_kernel<T><<<blocks, 256, 0, s>>>(p);
+  return launch_gate_picks(p, s);
 }
 
 template <typename T, int RT, bool GLU, int ACT>
-static void launch_expert_products(const ExpertArgs& p, int active, hipStream_t s) {
+static void launch_up(const ExpertArgs& p, int active, hipStream_t s) {
   constexpr int kOut = GLU ? 8 : 16;
-  expert_kernel<T, 4, RT, true, GLU, ACT><<<dim3((p.F + kOut - 1) / kOut, active), 256, 0, s>>>(p);
-  expert_kernel<T, 4, RT, false, false, GMM_ACT_NONE><<<dim3((p.D + 15) / 16, active), 256, 0, s>>>(p);
+  const int tiles = (p.F + kOut - 1) / kOut;
+  if (RT == 1 && (int64_t)tiles * active < 1024)
+    expert_kernel<T, 8, RT, true, GLU, ACT><<<dim3(tiles, active), 512, 0, s>>>(p);
+  else
+    expert_kernel<T, 4, RT, true, GLU, ACT><<<dim3(tiles, active), 256, 0, s>>>(p);
 }
 
 template <typename T, int ACT>
 static void launch_experts_act(const ExpertArgs& p, hipStream_t s) {
-  const int n = p.T * p.top, active = n < p.K ? n : p.K;
-  if (p.T <= 16) {
+  const int n = p.T * p.top, active = n < p.K ? n : p.K, tiles = (p.D + 15) / 16;
+  if (p.T <= kGatherRows) {
     if (p.glu)
-      launch_expert_products<T, 1, true, ACT>(p, active, s);
+      launch_up<T, 1, true, ACT>(p, active, s);
     else
-      launch_expert_products<T, 1, false, ACT>(p, active, s);
+      launch_up<T, 1, false, ACT>(p, active, s);
+    // 16 columns a block, or 8 or 4 where that leaves CUs without one
+    const int cols = p.D >= 16 * 256 ? 16 : p.D >= 8 * 256 ? 8 : 4;
+    expert_gather_kernel<T, 16><<<(p.D + cols - 1) / cols, 1024, 0, s>>>(p, cols);
   } else {
     if (p.glu)
-      launch_expert_products<T, 4, true, ACT>(p, active, s);
+      launch_up<T, 4, true, ACT>(p, active, s);
     else
-      launch_expert_products<T, 4, false, ACT>(p, active, s);
+      launch_up<T, 4, false, ACT>(p, active, s);
+    expert_kernel<T, 4, 4, false, false, GMM_ACT_NONE><<<dim3(tiles, active), 256, 0, s>>>(p);
+    expert_combine_kernel<T><<<dim3((p.D + 255) / 256, p.T), 256, 0, s>>>(p);
   }
 }
 
@@ -324,7 +341,6 @@ hipError_t launch_experts(int act, const ExpertArgs& p, hipStream_t s) {
     launch_experts_act<T, GMM_ACT_SILU>(p, s);
   else
     launch_experts_act<T, GMM_ACT_NONE>(p, s);
-  expert_combine_kernel<T><<<dim3((p.D + 255) / 256, p.T), 256, 0, s>>>(p);
   return hipGetLastError();
 }
 

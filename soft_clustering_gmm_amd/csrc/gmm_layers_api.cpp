@@ -284,7 +284,8 @@ static hipError_t linear_gradients(const void* dY, int y_f32, const T* X, int64_
 
 // Workspace of the layer of experts.
 struct ExpertPlan {
-  size_t o_feats, o_scores, o_wts, o_bad, o_place, o_row, o_expert, o_first, o_count, o_h, o_out, bytes;
+  size_t o_feats, o_consts, o_scores, o_wts, o_bad, o_place, o_row, o_ord, o_weight, o_scale, o_expert, o_first, o_count,
+      o_h, o_out, bytes;
 };
 
 static ExpertPlan expert_plan(int64_t T, int D, int F, int K, int d, int top, int e) {
@@ -296,17 +297,21 @@ static ExpertPlan expert_plan(int64_t T, int D, int F, int K, int d, int top, in
     off = align_up(off + bytes, 256);
     return o;
   };
-  x.o_feats = take((size_t)T * d * sizeof(double));
-  x.o_scores = take(d ? (size_t)T * K * sizeof(double) : 0);
+  x.o_feats = take((size_t)kGateParts * T * d * sizeof(double));
+  x.o_consts = take(d ? (size_t)K * sizeof(double) : 0);
+  x.o_scores = take(d && K > kScoresInLds ? (size_t)T * K * sizeof(double) : 0);
   x.o_wts = take(n * sizeof(float));
   x.o_bad = take(T * sizeof(int32_t));
   x.o_place = take(n * sizeof(int32_t));
   x.o_row = take(n * sizeof(int32_t));
+  x.o_ord = take(n * sizeof(int32_t));
+  x.o_weight = take(n * sizeof(float));
+  x.o_scale = take(T * sizeof(float));
   x.o_expert = take(n * sizeof(int32_t));
   x.o_first = take((n + 1) * sizeof(int32_t));
-  x.o_count = take(sizeof(int32_t));
+  x.o_count = take(kCounts * sizeof(int32_t));
   x.o_h = take(n * F * e);
-  x.o_out = take(n * D * sizeof(float));
+  x.o_out = take(T > kGatherRows ? n * D * sizeof(float) : 0);
   x.bytes = off;
   return x;
 }
@@ -321,11 +326,15 @@ static int check_experts(int32_t x_dtype, int64_t T, int32_t D, int32_t K, int32
 static void place_experts(ExpertArgs& p, const ExpertPlan& x, void* workspace) {
   char* b = static_cast<char*>(workspace);
   p.feats = reinterpret_cast<double*>(b + x.o_feats);
+  p.consts = reinterpret_cast<double*>(b + x.o_consts);
   p.scores = reinterpret_cast<double*>(b + x.o_scores);
   p.wts = reinterpret_cast<float*>(b + x.o_wts);
   p.bad = reinterpret_cast<int32_t*>(b + x.o_bad);
   p.place = reinterpret_cast<int32_t*>(b + x.o_place);
   p.row_of = reinterpret_cast<int32_t*>(b + x.o_row);
+  p.ord = reinterpret_cast<int32_t*>(b + x.o_ord);
+  p.weight = reinterpret_cast<float*>(b + x.o_weight);
+  p.scale = reinterpret_cast<float*>(b + x.o_scale);
   p.expert = reinterpret_cast<int32_t*>(b + x.o_expert);
   p.first = reinterpret_cast<int32_t*>(b + x.o_first);
   p.count = reinterpret_cast<int32_t*>(b + x.o_count);
@@ -422,8 +431,7 @@ int gmm_expert_layer(const void* X, int32_t x_dtype, int64_t N, int32_t D, const
   hipStream_t s = static_cast<hipStream_t>(stream);
   return with_type(x_dtype, [&](auto* t) {
     using T = std::remove_pointer_t<decltype(t)>;
-    hipError_t e = launch_gate<T>(p, s);
-    if (e == hipSuccess) e = launch_expert_lists(p, s);
+    hipError_t e = launch_gate<T>(p, s);  // and the lists
     if (e == hipSuccess) e = launch_experts<T>(act, p, s);
     return hip_status(e);
   });

@@ -115,6 +115,17 @@ def test_ties_go_to_the_lower_component(G):
     assert (resp == torch.tensor(1 / 40).cuda()).all()
 
 
+@pytest.mark.parametrize("T,K,d,top", [(1, 64, 128, 8), (3, 512, 20, 8), (2, 513, 20, 8), (5, 4096, 7, 3), (4, 4100, 3, 8),
+                                       (2, 65536, 2, 2), (128, 65, 128, 2)])
+def test_gate_sizes(G, T, K, d, top):
+    """Few and many components: picks and responsibilities against 64 bits, experts of one value."""
+    s, _ = layer(T, 48, 1, K, d, torch.float32, False, False, False, seed=K)
+    _, idx, resp = G.expert_layer(s["X"], s["P"], s["mu"], s["var"], s["logw"], s["W1"], s["W2"], glu=False, top=top)
+    want_idx, want_resp, _ = oracle.gate(s["X"], s["P"], s["mu"], s["var"], s["logw"], top, 0.0, False)
+    assert torch.equal(idx.cpu().long(), want_idx)
+    oracle.check(resp, want_resp, want_resp * (2.0 ** -24 + 1e-9) + 2.0 ** -149, "resp")
+
+
 def test_empty_batch_and_in_place(G):
     s, opt = layer(0, 64, 40, 6, 12, torch.float16, True, True, True, seed=0)
     y, idx, resp = G.expert_layer(*[s[k] for k in ("X", "P", "mu", "var", "logw", "W1", "W2")], **opt)
