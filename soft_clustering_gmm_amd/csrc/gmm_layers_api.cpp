@@ -204,19 +204,15 @@ static hipError_t linear_forward(const T* X, int64_t N, int d_in, const T* W, in
   p.b_vec = aligned16(bias);
   p.partial = reinterpret_cast<float*>(ws + l.o_part);
   hipError_t e = hipSuccess;
-  if (l.pad) {
-    T* w = reinterpret_cast<T*>(ws + l.o_w);
-    if ((e = launch_pad<T>(W, w, d_out, d_in, l.kp, s)) != hipSuccess) return e;
-    p.B = w;
-  }
+  if (l.pad) p.B = ws + l.o_w;
   for (int64_t r = 0; r < N; r += kLaunchRows) {
     const int64_t rows = std::min(N - r, kLaunchRows);
     p.M = rows;
     p.A = X + r * d_in;
     if (l.pad) {
-      T* x = reinterpret_cast<T*>(ws + l.o_x);
-      if ((e = launch_pad<T>(X + r * d_in, x, rows, d_in, l.kp, s)) != hipSuccess) return e;
-      p.A = x;
+      const PadJob px{X + r * d_in, ws + l.o_x, rows, l.kp, d_in}, pw{W, ws + l.o_w, r == 0 ? d_out : 0, l.kp, d_in};
+      if ((e = launch_pad<T>(px, pw, s)) != hipSuccess) return e;
+      p.A = ws + l.o_x;
     }
     const size_t at = (size_t)r * d_out * ey;
     p.C = static_cast<char*>(Y) + at;
@@ -236,8 +232,14 @@ static hipError_t linear_gradients(const void* dY, int y_f32, const T* X, int64_
   T* z = reinterpret_cast<T*>(ws + b.o_z);
   float* part = reinterpret_cast<float*>(ws + b.o_db);
   hipError_t e = hipSuccess;
+  PadJob px{}, pw{};
+  if (b.pad && dW) px = PadJob{X, ws + b.o_x, N, b.lx, d_in};
+  if (b.pad && dX) pw = PadJob{W, ws + b.o_w, d_out, b.lx, d_in};
   if (b.own_dz || db)
-    e = launch_dz<T>(act, dY, pre, y_f32, N, d_out, b.own_dz ? z : nullptr, b.lz, db ? part : nullptr, b.chunk, s);
+    e = launch_dz<T>(act, dY, pre, y_f32, N, d_out, b.own_dz ? z : nullptr, b.lz, db ? part : nullptr, b.chunk, px, pw,
+                     s);
+  else if (px.rows || pw.rows)
+    e = launch_pad<T>(px, pw, s);
   if (e == hipSuccess && db) e = launch_db<T>(part, b.chunks, d_out, db, s);
   if (e != hipSuccess) return e;
   const T* dZ = b.own_dz ? z : static_cast<const T*>(dY);
@@ -247,12 +249,7 @@ static hipError_t linear_gradients(const void* dY, int y_f32, const T* X, int64_
   p.N = d_in;
   p.ldb = b.lx;
   if (dX) {  // dX = dZ W
-    p.B = W;
-    if (b.pad) {
-      T* w = reinterpret_cast<T*>(ws + b.o_w);
-      if ((e = launch_pad<T>(W, w, d_out, d_in, b.lx, s)) != hipSuccess) return e;
-      p.B = w;
-    }
+    p.B = b.pad ? ws + b.o_w : static_cast<const void*>(W);
     p.lda = b.lz;
     p.K = d_out;
     p.c_vec = !b.pad && aligned16(dX);
@@ -265,12 +262,7 @@ static hipError_t linear_gradients(const void* dY, int y_f32, const T* X, int64_
     }
   }
   if (dW) {  // dW = dZ^T X
-    p.B = X;
-    if (b.pad) {
-      T* x = reinterpret_cast<T*>(ws + b.o_x);
-      if ((e = launch_pad<T>(X, x, N, d_in, b.lx, s)) != hipSuccess) return e;
-      p.B = x;
-    }
+    p.B = b.pad ? ws + b.o_x : static_cast<const void*>(X);
     p.A = dZ;
     p.lda = b.lz;
     p.M = d_out;
@@ -390,8 +382,8 @@ int gmm_linear_backward(const void* dY, int32_t y_dtype, const void* X, int32_t 
     hipStream_t s = static_cast<hipStream_t>(stream);
     if (N == 0) {  // sums over no rows
       hipError_t r = hipSuccess;
-      if (dW) r = launch_pad<T>(nullptr, static_cast<T*>(dW), d_out, 0, d_in, s);
-      if (r == hipSuccess && db) r = launch_pad<T>(nullptr, static_cast<T*>(db), 1, 0, d_out, s);
+      if (dW) r = launch_zero<T>(static_cast<T*>(dW), (int64_t)d_out * d_in, s);
+      if (r == hipSuccess && db) r = launch_zero<T>(static_cast<T*>(db), d_out, s);
       return hip_status(r);
     }
     return hip_status(linear_gradients<T>(dY, y_dtype == GMM_F32, static_cast<const T*>(X), N, d_in,

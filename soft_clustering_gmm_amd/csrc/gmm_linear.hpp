@@ -55,18 +55,27 @@ template <typename T>
 hipError_t launch_product(int variant, bool a_strided, bool b_strided, int act, const ProductArgs& p, hipStream_t s);
 template <typename T>
 hipError_t launch_few(int act, const FewArgs& p, hipStream_t s);
-// Rows of `cols` elements copied to rows of `ld` elements, zeros behind.
+// Rows of `cols` elements copied to rows of `ld` elements, zeros behind (no
+// rows: nothing).
+struct PadJob {
+  const void* src;
+  void* dst;
+  int64_t rows, ld;
+  int cols;
+};
 template <typename T>
-hipError_t launch_pad(const T* src, T* dst, int64_t rows, int cols, int64_t ld, hipStream_t s);
+hipError_t launch_pad(const PadJob& a, const PadJob& b, hipStream_t s);
+template <typename T>
+hipError_t launch_zero(T* p, int64_t n, hipStream_t s);
 // Sum of the parts, then the epilogue of ProductArgs.
 template <typename T>
 hipError_t launch_reduce(int act, const ProductArgs& p, hipStream_t s);
 // dZ = dY act'(pre) in the operands' type, rows of ldz elements (zeros
 // behind), and per-chunk column sums of the unrounded dZ in db_part; dZ or
-// db_part may be null.
+// db_part may be null. The two copies run in the same launch.
 template <typename T>
 hipError_t launch_dz(int act, const void* dY, const void* pre, int y_f32, int64_t rows, int cols, T* dZ, int64_t ldz,
-                     float* db_part, int64_t chunk_rows, hipStream_t s);
+                     float* db_part, int64_t chunk_rows, const PadJob& px, const PadJob& pw, hipStream_t s);
 template <typename T>
 hipError_t launch_db(const float* db_part, int64_t chunks, int cols, T* db, hipStream_t s);
 

@@ -512,28 +512,56 @@ __global__ void __launch_bounds__(64 * NW) few_kernel(const FewArgs p) {
   }
 }
 
+// Rows of any length and start copied to rows of whole 16-byte pieces, zeros
+// behind: pieces i0, i0 + stride, ...
 template <typename T>
-__global__ void __launch_bounds__(256) pad_kernel(const T* src, T* dst, int64_t rows, int cols, int64_t ld) {
-  const int64_t total = rows * ld;
-  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
-    const int64_t r = i / ld;
-    const int c = (int)(i - r * ld);
-    dst[i] = c < cols ? src[r * cols + c] : (T)0.f;
+__device__ __forceinline__ void pad_rows(const PadJob& j, int64_t i0, int64_t stride) {
+  constexpr int P = Frag<T>::kPer;
+  const int pieces = (int)(j.ld / P);
+  const int64_t total = j.rows * pieces;
+  for (int64_t i = i0; i < total; i += stride) {
+    const int64_t r = i / pieces;
+    const int c = (int)(i - r * pieces) * P;
+    *reinterpret_cast<u32x4*>(static_cast<T*>(j.dst) + r * j.ld + c) =
+        load_frag<T>(static_cast<const T*>(j.src) + r * j.cols + c, j.cols - c);
   }
+}
+
+// Two copies in one launch, half of the blocks each.
+template <typename T>
+__global__ void __launch_bounds__(256) pad_kernel(const PadJob a, const PadJob b) {
+  const int half = gridDim.x / 2;
+  if ((int)blockIdx.x < half)
+    pad_rows<T>(a, blockIdx.x * 256ll + threadIdx.x, half * 256ll);
+  else
+    pad_rows<T>(b, (blockIdx.x - half) * 256ll + threadIdx.x, half * 256ll);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) zero_kernel(T* p, int64_t n) {
+  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < n; i += gridDim.x * 256ll) p[i] = (T)0.f;
 }
 
 // dZ and the column sums of a chunk of rows. A thread owns V consecutive
 // columns (V * 16 bits or more in one access where the rows allow it), 256 / CG
-// rows go at a time; the rows' sums meet in LDS at the end.
+// rows go at a time; the rows' sums meet in LDS at the end. The last `pads`
+// blocks copy X and W to padded rows, where the products need that.
 template <typename T, int ACT, int V, int CG>
 __global__ void __launch_bounds__(256)
 dz_kernel(const void* dY, const void* pre, int y_f32, int64_t rows, int cols, T* dZ, int64_t ldz, float* db_part,
-          int64_t chunk_rows) {
+          int64_t chunk_rows, int across, int pads, const PadJob px, const PadJob pw) {
   constexpr int RG = 256 / CG;
   __shared__ float red[RG][CG * V];
+  const int pad = (int)blockIdx.x - ((int)gridDim.x - pads);
+  if (pad >= 0) {
+    pad_rows<T>(px, pad * 256ll + threadIdx.x, pads * 256ll);
+    pad_rows<T>(pw, pad * 256ll + threadIdx.x, pads * 256ll);
+    return;
+  }
+  const int bx = blockIdx.x % across, by = blockIdx.x / across;
   const int cg = threadIdx.x % CG, rg = threadIdx.x / CG;
-  const int64_t c = ((int64_t)blockIdx.x * CG + cg) * V;
-  const int64_t r0 = blockIdx.y * chunk_rows, r1 = min(rows, r0 + chunk_rows);
+  const int64_t c = ((int64_t)bx * CG + cg) * V;
+  const int64_t r0 = by * chunk_rows, r1 = min(rows, r0 + chunk_rows);
   const int left = (int)min((int64_t)V, cols - c);  // of this thread's columns
   float sum[V];
 #pragma unroll
@@ -559,11 +587,11 @@ dz_kernel(const void* dY, const void* pre, int y_f32, int64_t rows, int cols, T*
   for (int i = 0; i < V; ++i) red[rg][cg * V + i] = sum[i];
   __syncthreads();
   for (int i = threadIdx.x; i < CG * V; i += 256) {
-    const int64_t col = (int64_t)blockIdx.x * CG * V + i;
+    const int64_t col = (int64_t)bx * CG * V + i;
     float t = 0.f;
 #pragma unroll
     for (int g = 0; g < RG; ++g) t += red[g][i];
-    if (col < cols) db_part[blockIdx.y * (int64_t)cols + col] = t;
+    if (col < cols) db_part[by * (int64_t)cols + col] = t;
   }
 }
 
@@ -641,8 +669,15 @@ static unsigned blocks_for(int64_t items) {
 }
 
 template <typename T>
-hipError_t launch_pad(const T* src, T* dst, int64_t rows, int cols, int64_t ld, hipStream_t s) {
-  pad_kernel<T><<<blocks_for(rows * ld), 256, 0, s>>>(src, dst, rows, cols, ld);
+hipError_t launch_pad(const PadJob& a, const PadJob& b, hipStream_t s) {
+  const int64_t pieces = (a.rows * a.ld > b.rows * b.ld ? a.rows * a.ld : b.rows * b.ld) / Frag<T>::kPer;
+  pad_kernel<T><<<2 * blocks_for(pieces), 256, 0, s>>>(a, b);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch_zero(T* p, int64_t n, hipStream_t s) {
+  zero_kernel<T><<<blocks_for(n), 256, 0, s>>>(p, n);
   return hipGetLastError();
 }
 
@@ -660,27 +695,31 @@ hipError_t launch_reduce(int act, const ProductArgs& p, hipStream_t s) {
 
 template <typename T, int ACT, int V>
 static void launch_dz_columns(const void* dY, const void* pre, int y_f32, int64_t rows, int cols, T* dZ, int64_t ldz,
-                              float* db_part, int64_t chunk_rows, hipStream_t s) {
-  const int64_t groups = ((dZ ? ldz : cols) + V - 1) / V;
-  const unsigned y = (unsigned)((rows + chunk_rows - 1) / chunk_rows);
+                              float* db_part, int64_t chunk_rows, const PadJob& px, const PadJob& pw, hipStream_t s) {
+  const int64_t groups = ((dZ ? ldz : cols) + V - 1) / V, chunks = (rows + chunk_rows - 1) / chunk_rows;
+  const int64_t pieces = (px.rows * px.ld + pw.rows * pw.ld) / Frag<T>::kPer;
+  const int pads = pieces ? (int)blocks_for(pieces) : 0;
+  const int across = groups > 16 ? (int)((groups + 63) / 64) : 1;
+  const unsigned grid = (unsigned)(across * chunks + pads);
   if (groups > 16)
-    dz_kernel<T, ACT, V, 64><<<dim3((unsigned)((groups + 63) / 64), y), 256, 0, s>>>(dY, pre, y_f32, rows, cols, dZ,
-                                                                                  ldz, db_part, chunk_rows);
+    dz_kernel<T, ACT, V, 64><<<grid, 256, 0, s>>>(dY, pre, y_f32, rows, cols, dZ, ldz, db_part, chunk_rows, across,
+                                                  pads, px, pw);
   else  // narrow rows: more of them at a time
-    dz_kernel<T, ACT, V, 16><<<dim3(1, y), 256, 0, s>>>(dY, pre, y_f32, rows, cols, dZ, ldz, db_part, chunk_rows);
+    dz_kernel<T, ACT, V, 16><<<grid, 256, 0, s>>>(dY, pre, y_f32, rows, cols, dZ, ldz, db_part, chunk_rows, across,
+                                                  pads, px, pw);
 }
 
 template <typename T>
 hipError_t launch_dz(int act, const void* dY, const void* pre, int y_f32, int64_t rows, int cols, T* dZ, int64_t ldz,
-                     float* db_part, int64_t chunk_rows, hipStream_t s) {
+                     float* db_part, int64_t chunk_rows, const PadJob& px, const PadJob& pw, hipStream_t s) {
   constexpr int P = 16 / sizeof(T);
   const bool vec = cols % P == 0 && ((reinterpret_cast<uintptr_t>(dY) | reinterpret_cast<uintptr_t>(pre)) & 15) == 0;
   return with_act(act, [&](auto a) {
     constexpr int ACT = decltype(a)::value;
     if (vec)
-      launch_dz_columns<T, ACT, P>(dY, pre, y_f32, rows, cols, dZ, ldz, db_part, chunk_rows, s);
+      launch_dz_columns<T, ACT, P>(dY, pre, y_f32, rows, cols, dZ, ldz, db_part, chunk_rows, px, pw, s);
     else
-      launch_dz_columns<T, ACT, 1>(dY, pre, y_f32, rows, cols, dZ, ldz, db_part, chunk_rows, s);
+      launch_dz_columns<T, ACT, 1>(dY, pre, y_f32, rows, cols, dZ, ldz, db_part, chunk_rows, px, pw, s);
     return hipGetLastError();
   });
 }
@@ -694,10 +733,11 @@ hipError_t launch_db(const float* db_part, int64_t chunks, int cols, T* db, hipS
 #define GMM_LINEAR_TYPE(T)                                                                                         \
   template hipError_t launch_product<T>(int, bool, bool, int, const ProductArgs&, hipStream_t);                    \
   template hipError_t launch_few<T>(int, const FewArgs&, hipStream_t);                                             \
-  template hipError_t launch_pad<T>(const T*, T*, int64_t, int, int64_t, hipStream_t);                             \
+  template hipError_t launch_pad<T>(const PadJob&, const PadJob&, hipStream_t);                                    \
+  template hipError_t launch_zero<T>(T*, int64_t, hipStream_t);                                                    \
   template hipError_t launch_reduce<T>(int, const ProductArgs&, hipStream_t);                                      \
   template hipError_t launch_dz<T>(int, const void*, const void*, int, int64_t, int, T*, int64_t, float*, int64_t, \
-                                   hipStream_t);                                                                   \
+                                   const PadJob&, const PadJob&, hipStream_t);                                                                   \
   template hipError_t launch_db<T>(const float*, int64_t, int, T*, hipStream_t);
 
 }  // namespace gmm

@@ -9,6 +9,7 @@ this module on a machine without it raises immediately.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -19,6 +20,7 @@ LIB_PATH = os.path.join(_HERE, "libgmm_mi355x.so")
 GMM_F32, GMM_F16, GMM_BF16 = 0, 1, 2
 REGIME_AUTO, REGIME_SINGLE, REGIME_TWOPASS, REGIME_SMALLK = 0, 1, 2, 3
 ACT_NONE, ACT_RELU, ACT_GELU, ACT_SILU = 0, 1, 2, 3
+WORKSPACE_NONE = 256  # what gmm_linear_workspace_bytes reports for a call that needs no workspace
 STATS_FP32, STATS_SPLIT_BF16, STATS_AUTO = 0, 1, 2  # STATS_AUTO is the default
 
 EXPORTS = (
@@ -400,8 +402,17 @@ def kmeans_iterate(X, C, iters: int, *, ws=None):
     return hist[:iters]
 
 
+# A layer's call is often shorter than its launch: sizes are looked up once, and the stream is torch's raw handle.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
 def _matrix(t, name):
-    if t.dim() != 2 or t.device.type != "cuda" or not t.is_contiguous():
+    if t.dim() != 2 or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous 2-d GPU tensor")
     return t.shape
 
@@ -411,9 +422,17 @@ def _optional(t, name, dtype, shape, device):
         _need(t, name, dtype, shape, device)
 
 
-def _scratch(ws, nbytes, device, what):
-    if ws is not None:
-        return ws
+@functools.lru_cache(maxsize=4096)
+def _linear_bytes(N, d_in, d_out, x_dtype, backward):
+    return int(lib().gmm_linear_workspace_bytes(N, d_in, d_out, x_dtype, backward))
+
+
+@functools.lru_cache(maxsize=4096)
+def _expert_bytes(N, D, K, F, d, top, x_dtype):
+    return int(lib().gmm_expert_workspace_bytes(N, D, K, F, d, top, x_dtype))
+
+
+def _scratch(nbytes, device, what):
     if nbytes == 0:
         raise ValueError(f"unsupported {what}")
     return torch.empty(nbytes, dtype=torch.uint8, device=device)
@@ -421,8 +440,8 @@ def _scratch(ws, nbytes, device, what):
 
 def linear_workspace(N: int, d_in: int, d_out: int, dtype, device, *, backward: bool = False) -> torch.Tensor:
     """A device workspace for linear (or linear_backward) with operands of this torch dtype."""
-    nb = int(lib().gmm_linear_workspace_bytes(N, d_in, d_out, _DTYPES[dtype], int(backward)))
-    return _scratch(None, nb, device, f"N={N} d_in={d_in} d_out={d_out}")
+    return _scratch(_linear_bytes(N, d_in, d_out, _DTYPES[dtype], int(backward)), device,
+                    f"N={N} d_in={d_in} d_out={d_out}")
 
 
 def linear(X, W, *, bias=None, act: int = ACT_NONE, residual=None, out_dtype=None, want_pre: bool = False, ws=None):
@@ -431,22 +450,26 @@ def linear(X, W, *, bias=None, act: int = ACT_NONE, residual=None, out_dtype=Non
     X N x d_in, W d_out x d_in and bias d_out share one type; Y, residual and pre are N x d_out of out_dtype
     (X's type, the default, or float32)."""
     N, d_in = _matrix(X, "X")
-    dev, xt = X.device, _xtype(X)
+    dev, t = X.device, X.dtype
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return linear(X, W, bias=bias, act=act, residual=residual, out_dtype=out_dtype, want_pre=want_pre, ws=ws)
+    xt = _xtype(X)
     d_out = W.shape[0]
-    _need(W, "W", X.dtype, (d_out, d_in), dev)
-    _optional(bias, "bias", X.dtype, (d_out,), dev)
-    out_dtype = X.dtype if out_dtype is None else out_dtype
-    if out_dtype not in (X.dtype, torch.float32):
-        raise ValueError(f"out_dtype must be {X.dtype} or float32, got {out_dtype}")
+    _need(W, "W", t, (d_out, d_in), dev)
+    _optional(bias, "bias", t, (d_out,), dev)
+    if out_dtype is None:
+        out_dtype = t
+    elif out_dtype != t and out_dtype != torch.float32:
+        raise ValueError(f"out_dtype must be {t} or float32, got {out_dtype}")
     _optional(residual, "residual", out_dtype, (N, d_out), dev)
-    with torch.cuda.device(dev):
-        Y = torch.empty(N, d_out, dtype=out_dtype, device=dev)
-        pre = torch.empty(N, d_out, dtype=out_dtype, device=dev) if want_pre else None
-        if ws is None:
-            ws = linear_workspace(N, d_in, d_out, X.dtype, dev)
-        _check("gmm_linear", lib().gmm_linear(
-            _ptr(X), xt, N, d_in, _ptr(W), d_out, _ptr(bias), act, _ptr(residual), _ptr(Y), _DTYPES[out_dtype],
-            _ptr(pre), _ptr(ws), ws.numel(), _stream(dev)))
+    Y = torch.empty(N, d_out, dtype=out_dtype, device=dev)
+    pre = torch.empty(N, d_out, dtype=out_dtype, device=dev) if want_pre else None
+    if ws is None and _linear_bytes(N, d_in, d_out, xt, 0) != WORKSPACE_NONE:
+        ws = linear_workspace(N, d_in, d_out, t, dev)
+    _check("gmm_linear", lib().gmm_linear(
+        X.data_ptr(), xt, N, d_in, W.data_ptr(), d_out, _at(bias), act, _at(residual), Y.data_ptr(),
+        _DTYPES[out_dtype], _at(pre), _at(ws), 0 if ws is None else ws.numel(), _raw_stream(dev.index)))
     return Y, pre
 
 
@@ -455,69 +478,76 @@ def linear_backward(dY, X, W, *, pre=None, act: int = ACT_NONE, want_dx: bool = 
     """Gradients of linear: (dX, dW, db) in X's type, None for what is not wanted. pre is linear's second result
     (not needed with ACT_NONE). The residual's gradient is dY."""
     N, d_in = _matrix(X, "X")
-    dev, xt = X.device, _xtype(X)
+    dev, t = X.device, X.dtype
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return linear_backward(dY, X, W, pre=pre, act=act, want_dx=want_dx, want_dw=want_dw, want_db=want_db,
+                                   ws=ws)
+    xt = _xtype(X)
     d_out = W.shape[0]
-    _need(W, "W", X.dtype, (d_out, d_in), dev)
-    if dY.dtype not in (X.dtype, torch.float32):
-        raise ValueError(f"dY must be {X.dtype} or float32, got {dY.dtype}")
-    _need(dY, "dY", dY.dtype, (N, d_out), dev)
+    _need(W, "W", t, (d_out, d_in), dev)
+    yt = dY.dtype
+    if yt != t and yt != torch.float32:
+        raise ValueError(f"dY must be {t} or float32, got {yt}")
+    _need(dY, "dY", yt, (N, d_out), dev)
     if pre is None and act != ACT_NONE:
         raise ValueError("pre is needed with an activation")
-    _optional(pre, "pre", dY.dtype, (N, d_out), dev)
-    with torch.cuda.device(dev):
-        dX = torch.empty_like(X) if want_dx else None
-        dW = torch.empty_like(W) if want_dw else None
-        db = torch.empty(d_out, dtype=X.dtype, device=dev) if want_db else None
-        if ws is None:
-            ws = linear_workspace(N, d_in, d_out, X.dtype, dev, backward=True)
-        _check("gmm_linear_backward", lib().gmm_linear_backward(
-            _ptr(dY), _DTYPES[dY.dtype], _ptr(X), xt, N, d_in, _ptr(W), d_out, _ptr(pre), act, _ptr(dX), _ptr(dW),
-            _ptr(db), _ptr(ws), ws.numel(), _stream(dev)))
+    _optional(pre, "pre", yt, (N, d_out), dev)
+    dX = torch.empty_like(X) if want_dx else None
+    dW = torch.empty_like(W) if want_dw else None
+    db = torch.empty(d_out, dtype=t, device=dev) if want_db else None
+    if ws is None:
+        ws = linear_workspace(N, d_in, d_out, t, dev, backward=True)
+    _check("gmm_linear_backward", lib().gmm_linear_backward(
+        dY.data_ptr(), _DTYPES[yt], X.data_ptr(), xt, N, d_in, W.data_ptr(), d_out, _at(pre), act, _at(dX), _at(dW),
+        _at(db), ws.data_ptr(), ws.numel(), _raw_stream(dev.index)))
     return dX, dW, db
 
 
 def expert_workspace(N: int, D: int, K: int, F: int, d: int, top: int, dtype, device) -> torch.Tensor:
     """A device workspace for expert_layer (d >= 1 features) or expert_rows (d = 0)."""
-    nb = int(lib().gmm_expert_workspace_bytes(N, D, K, F, d, top, _DTYPES[dtype]))
-    return _scratch(None, nb, device, f"N={N} D={D} K={K} F={F} d={d} top={top}")
+    return _scratch(_expert_bytes(N, D, K, F, d, top, _DTYPES[dtype]), device,
+                    f"N={N} D={D} K={K} F={F} d={d} top={top}")
 
 
 def _experts_args(X, W1, W2, b1, b2, glu, residual):
     N, D = _matrix(X, "X")
-    _xtype(X)
     dev, t = X.device, X.dtype
     if W2.dim() != 3:
         raise ValueError("W2 must be K x D x F")
-    K, F = W2.shape[0], W2.shape[2]
+    K, _, F = W2.shape
     up = 2 * F if glu else F
     _need(W1, "W1", t, (K, up, D), dev)
     _need(W2, "W2", t, (K, D, F), dev)
     _optional(b1, "b1", t, (K, up), dev)
     _optional(b2, "b2", t, (K, D), dev)
     _optional(residual, "residual", t, (N, D), dev)
-    return N, D, K, F, dev
+    return N, D, K, F, dev, _xtype(X)
 
 
 def expert_layer(X, P, mu, var, logw, W1, W2, *, b1=None, b2=None, act: int = ACT_SILU, glu: bool = True,
                  top: int = 2, border_threshold: float = 0.0, renorm: bool = False, residual=None, ws=None):
     """Layer of experts gated by the mixture's posterior at P x, for at most 128 rows: returns
     (Y[N,D], idx[N,top] int32, resp[N,top] float32)."""
-    N, D, K, F, dev = _experts_args(X, W1, W2, b1, b2, glu, residual)
+    N, D, K, F, dev, xt = _experts_args(X, W1, W2, b1, b2, glu, residual)
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return expert_layer(X, P, mu, var, logw, W1, W2, b1=b1, b2=b2, act=act, glu=glu, top=top,
+                                border_threshold=border_threshold, renorm=renorm, residual=residual, ws=ws)
     d = P.shape[0]
     _need(P, "P", X.dtype, (d, D), dev)
     _need(mu, "mu", torch.float32, (K, d), dev)
     _need(var, "var", torch.float32, (K, d), dev)
     _need(logw, "logw", torch.float32, (K,), dev)
-    with torch.cuda.device(dev):
-        if ws is None:
-            ws = expert_workspace(N, D, K, F, d, top, X.dtype, dev)
-        Y = torch.empty(N, D, dtype=X.dtype, device=dev)
-        idx = torch.empty(N, top, dtype=torch.int32, device=dev)
-        resp = torch.empty(N, top, dtype=torch.float32, device=dev)
-        _check("gmm_expert_layer", lib().gmm_expert_layer(
-            _ptr(X), _xtype(X), N, D, _ptr(P), d, _ptr(mu), _ptr(var), _ptr(logw), K, top, float(border_threshold),
-            int(renorm), _ptr(W1), _ptr(b1), _ptr(W2), _ptr(b2), F, act, int(glu), _ptr(residual), _ptr(Y), _ptr(idx),
-            _ptr(resp), _ptr(ws), ws.numel(), _stream(dev)))
+    if ws is None:
+        ws = expert_workspace(N, D, K, F, d, top, X.dtype, dev)
+    Y = torch.empty(N, D, dtype=X.dtype, device=dev)
+    idx = torch.empty(N, top, dtype=torch.int32, device=dev)
+    resp = torch.empty(N, top, dtype=torch.float32, device=dev)
+    _check("gmm_expert_layer", lib().gmm_expert_layer(
+        X.data_ptr(), xt, N, D, P.data_ptr(), d, mu.data_ptr(), var.data_ptr(), logw.data_ptr(), K, top,
+        border_threshold, renorm, W1.data_ptr(), _at(b1), W2.data_ptr(), _at(b2), F, act, glu, _at(residual),
+        Y.data_ptr(), idx.data_ptr(), resp.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(dev.index)))
     return Y, idx, resp
 
 
@@ -525,19 +555,21 @@ def expert_rows(X, idx, wts, W1, W2, *, b1=None, b2=None, act: int = ACT_SILU, g
                 ws=None):
     """The experts of expert_layer for given picks (idx N x top int32, wts N x top float32, for instance those of
     assign_top2): returns Y[N,D]. A pick outside [0, K) is skipped."""
-    N, D, K, F, dev = _experts_args(X, W1, W2, b1, b2, glu, residual)
+    N, D, K, F, dev, xt = _experts_args(X, W1, W2, b1, b2, glu, residual)
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return expert_rows(X, idx, wts, W1, W2, b1=b1, b2=b2, act=act, glu=glu, residual=residual, ws=ws)
     if idx.dim() != 2:
         raise ValueError("idx must be N x top")
     top = idx.shape[1]
     _need(idx, "idx", torch.int32, (N, top), dev)
     _need(wts, "wts", torch.float32, (N, top), dev)
-    with torch.cuda.device(dev):
-        if ws is None:
-            ws = expert_workspace(N, D, K, F, 0, top, X.dtype, dev)
-        Y = torch.empty(N, D, dtype=X.dtype, device=dev)
-        _check("gmm_expert_rows", lib().gmm_expert_rows(
-            _ptr(X), _xtype(X), N, D, _ptr(idx), _ptr(wts), top, K, _ptr(W1), _ptr(b1), _ptr(W2), _ptr(b2), F, act,
-            int(glu), _ptr(residual), _ptr(Y), _ptr(ws), ws.numel(), _stream(dev)))
+    if ws is None:
+        ws = expert_workspace(N, D, K, F, 0, top, X.dtype, dev)
+    Y = torch.empty(N, D, dtype=X.dtype, device=dev)
+    _check("gmm_expert_rows", lib().gmm_expert_rows(
+        X.data_ptr(), xt, N, D, idx.data_ptr(), wts.data_ptr(), top, K, W1.data_ptr(), _at(b1), W2.data_ptr(),
+        _at(b2), F, act, glu, _at(residual), Y.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(dev.index)))
     return Y
 
 
