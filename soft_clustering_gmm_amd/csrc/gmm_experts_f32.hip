@@ -7,6 +7,13 @@
 namespace gmm {
 GMM_EXPERTS_TYPE(float)
 
+// Orders this wave's LDS accesses (all lanes) before its later ones.
+__device__ __forceinline__ void wave_lds_order() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 struct Best {
   double s;
   int k;
@@ -14,67 +21,79 @@ struct Best {
 __device__ __forceinline__ bool better(double s, int k, const Best& b) { return s > b.s || (s == b.s && k < b.k); }
 
 struct ListScratch {
-  int key[kMaxPicks];
+  int key[kMaxPicks];   // expert * kMaxPicks + number of a listed pick, INT_MAX: none
   int idx[kMaxPicks];
   float wts[kMaxPicks];
-  int head[kMaxPicks];  // by place: the expert of the pick, INT_MAX behind the last
+  int head[kMaxPicks + 1];  // by place: the expert of the pick, INT_MAX behind the last
   int waves[16];
 };
 
 // The picks in the order of their experts (a pick's place: how many picks have
 // a lower expert, or the same and a lower number), and each expert's places.
 // A row's further picks of an expert that it has picked already add their
-// weight to the first. 1024 threads, each with its pick's expert and weight (-1
-// behind the last pick).
+// weight to the first. A thread a pick, with its expert and weight (-1 behind
+// the last); ONE: at most 64 picks, and only the first wave calls.
+template <bool ONE>
 __device__ __forceinline__ void expert_lists(const ExpertArgs& p, ListScratch& l, int idx, float wt) {
+  static_assert(65536ll * kMaxPicks < INT_MAX, "keys fit");
   const int n = p.T * p.top, i = threadIdx.x, row = i / p.top;
+  auto sync = [] {
+    if (ONE)
+      wave_lds_order();
+    else
+      __syncthreads();
+  };
   l.idx[i] = idx;
   l.wts[i] = wt;
-  __syncthreads();
+  l.head[i] = INT_MAX;
+  if (i == 0) l.head[ONE ? 64 : kMaxPicks] = INT_MAX;
+  sync();
   int mine = INT_MAX;
   float w = 0.f, most = 0.f;
-  const int k = idx;
-  if (k >= 0 && k < p.K) {
-    mine = k;
+  if (idx >= 0 && idx < p.K) {
+    mine = idx * kMaxPicks + i;
     for (int q = row * p.top; q < (row + 1) * p.top; ++q)
-      if (l.idx[q] == k) {
+      if (l.idx[q] == idx) {
         if (q < i) mine = INT_MAX;
         if (q >= i) w += l.wts[q];
       }
   }
   l.key[i] = mine;
-  l.head[i] = INT_MAX;
-  __syncthreads();
-  int place = 0;
-  for (int q = 0; q < n; q += 4) {  // key[] is INT_MAX behind n
-    const int4 v = *reinterpret_cast<const int4*>(l.key + q);
-    place += (v.x < mine || (v.x == mine && q < i)) + (v.y < mine || (v.y == mine && q + 1 < i)) +
-             (v.z < mine || (v.z == mine && q + 2 < i)) + (v.w < mine || (v.w == mine && q + 3 < i));
-  }
+  sync();
   const bool some = mine != INT_MAX;
-  if (i < n) p.place[i] = some ? place : -1;
-  if (some) {
-    l.head[place] = mine;
-    p.row_of[place] = row;
-    p.weight[place] = w;
+  if (i < n) {
+    int place = 0;
+    for (int q = 0; q < n; q += 4) {  // key[] is INT_MAX behind n
+      const int4 v = *reinterpret_cast<const int4*>(l.key + q);
+      place += (v.x < mine) + (v.y < mine) + (v.z < mine) + (v.w < mine);
+    }
+    p.place[i] = some ? place : -1;
+    if (some) {
+      l.head[place] = idx;
+      p.row_of[place] = row;
+      p.weight[place] = w;
+    }
   }
   if (i < p.T) {
     for (int q = i * p.top; q < (i + 1) * p.top; ++q)
       if (l.key[q] != INT_MAX) most = fmaxf(most, fabsf(l.wts[q]));
     p.scale[i] = most > 0.f ? most : 1.f;
   }
-  __syncthreads();
+  sync();
   // the first place of every expert, numbered by a scan over the places
   const int e = l.head[i];
   const bool start = e != INT_MAX && (i == 0 || l.head[i - 1] != e);
   const uint64_t starts = __ballot(start);
   const int lane = i & 63, wave = i >> 6;
-  if (lane == 0) l.waves[wave] = __popcll(starts);
-  __syncthreads();
-  int before = 0, total = 0;
-  for (int v = 0; v < 16; ++v) {
-    if (v < wave) before += l.waves[v];
-    total += l.waves[v];
+  int before = 0, total = __popcll(starts);
+  if (!ONE) {
+    if (lane == 0) l.waves[wave] = total;
+    __syncthreads();
+    total = 0;
+    for (int v = 0; v < 16; ++v) {
+      if (v < wave) before += l.waves[v];
+      total += l.waves[v];
+    }
   }
   const int a = before + __popcll(starts & (~0ull >> (63 - lane))) - 1;
   if (e != INT_MAX) p.ord[i] = a;
@@ -83,7 +102,7 @@ __device__ __forceinline__ void expert_lists(const ExpertArgs& p, ListScratch& l
     p.first[a] = i;
   }
   // the picks end where the INT_MAX begin
-  if (e != INT_MAX && (i == kMaxPicks - 1 || l.head[i + 1] == INT_MAX)) {
+  if (e != INT_MAX && l.head[i + 1] == INT_MAX) {
     p.first[total] = i + 1;
     p.count[kPlaces] = i + 1;
   }
@@ -95,9 +114,14 @@ __device__ __forceinline__ void expert_lists(const ExpertArgs& p, ListScratch& l
 
 __global__ void __launch_bounds__(1024) expert_lists_kernel(const ExpertArgs p) {
   __shared__ __align__(16) ListScratch l;
-  const int i = threadIdx.x;
-  const bool some = i < p.T * p.top;
-  expert_lists(p, l, some ? p.in_idx[i] : -1, some ? p.in_wts[i] : 0.f);
+  const int i = threadIdx.x, n = p.T * p.top;
+  if (n <= 64 && i >= 64) return;
+  const int idx = i < n ? p.in_idx[i] : -1;
+  const float wt = i < n ? p.in_wts[i] : 0.f;
+  if (n <= 64)
+    expert_lists<true>(p, l, idx, wt);
+  else
+    expert_lists<false>(p, l, idx, wt);
 }
 
 // 1 / v: the hardware's estimate and two Newton steps (the estimate has 2^-14
@@ -120,9 +144,9 @@ __device__ __forceinline__ double reciprocal(double v) {
 // which pick it is. More components are picked one after the other, each pick
 // the best of those after the last.
 //
-// One block a row is latency from end to end: 12 us a row of 64 components
-// with the component's constant computed here, the maxima found by shuffles and
-// the lists behind an acquire of the whole L2.
+// One block a row is latency from end to end: for one row of 64 components
+// (64 features, 2 picks) 13 us with the constants computed here, the maxima
+// found by shuffles and the lists behind an acquire of the whole L2, 7 us so.
 __global__ void __launch_bounds__(1024) gate_pick_kernel(const ExpertArgs p) {
   constexpr int NW = 16, kPerLane = 8, kRanked = 512;
   __shared__ __align__(16) union {
@@ -288,16 +312,17 @@ __global__ void __launch_bounds__(1024) gate_pick_kernel(const ExpertArgs p) {
       if (lane == 0) last_block = atomicAdd(p.count + kRowsDone, 1) == p.T - 1;
     }
   }
-  if (p.T > 1) {
-    __syncthreads();
-    if (!last_block) return;
-    // past the caches, as other blocks wrote them
-    const bool some = tid < p.T * p.top;
-    idx = some ? __hip_atomic_load(p.in_idx + tid, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : -1;
-    wt = some ? __hip_atomic_load(p.in_wts + tid, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0.f;
-  }
+  const int n = p.T * p.top;
   __syncthreads();  // the scores' memory is free
-  expert_lists(p, sh.lists, idx, wt);
+  if ((p.T > 1 && !last_block) || (n <= 64 && wave > 0)) return;
+  if (p.T > 1) {  // past the caches, as other blocks wrote them
+    idx = tid < n ? __hip_atomic_load(p.in_idx + tid, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : -1;
+    wt = tid < n ? __hip_atomic_load(p.in_wts + tid, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0.f;
+  }
+  if (n <= 64)
+    expert_lists<true>(p, sh.lists, idx, wt);
+  else
+    expert_lists<false>(p, sh.lists, idx, wt);
 }
 
 hipError_t launch_gate_picks(const ExpertArgs& p, hipStream_t s) {

@@ -164,7 +164,7 @@ __device__ __forceinline__ void expert_rows_part(const ExpertArgs& p, const T* B
       if (GLU) z *= u;
       // The gathering product adds a row's experts up as it goes, so their
       // weights come in here, as parts of the row's largest.
-      if (p.T <= kGatherRows) z *= p.weight[place] / p.scale[p.row_of[place]];
+      if (p.T * p.top <= kGatherPicks) z *= p.weight[place] / p.scale[p.row_of[place]];
       // rounded to the operands' type: what the second product's matrix instruction takes
       static_cast<T*>(p.h)[place * p.F + n0 + n] = (T)z;
     } else {
@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(256) expert_combine_kernel(const ExpertArgs p)
   static_cast<T*>(p.Y)[at] = (T)y;
 }
 
-// The second product and the sum over a row's experts for at most 16 rows: the
+// The second product and the sum over a row's experts for a few picks: the
 // columns of the matrix instruction are the rows of the call, and a block runs
 // `cols` columns of Y (at most 16; fewer where that fills the chip) through all
 // experts with picks, one long contraction over (expert, k) that its waves
@@ -226,8 +226,7 @@ __global__ void __launch_bounds__(256) expert_combine_kernel(const ExpertArgs p)
 // the whole sum.
 template <typename T, int NW>
 __global__ void __launch_bounds__(64 * NW) expert_gather_kernel(const ExpertArgs p, int cols) {
-  constexpr int P = Frag<T>::kPer, kStep = 4 * P, U = 8, kMost = kGatherRows * kMaxTop;
-  static_assert(64 * NW >= kMost, "one thread per pick");
+  constexpr int P = Frag<T>::kPer, kStep = 4 * P, U = 8, kMost = kGatherPicks;
   __shared__ float red[NW][16][17];
   __shared__ int16_t at[kMost][16];  // [expert][row]: place of the row's pick, -1: none
   __shared__ int expert[kMost];
@@ -239,7 +238,7 @@ __global__ void __launch_bounds__(64 * NW) expert_gather_kernel(const ExpertArgs
     ord = p.ord[i];
     row_of = p.row_of[i];
   }
-  for (int q = i; q < kMost * 8; q += 64 * NW) reinterpret_cast<int*>(at)[q] = -1;
+  if (i < kMost * 16) (&at[0][0])[i] = -1;
   __syncthreads();
   if (i < count) expert[i] = e;
   if (i < places) at[ord][row_of] = (int16_t)i;
@@ -313,22 +312,28 @@ static void launch_up(const ExpertArgs& p, int active, hipStream_t s) {
 template <typename T, int ACT>
 static void launch_experts_act(const ExpertArgs& p, hipStream_t s) {
   const int n = p.T * p.top, active = n < p.K ? n : p.K, tiles = (p.D + 15) / 16;
-  if (p.T <= kGatherRows) {
+  if (p.T <= 16) {
     if (p.glu)
       launch_up<T, 1, true, ACT>(p, active, s);
     else
       launch_up<T, 1, false, ACT>(p, active, s);
-    // 16 columns a block, or 8 or 4 where that leaves CUs without one
-    const int cols = p.D >= 16 * 256 ? 16 : p.D >= 8 * 256 ? 8 : 4;
-    expert_gather_kernel<T, 16><<<(p.D + cols - 1) / cols, 1024, 0, s>>>(p, cols);
   } else {
     if (p.glu)
       launch_up<T, 4, true, ACT>(p, active, s);
     else
       launch_up<T, 4, false, ACT>(p, active, s);
-    expert_kernel<T, 4, 4, false, false, GMM_ACT_NONE><<<dim3(tiles, active), 256, 0, s>>>(p);
-    expert_combine_kernel<T><<<dim3((p.D + 255) / 256, p.T), 256, 0, s>>>(p);
   }
+  if (n <= kGatherPicks) {
+    // 16 columns a block, or 8 or 4 where that leaves CUs without one
+    const int cols = p.D >= 16 * 256 ? 16 : p.D >= 8 * 256 ? 8 : 4;
+    expert_gather_kernel<T, 16><<<(p.D + cols - 1) / cols, 1024, 0, s>>>(p, cols);
+    return;
+  }
+  if (p.T <= 16)
+    expert_kernel<T, 4, 1, false, false, GMM_ACT_NONE><<<dim3(tiles, active), 256, 0, s>>>(p);
+  else
+    expert_kernel<T, 4, 4, false, false, GMM_ACT_NONE><<<dim3(tiles, active), 256, 0, s>>>(p);
+  expert_combine_kernel<T><<<dim3((p.D + 255) / 256, p.T), 256, 0, s>>>(p);
 }
 
 template <typename T>

@@ -14,7 +14,8 @@ namespace gmm {
 
 constexpr int kMaxWidth = 65536;             // d_in, d_out, width, hidden
 constexpr int64_t kLaunchRows = 1 << 20;     // rows of one launch (the grid's size)
-constexpr int64_t kDzRows = 64;              // rows per column-sum chunk, at least
+constexpr int64_t kDzRows = 16;              // rows per column-sum chunk, at least
+constexpr int64_t kDzBlocks = 2048;          // blocks of the column sums, where the rows allow it
 
 static size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -37,8 +38,8 @@ static int with_type(int t, F&& f) {
 // least of a time model, whose us per step were fitted to measurements on an
 // MI355X (2-byte elements: 256-row tiles 1263 TFLOP/s at 8192 x 16384 x 4096
 // against 1075 with 128-row tiles; 128-row tiles 26.6 us at 2048^3 against 29.9
-// with 64-row and 52.9 with 256-row ones; single precision: 64-row tiles 76 us
-// at 4096 x 1024 x 1024 against 80 and 104).
+// with 64-row and 52.9 with 256-row ones; single precision: 128-row tiles 80 us
+// at 4096 x 1024 x 1024 against 86 and 104).
 struct Cut {
   int variant, splits;
   int64_t split_k;
@@ -50,7 +51,7 @@ static Cut choose_cut(int64_t M, int64_t N, int64_t K, int e) {
     double one, full;   // us of a step with one block on a CU, and with all
   };
   static const Rate kRates[2][kTileVariants] = {{{1, 1.7, 1.7}, {2, 0.7, 1.02}, {4, 0.5, 0.82}},
-                                                {{1, 7.5, 7.5}, {2, 2.4, 3.8}, {4, 0.8, 2.1}}};
+                                                {{1, 7.5, 7.5}, {2, 2.4, 3.8}, {4, 0.8, 2.6}}};
   constexpr int kCus = 256;
   constexpr double kFixedUs = 3., kReduceUs = 3., kBytesPerUs = 3e6;
   const int64_t step = kStepBytes / e, steps = std::max<int64_t>(ceil_div(K, step), 1);
@@ -147,7 +148,8 @@ static BackwardPlan backward_plan(int64_t N, int d_in, int d_out, int e, bool pl
   b.lz = row_len(d_out, e);
   b.pad = b.lx != d_in;
   b.own_dz = !(plain_dz && b.lz == d_out) && (want_dx || want_dw);
-  b.chunk = std::max<int64_t>(kDzRows, ceil_div(N, 32768));
+  const int64_t across = ceil_div(d_out, 64 * (16 / e));
+  b.chunk = std::max(kDzRows, ceil_div(ceil_div(N * across, kDzBlocks), kDzRows) * kDzRows);
   b.chunks = ceil_div(N, b.chunk);
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -303,7 +305,7 @@ static ExpertPlan expert_plan(int64_t T, int D, int F, int K, int d, int top, in
   x.o_first = take((n + 1) * sizeof(int32_t));
   x.o_count = take(kCounts * sizeof(int32_t));
   x.o_h = take(n * F * e);
-  x.o_out = take(T > kGatherRows ? n * D * sizeof(float) : 0);
+  x.o_out = take(n > kGatherPicks ? n * D * sizeof(float) : 0);
   x.bytes = off;
   return x;
 }

@@ -351,7 +351,7 @@ product_kernel(const ProductArgs p) {
   auto multiply = [&](int kk, int h) {
     Frag<T>::template mma_tiles<HI, NI>(fb[kk], fa[h], acc + h * HI);
   };
-  // The reads of one phase, one before every few of its matrix instructions.
+  // The reads of one phase, one after every few of its matrix instructions.
   constexpr int kPerA = !AS ? 1 : sizeof(T) == 4 ? 4 : 2, kPerB = !BS ? 1 : sizeof(T) == 4 ? 4 : 2;
   constexpr int kMma = HI * NI * (sizeof(T) == 4 ? 4 : 1);
   auto interleave = [&](auto with_b) {
@@ -359,14 +359,14 @@ product_kernel(const ProductArgs p) {
     constexpr int between = kMma / reads > 1 ? kMma / reads : 1;
 #pragma unroll
     for (int i = 0; i < reads; ++i) {
-      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
       __builtin_amdgcn_sched_group_barrier(0x008, between, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
     }
     __builtin_amdgcn_sched_barrier(0);
   };
   load(0);
   step_barrier(lds);
-  if (steps > 1) load(1);
+  load(1);
   read_a(0, 0, 0);
   read_b(0, 0);
   __builtin_amdgcn_sched_barrier(0);
@@ -382,13 +382,14 @@ product_kernel(const ProductArgs p) {
     multiply(1, 0);
     interleave(std::false_type{});
     step_barrier(lds);
-    if (s + 2 < steps) load(s + 2);
+    load(s + 2);  // past the end: zeros, no traffic
     __builtin_amdgcn_sched_barrier(0);
     read_a(s + 1, 0, 0);  // after the last step: what an earlier step left, not used
     read_b(s + 1, 0);
     multiply(1, 1);
     interleave(std::true_type{});
   }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // nothing arrives in LDS after the block's end
 
   const int n = at.n0 + wn * TN + (lane >> 4) * W;
   if (n >= p.N) return;
@@ -548,8 +549,8 @@ __global__ void __launch_bounds__(256) zero_kernel(T* p, int64_t n) {
 // blocks copy X and W to padded rows, where the products need that.
 template <typename T, int ACT, int V, int CG>
 __global__ void __launch_bounds__(256)
-dz_kernel(const void* dY, const void* pre, int y_f32, int64_t rows, int cols, T* dZ, int64_t ldz, float* db_part,
-          int64_t chunk_rows, int across, int pads, const PadJob px, const PadJob pw) {
+dz_kernel(const void* __restrict__ dY, const void* __restrict__ pre, int y_f32, int64_t rows, int cols,
+          T* __restrict__ dZ, int64_t ldz, float* __restrict__ db_part, int64_t chunk_rows, int across, int pads, const PadJob px, const PadJob pw) {
   constexpr int RG = 256 / CG;
   __shared__ float red[RG][CG * V];
   const int pad = (int)blockIdx.x - ((int)gridDim.x - pads);
@@ -567,17 +568,25 @@ dz_kernel(const void* dY, const void* pre, int y_f32, int64_t rows, int cols, T*
 #pragma unroll
   for (int i = 0; i < V; ++i) sum[i] = 0.f;
   if (c < cols) {
-    for (int64_t r = r0 + rg; r < r1; r += RG) {
-      float v[V], z[V];
-      load_row<T, V>(dY, r * cols + c, left, y_f32, V > 1, v);
-      if (ACT != GMM_ACT_NONE) {
-        load_row<T, V>(pre, r * cols + c, left, y_f32, V > 1, z);
+    constexpr int U = 4;  // rows in flight
+    for (int64_t r = r0 + rg; r < r1; r += U * RG) {
+      float v[U][V], z[U][V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] *= act_slope<ACT>(z[i]);
-      }
+      for (int u = 0; u < U; ++u)
+        if (r + u * RG < r1) {
+          load_row<T, V>(dY, (r + u * RG) * cols + c, left, y_f32, V > 1, v[u]);
+          if (ACT != GMM_ACT_NONE) load_row<T, V>(pre, (r + u * RG) * cols + c, left, y_f32, V > 1, z[u]);
+        }
 #pragma unroll
-      for (int i = 0; i < V; ++i) sum[i] += v[i];
-      if (dZ) store_row<T, V>(dZ, r * ldz + c, left, false, V > 1, v);
+      for (int u = 0; u < U; ++u)
+        if (r + u * RG < r1) {
+          if (ACT != GMM_ACT_NONE)
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[u][i] *= act_slope<ACT>(z[u][i]);
+#pragma unroll
+          for (int i = 0; i < V; ++i) sum[i] += v[u][i];
+          if (dZ) store_row<T, V>(dZ, (r + u * RG) * ldz + c, left, false, V > 1, v[u]);
+        }
     }
   } else if (dZ && c < ldz) {  // the rows' padding (V = 1: rows of whole pieces have none)
     for (int64_t r = r0 + rg; r < r1; r += RG) dZ[r * ldz + c] = (T)0.f;
@@ -595,22 +604,27 @@ dz_kernel(const void* dY, const void* pre, int y_f32, int64_t rows, int cols, T*
   }
 }
 
-// Column sums of the chunks' sums: 16 columns a block, 16 chunks at a time.
+// Column sums of the chunks' sums: 16 columns a block, 64 chunks at a time.
 template <typename T>
-__global__ void __launch_bounds__(256) db_kernel(const float* part, int64_t chunks, int cols, T* db) {
-  __shared__ float red[16][17];
+__global__ void __launch_bounds__(1024) db_kernel(const float* part, int64_t chunks, int cols, T* db) {
+  constexpr int Y = 64;
+  __shared__ float red[Y][17];
   const int x = threadIdx.x & 15, y = threadIdx.x >> 4;
   const int c = blockIdx.x * 16 + x;
   float sum = 0.f;
-  if (c < cols)
-    for (int64_t i = y; i < chunks; i += 16) sum += part[i * cols + c];
+  if (c < cols) {
+#pragma unroll 4
+    for (int64_t i = y; i < chunks; i += Y) sum += part[i * cols + c];
+  }
   red[y][x] = sum;
   __syncthreads();
-  if (y == 0 && c < cols) {
+  if (threadIdx.x < 64) {  // a wave: 4 threads a column, 16 of the sums each
     sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) sum += red[i][x];
-    db[c] = (T)sum;
+    for (int i = 0; i < Y / 4; ++i) sum += red[y * (Y / 4) + i][x];
+    sum += __shfl_xor(sum, 16);
+    sum += __shfl_xor(sum, 32);
+    if (y == 0 && c < cols) db[c] = (T)sum;
   }
 }
 
@@ -726,7 +740,7 @@ hipError_t launch_dz(int act, const void* dY, const void* pre, int y_f32, int64_
 
 template <typename T>
 hipError_t launch_db(const float* db_part, int64_t chunks, int cols, T* db, hipStream_t s) {
-  db_kernel<T><<<(cols + 15) / 16, 256, 0, s>>>(db_part, chunks, cols, db);
+  db_kernel<T><<<(cols + 15) / 16, 1024, 0, s>>>(db_part, chunks, cols, db);
   return hipGetLastError();
 }
 
