@@ -202,8 +202,6 @@ static hipError_t linear_forward(const T* X, int64_t N, int d_in, const T* W, in
   p.K = d_in;
   p.bias = bias;
   p.c_f32 = y_f32;
-  p.c_vec = (int64_t)d_out * ey % 16 == 0 && aligned16(Y) && aligned16(residual) && aligned16(pre);
-  p.b_vec = aligned16(bias);
   p.partial = reinterpret_cast<float*>(ws + l.o_part);
   hipError_t e = hipSuccess;
   if (l.pad) p.B = ws + l.o_w;
@@ -254,7 +252,6 @@ static hipError_t linear_gradients(const void* dY, int y_f32, const T* X, int64_
     p.B = b.pad ? ws + b.o_w : static_cast<const void*>(W);
     p.lda = b.lz;
     p.K = d_out;
-    p.c_vec = !b.pad && aligned16(dX);
     for (int64_t r = 0; r < N; r += kLaunchRows) {
       p.M = std::min(N - r, kLaunchRows);
       p.A = dZ + r * b.lz;
@@ -270,7 +267,6 @@ static hipError_t linear_gradients(const void* dY, int y_f32, const T* X, int64_
     p.M = d_out;
     p.K = N;
     p.C = dW;
-    p.c_vec = !b.pad && aligned16(dW);
     e = run_product<T>(choose_cut(d_out, d_in, N, sizeof(T)), true, true, GMM_ACT_NONE, p, s);
   }
   return e;

@@ -178,72 +178,58 @@ struct Operand {
   }
 };
 
-// Loads / stores of W consecutive values of C's type as floats. `vec`: 16-byte
-// accesses are allowed; n is the number of values inside the row.
-template <typename T, int W>
-__device__ __forceinline__ void load_row(const void* p, int64_t at, int n, bool is_f32, bool vec, float* out) {
-  if (is_f32) {
-    const float* q = static_cast<const float*>(p) + at;
-    if (vec && n >= W) {
+// W consecutive values of a row, n of them inside it, as floats; whole ones in
+// 16-byte accesses of any alignment.
+template <typename E, int W>
+__device__ __forceinline__ void load_as(const E* q, int n, float* out) {
+  constexpr int P = 16 / sizeof(E) < W ? 16 / sizeof(E) : W;
+  if (n >= W) {
 #pragma unroll
-      for (int i = 0; i < W; i += 4) *reinterpret_cast<f32x4*>(out + i) = *reinterpret_cast<const f32x4*>(q + i);
-    } else {
+    for (int i = 0; i < W; i += P) {
+      E e[P];
+      __builtin_memcpy(e, q + i, sizeof(e));
 #pragma unroll
-      for (int i = 0; i < W; ++i) out[i] = i < n ? q[i] : 0.f;
+      for (int k = 0; k < P; ++k) out[i + k] = (float)e[k];
     }
   } else {
-    const T* q = static_cast<const T*>(p) + at;
-    constexpr int P = W * sizeof(T) < 16 ? 1 : 16 / sizeof(T);
-    if (P > 1 && vec && n >= W) {
 #pragma unroll
-      for (int i = 0; i < W; i += P) {
-        union {
-          u32x4 v;
-          T e[16 / sizeof(T)];
-        } u;
-        u.v = *reinterpret_cast<const u32x4*>(q + i);
-#pragma unroll
-        for (int k = 0; k < P; ++k) out[i + k] = (float)u.e[k];
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < W; ++i) out[i] = i < n ? (float)q[i] : 0.f;
-    }
+    for (int i = 0; i < W; ++i) out[i] = i < n ? (float)q[i] : 0.f;
   }
 }
 
-template <typename T, int W>
-__device__ __forceinline__ void store_row(void* p, int64_t at, int n, bool is_f32, bool vec, const float* v) {
-  if (is_f32) {
-    float* q = static_cast<float*>(p) + at;
-    if (vec && n >= W) {
+template <typename E, int W>
+__device__ __forceinline__ void store_as(E* q, int n, const float* v) {
+  constexpr int P = 16 / sizeof(E) < W ? 16 / sizeof(E) : W;
+  if (n >= W) {
 #pragma unroll
-      for (int i = 0; i < W; i += 4) *reinterpret_cast<f32x4*>(q + i) = f32x4{v[i], v[i + 1], v[i + 2], v[i + 3]};
-    } else {
+    for (int i = 0; i < W; i += P) {
+      E e[P];
 #pragma unroll
-      for (int i = 0; i < W; ++i)
-        if (i < n) q[i] = v[i];
+      for (int k = 0; k < P; ++k) e[k] = (E)v[i + k];
+      __builtin_memcpy(q + i, e, sizeof(e));
     }
   } else {
-    T* q = static_cast<T*>(p) + at;
-    constexpr int P = W * sizeof(T) < 16 ? 1 : 16 / sizeof(T);
-    if (P > 1 && vec && n >= W) {
 #pragma unroll
-      for (int i = 0; i < W; i += P) {
-        union {
-          u32x4 v;
-          T e[16 / sizeof(T)];
-        } u;
-#pragma unroll
-        for (int k = 0; k < P; ++k) u.e[k] = (T)v[i + k];
-        *reinterpret_cast<u32x4*>(q + i) = u.v;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < W; ++i)
-        if (i < n) q[i] = (T)v[i];
-    }
+    for (int i = 0; i < W; ++i)
+      if (i < n) q[i] = (E)v[i];
   }
+}
+
+// The same at element `at` of an array of C's type.
+template <typename T, int W>
+__device__ __forceinline__ void load_row(const void* p, int64_t at, int n, bool is_f32, float* out) {
+  if (is_f32)
+    load_as<float, W>(static_cast<const float*>(p) + at, n, out);
+  else
+    load_as<T, W>(static_cast<const T*>(p) + at, n, out);
+}
+
+template <typename T, int W>
+__device__ __forceinline__ void store_row(void* p, int64_t at, int n, bool is_f32, const float* v) {
+  if (is_f32)
+    store_as<float, W>(static_cast<float*>(p) + at, n, v);
+  else
+    store_as<T, W>(static_cast<T*>(p) + at, n, v);
 }
 
 // z + bias -> pre, act(.) + residual -> C for W consecutive n of one row.
@@ -253,16 +239,16 @@ __device__ __forceinline__ void finish_row(const ProductArgs& p, int64_t m, int 
   const int left = p.N - n;
 #pragma unroll
   for (int i = 0; i < W; ++i) z[i] += bias[i];
-  if (p.pre) store_row<T, W>(p.pre, at, left, p.c_f32, p.c_vec, z);
+  if (p.pre) store_row<T, W>(p.pre, at, left, p.c_f32, z);
 #pragma unroll
   for (int i = 0; i < W; ++i) z[i] = act_value<ACT>(z[i]);
   if (p.residual) {
     float r[W];
-    load_row<T, W>(p.residual, at, left, p.c_f32, p.c_vec, r);
+    load_row<T, W>(p.residual, at, left, p.c_f32, r);
 #pragma unroll
     for (int i = 0; i < W; ++i) z[i] += r[i];
   }
-  store_row<T, W>(p.C, at, left, p.c_f32, p.c_vec, z);
+  store_row<T, W>(p.C, at, left, p.c_f32, z);
 }
 
 // A block's tile and part of the contraction. Tiles go in groups of 8 tile
@@ -300,7 +286,7 @@ __device__ __forceinline__ void finish_tile(const ProductArgs& p, int part, int6
   if (p.splits == 1)
     finish_row<T, ACT, W>(p, m, n, z, bias);
   else
-    store_row<T, W>(p.partial, ((int64_t)part * p.M + m) * p.N + n, p.N - n, true, p.N % 4 == 0, z);
+    store_as<float, W>(p.partial + ((int64_t)part * p.M + m) * p.N + n, p.N - n, z);
 }
 
 template <typename T, int BM, int BN, int WM, int WN, bool AS, bool BS, int ACT>
@@ -396,7 +382,7 @@ product_kernel(const ProductArgs p) {
   float bias[W];
 #pragma unroll
   for (int i = 0; i < W; ++i) bias[i] = 0.f;
-  if (p.splits == 1 && p.bias) load_row<T, W>(p.bias, n, p.N - n, false, p.b_vec, bias);
+  if (p.splits == 1 && p.bias) load_as<T, W>(static_cast<const T*>(p.bias) + n, p.N - n, bias);
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
     const int64_t m = at.m0 + wm * TM + 16 * i + (lane & 15);
@@ -424,7 +410,7 @@ __global__ void __launch_bounds__(256) product_reduce_kernel(const ProductArgs p
       const float* q = p.partial + m * p.N + n;
       for (int s = s0; s < s1; ++s) {
         float v[W];
-        load_row<float, W>(q + s * part, 0, W, true, W == 4, v);
+        load_as<float, W>(q + s * part, W, v);
 #pragma unroll
         for (int k = 0; k < W; ++k) z[k] += v[k];
       }
@@ -441,7 +427,7 @@ __global__ void __launch_bounds__(256) product_reduce_kernel(const ProductArgs p
 #pragma unroll
       for (int k = 0; k < W; ++k)
         z[k] = (red[0][mine][k] + red[1][mine][k]) + (red[2][mine][k] + red[3][mine][k]);
-      if (p.bias) load_row<T, W>(p.bias, col, W, false, false, bias);
+      if (p.bias) load_as<T, W>(static_cast<const T*>(p.bias) + col, W, bias);
       finish_row<T, ACT, W>(p, row, col, z, bias);
     }
   }
@@ -449,65 +435,37 @@ __global__ void __launch_bounds__(256) product_reduce_kernel(const ProductArgs p
 
 // ---------------------------------------------------------------------------
 // Few rows. The weights are read once and everything else is small, so the
-// kernel is a stream over B: a block owns 16 rows of B, its waves split the
-// contraction, and every lane holds several 16-byte loads of B in flight. The
-// rows of A come from the caches, 16 at a time as the second operand.
+// kernel is a stream over B: a block owns NT * 16 rows of B, its waves split
+// the contraction. The rows of A come from the caches as the second operand.
 // ---------------------------------------------------------------------------
-template <typename T, int NW, int RT, int ACT>
+template <typename T, int NW, int NT, int ACT>
 __global__ void __launch_bounds__(64 * NW) few_kernel(const FewArgs p) {
-  constexpr int P = Frag<T>::kPer, kStep = 4 * P, U = RT == 1 ? 8 : 4;
-  __shared__ float red[NW][RT][16][17];
+  constexpr int NB = 16 * NT;
+  __shared__ float red[NW][16][NB + 1];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
-  const int n0 = blockIdx.x * 16;
-  const int brow = min(n0 + r, p.N - 1);
-  const T* B = static_cast<const T*>(p.B) + (int64_t)brow * p.K + g * P;
-  const T* A[RT];
+  const int n0 = blockIdx.x * NB;
+  const T *brow[NT], *arow = static_cast<const T*>(p.A) + (int64_t)min(r, p.M - 1) * p.K;
 #pragma unroll
-  for (int t = 0; t < RT; ++t)
-    A[t] = static_cast<const T*>(p.A) + (int64_t)min(16 * t + r, p.M - 1) * p.K + g * P;
-  f32x4 acc[RT];
+  for (int j = 0; j < NT; ++j) brow[j] = static_cast<const T*>(p.B) + (int64_t)min(n0 + 16 * j + r, p.N - 1) * p.K;
+  f32x4 acc[1][NT];
+  stream_rows<T, NW, 1, NT, 8 / NT>(brow, &arow, p.K, wave, g, acc);
 #pragma unroll
-  for (int t = 0; t < RT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const int steps = (p.K + kStep - 1) / kStep, per = (steps + NW - 1) / NW;
-  const int s0 = wave * per, s1 = min(steps, s0 + per);
-  int s = s0;
-  for (; s + U <= s1 && (s + U) * kStep <= p.K; s += U) {
-    u32x4 fb[U], fa[U][RT];
+  for (int j = 0; j < NT; ++j)
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      fb[u] = load16(B + (s + u) * kStep);
-#pragma unroll
-      for (int t = 0; t < RT; ++t) fa[u][t] = load16(A[t] + (s + u) * kStep);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int t = 0; t < RT; ++t) acc[t] = Frag<T>::mma(fb[u], fa[u][t], acc[t]);
-  }
-  for (; s < s1; ++s) {
-    const int left = p.K - s * kStep - g * P;
-    const u32x4 fb = load_frag<T>(B + s * kStep, left);
-#pragma unroll
-    for (int t = 0; t < RT; ++t) acc[t] = Frag<T>::mma(fb, load_frag<T>(A[t] + s * kStep, left), acc[t]);
-  }
-#pragma unroll
-  for (int t = 0; t < RT; ++t)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) red[wave][t][r][4 * g + q] = acc[t][q];
+    for (int q = 0; q < 4; ++q) red[wave][r][16 * j + 4 * g + q] = acc[0][j][q];
   __syncthreads();
-  for (int i = threadIdx.x; i < 256 * RT; i += 64 * NW) {
-    const int n = i & 15, m = i >> 4;
+  for (int i = threadIdx.x; i < 16 * NB; i += 64 * NW) {
+    const int n = i % NB, m = i / NB;
     if (m >= p.M || n0 + n >= p.N) continue;
     float z = 0.f;
 #pragma unroll
-    for (int w = 0; w < NW; ++w) z += red[w][m >> 4][m & 15][n];
+    for (int w = 0; w < NW; ++w) z += red[w][m][n];
     ProductArgs e;
     e.N = p.N;
     e.residual = p.residual;
     e.C = p.C;
     e.pre = p.pre;
     e.c_f32 = p.c_f32;
-    e.c_vec = 0;
     float bias = p.bias ? (float)static_cast<const T*>(p.bias)[n0 + n] : 0.f;
     finish_row<T, ACT, 1>(e, m, n0 + n, &z, &bias);
   }
@@ -521,7 +479,8 @@ __device__ __forceinline__ void pad_rows(const PadJob& j, int64_t i0, int64_t st
   const int pieces = (int)(j.ld / P);
   const int64_t total = j.rows * pieces;
   for (int64_t i = i0; i < total; i += stride) {
-    const int64_t r = i / pieces;
+    // a 64-bit division is a hundred instructions, a 32-bit one twenty
+    const int64_t r = total < (1ll << 31) ? (int64_t)((uint32_t)i / (uint32_t)pieces) : i / pieces;
     const int c = (int)(i - r * pieces) * P;
     *reinterpret_cast<u32x4*>(static_cast<T*>(j.dst) + r * j.ld + c) =
         load_frag<T>(static_cast<const T*>(j.src) + r * j.cols + c, j.cols - c);
@@ -544,7 +503,7 @@ __global__ void __launch_bounds__(256) zero_kernel(T* p, int64_t n) {
 }
 
 // dZ and the column sums of a chunk of rows. A thread owns V consecutive
-// columns (V * 16 bits or more in one access where the rows allow it), 256 / CG
+// columns (16 bytes of the operands' type), 256 / CG
 // rows go at a time; the rows' sums meet in LDS at the end. The last `pads`
 // blocks copy X and W to padded rows, where the products need that.
 template <typename T, int ACT, int V, int CG>
@@ -567,15 +526,15 @@ dz_kernel(const void* __restrict__ dY, const void* __restrict__ pre, int y_f32, 
   float sum[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) sum[i] = 0.f;
-  if (c < cols) {
+  if (c < cols) {  // dZ's padding, less than V, is behind the last of them: loaded as zeros
     constexpr int U = 4;  // rows in flight
     for (int64_t r = r0 + rg; r < r1; r += U * RG) {
       float v[U][V], z[U][V];
 #pragma unroll
       for (int u = 0; u < U; ++u)
         if (r + u * RG < r1) {
-          load_row<T, V>(dY, (r + u * RG) * cols + c, left, y_f32, V > 1, v[u]);
-          if (ACT != GMM_ACT_NONE) load_row<T, V>(pre, (r + u * RG) * cols + c, left, y_f32, V > 1, z[u]);
+          load_row<T, V>(dY, (r + u * RG) * cols + c, left, y_f32, v[u]);
+          if (ACT != GMM_ACT_NONE) load_row<T, V>(pre, (r + u * RG) * cols + c, left, y_f32, z[u]);
         }
 #pragma unroll
       for (int u = 0; u < U; ++u)
@@ -585,11 +544,9 @@ dz_kernel(const void* __restrict__ dY, const void* __restrict__ pre, int y_f32, 
             for (int i = 0; i < V; ++i) v[u][i] *= act_slope<ACT>(z[u][i]);
 #pragma unroll
           for (int i = 0; i < V; ++i) sum[i] += v[u][i];
-          if (dZ) store_row<T, V>(dZ, (r + u * RG) * ldz + c, left, false, V > 1, v[u]);
+          if (dZ) store_as<T, V>(dZ + (r + u * RG) * ldz + c, (int)min((int64_t)V, ldz - c), v[u]);
         }
     }
-  } else if (dZ && c < ldz) {  // the rows' padding (V = 1: rows of whole pieces have none)
-    for (int64_t r = r0 + rg; r < r1; r += RG) dZ[r * ldz + c] = (T)0.f;
   }
   if (!db_part) return;
 #pragma unroll
@@ -668,11 +625,12 @@ template <typename T>
 hipError_t launch_few(int act, const FewArgs& p, hipStream_t s) {
   return with_act(act, [&](auto a) {
     constexpr int ACT = decltype(a)::value;
-    const dim3 grid((p.N + 15) / 16);
-    if (p.M <= 16)
-      few_kernel<T, 8, 1, ACT><<<grid, 512, 0, s>>>(p);
+    // more than two blocks a CU: two tiles a block, which halves what is read
+    // of A; a single row is one address for all lanes and costs little
+    if (p.N >= 16 * 512 && p.M > 1)
+      few_kernel<T, 8, 2, ACT><<<(p.N + 31) / 32, 512, 0, s>>>(p);
     else
-      few_kernel<T, 8, 4, ACT><<<grid, 512, 0, s>>>(p);
+      few_kernel<T, 8, 1, ACT><<<(p.N + 15) / 16, 512, 0, s>>>(p);
     return hipGetLastError();
   });
 }
@@ -710,7 +668,7 @@ hipError_t launch_reduce(int act, const ProductArgs& p, hipStream_t s) {
 template <typename T, int ACT, int V>
 static void launch_dz_columns(const void* dY, const void* pre, int y_f32, int64_t rows, int cols, T* dZ, int64_t ldz,
                               float* db_part, int64_t chunk_rows, const PadJob& px, const PadJob& pw, hipStream_t s) {
-  const int64_t groups = ((dZ ? ldz : cols) + V - 1) / V, chunks = (rows + chunk_rows - 1) / chunk_rows;
+  const int64_t groups = (cols + V - 1) / V, chunks = (rows + chunk_rows - 1) / chunk_rows;
   const int64_t pieces = (px.rows * px.ld + pw.rows * pw.ld) / Frag<T>::kPer;
   const int pads = pieces ? (int)blocks_for(pieces) : 0;
   const int across = groups > 16 ? (int)((groups + 63) / 64) : 1;
@@ -726,14 +684,9 @@ static void launch_dz_columns(const void* dY, const void* pre, int y_f32, int64_
 template <typename T>
 hipError_t launch_dz(int act, const void* dY, const void* pre, int y_f32, int64_t rows, int cols, T* dZ, int64_t ldz,
                      float* db_part, int64_t chunk_rows, const PadJob& px, const PadJob& pw, hipStream_t s) {
-  constexpr int P = 16 / sizeof(T);
-  const bool vec = cols % P == 0 && ((reinterpret_cast<uintptr_t>(dY) | reinterpret_cast<uintptr_t>(pre)) & 15) == 0;
   return with_act(act, [&](auto a) {
-    constexpr int ACT = decltype(a)::value;
-    if (vec)
-      launch_dz_columns<T, ACT, P>(dY, pre, y_f32, rows, cols, dZ, ldz, db_part, chunk_rows, px, pw, s);
-    else
-      launch_dz_columns<T, ACT, 1>(dY, pre, y_f32, rows, cols, dZ, ldz, db_part, chunk_rows, px, pw, s);
+    launch_dz_columns<T, decltype(a)::value, Frag<T>::kPer>(dY, pre, y_f32, rows, cols, dZ, ldz, db_part, chunk_rows,
+                                                            px, pw, s);
     return hipGetLastError();
   });
 }

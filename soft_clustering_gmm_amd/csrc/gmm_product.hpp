@@ -154,6 +154,46 @@ __device__ __forceinline__ u32x4 load_frag(const T* p, int n) {
   return u.v;
 }
 
+// A stream over weights with a few rows beside them: NT * 16 rows of B (at
+// brow[j], this lane's row of tile j) times RT * 16 rows of A (at arow[t]), both
+// k-contiguous with K elements a row and of any alignment, over the steps of k
+// that are this wave's of NW. Every lane holds U steps of 16-byte loads in
+// flight; the loads of B come first, as A's addresses may still be on their way.
+template <typename T, int NW, int RT, int NT, int U>
+__device__ __forceinline__ void stream_rows(const T* const* brow, const T* const* arow, int K, int wave, int g,
+                                            f32x4 (*acc)[NT]) {
+  constexpr int P = Frag<T>::kPer, kStep = 4 * P;
+#pragma unroll
+  for (int t = 0; t < RT; ++t)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[t][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int steps = (K + kStep - 1) / kStep, per = (steps + NW - 1) / NW;
+  const int s1 = min(steps, (wave + 1) * per);
+  int k = wave * per * kStep + g * P;
+  int s = wave * per;
+  for (; s + U <= s1 && (s + U) * kStep <= K; s += U, k += U * kStep) {
+    u32x4 fb[U][NT], fa[U][RT];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) fb[u][j] = load16(brow[j] + k + u * kStep);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int t = 0; t < RT; ++t) fa[u][t] = load16(arow[t] + k + u * kStep);
+#pragma unroll
+    for (int u = 0; u < U; ++u) Frag<T>::template mma_tiles<RT, NT>(fb[u], fa[u], acc);
+  }
+  for (; s < s1; ++s, k += kStep) {
+    u32x4 fb[NT], fa[RT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) fb[j] = load_frag<T>(brow[j] + k, K - k);
+#pragma unroll
+    for (int t = 0; t < RT; ++t) fa[t] = load_frag<T>(arow[t] + k, K - k);
+    Frag<T>::template mma_tiles<RT, NT>(fb, fa, acc);
+  }
+}
+
 // Block b of `total` in launch order -> its place in an order in which the
 // blocks that one XCD runs (every eighth) are neighbours and share its L2.
 __device__ __forceinline__ int xcd_place(int b, int total) {
