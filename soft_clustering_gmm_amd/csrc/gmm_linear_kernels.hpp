@@ -17,16 +17,24 @@ __device__ __forceinline__ lds_ptr to_lds(const void* p) {
 
 // ---------------------------------------------------------------------------
 // Tiled product. A block computes a BM x BN tile of C with WM x WN waves; a
-// step of the contraction brings kStepBytes of k of both operands into one
-// half of LDS, by loads that go to LDS directly, while the waves multiply the
-// other half.
+// step of the contraction brings kStepBytes of k of both operands into one of
+// two slots of LDS, by loads that go to LDS directly. A's tile is two halves of
+// rows, and every wave owns rows in both.
 //
-// The loop is pipelined in registers too: a step has two half steps of k, and
-// the fragments of the next half step are read from LDS between the matrix
-// instructions of the present one. The barrier stands between the half steps,
-// where every wave holds its last fragments of the old step in registers: it
-// says that the next step's tiles have arrived and that the old half of LDS
-// may be filled again, and matrix instructions follow it at once.
+// A step has four phases (half of A, half of k), and the fragments of the next
+// phase are read from LDS between the matrix instructions of the present one:
+//   phase 0: multiply A0, first k;   read A0 and B, second k
+//   barrier: A1 of this step has arrived; A0 and B are read out -> load theirs
+//            of step s + 2
+//   phase 1: multiply A0, second k;  read A1, first k
+//   phase 2: multiply A1, first k;   read A1, second k
+//   barrier: A0 and B of the next step have arrived; A1 is read out -> load it
+//   phase 3: multiply A1, second k;  read A0 and B, first k, of the next step
+// A load so has one and a half steps to arrive. That is what bounds the large
+// shapes: with one step (both barriers in one place) the loads alone took 692 us
+// at 8192 x 16384 x 4096 in bfloat16, the matrix instructions alone 535 and the
+// LDS reads alone 430; with two steps in flight and 4 tile rows side by side
+// instead of 8 the loads took 546.
 //
 // The matrix instruction gets B's rows (n) as its first operand and A's rows
 // (m) as its second, so a lane's results are 4 consecutive n of one m; the
@@ -54,10 +62,11 @@ __device__ __forceinline__ void load_to_lds(uint32_t lds, uint32_t offset, i32x4
                : "s"(lds), "v"(offset), "s"(buffer));
 }
 
-// Every load of this wave has arrived in LDS and its LDS reads are done; then
-// the block's barrier. `lds` ties the tile's memory to it.
+// All but the last PENDING loads of this wave have arrived in LDS and its LDS
+// reads are done; then the block's barrier. `lds` ties the tiles' memory to it.
+template <int PENDING>
 __device__ __forceinline__ void step_barrier(const void* lds) {
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" : : "v"(to_lds(lds)) : "memory");
+  asm volatile("s_waitcnt vmcnt(%1) lgkmcnt(0)\n\ts_barrier" : : "v"(to_lds(lds)), "n"(PENDING) : "memory");
 }
 
 template <int NI>
@@ -88,6 +97,7 @@ struct Operand {
   uint32_t off[kLoads];  // byte offset of this lane's chunk from base
 
   static __device__ __forceinline__ int key(int k) {
+    if (kRowChunks == 4) return (k & 2);  // 64-byte rows: four of k are 256 bytes by themselves
     return PERM ? key_k_perm<NI>(k) : key_k(k);
   }
 
@@ -123,10 +133,12 @@ struct Operand {
     }
   }
 
-  // Loads of step `step` of the part, of whose k `k_left` remain.
-  __device__ __forceinline__ void load(uint32_t lds, int64_t step, int64_t k_left, int wave, int lane) const {
-    const uintptr_t b = reinterpret_cast<uintptr_t>(base) + step * step_bytes;
-    int64_t n = left - step * step_bytes;
+  // Loads of step `step` of the part, of whose k `k_left` remain, `ahead` bytes
+  // further on (the other half of a tile).
+  __device__ __forceinline__ void load(uint32_t lds, int64_t step, int64_t k_left, int wave, int lane,
+                                       int64_t ahead) const {
+    const uintptr_t b = reinterpret_cast<uintptr_t>(base) + step * step_bytes + ahead;
+    int64_t n = left - step * step_bytes - ahead;
     n = n < 0 ? 0 : n > 0x7fffffff ? 0x7fffffff : n;
     i32x4 buffer;
     buffer[0] = (int)(uint32_t)b;
@@ -251,7 +263,7 @@ __device__ __forceinline__ void finish_row(const ProductArgs& p, int64_t m, int 
   store_row<T, W>(p.C, at, left, p.c_f32, z);
 }
 
-// A block's tile and part of the contraction. Tiles go in groups of 8 tile
+// A block's tile and part of the contraction. Tiles go in groups of 4 tile
 // rows, column by column within a group, so that the blocks an XCD runs
 // together share rows of A and of B in its L2.
 struct Place {
@@ -263,7 +275,7 @@ __device__ __forceinline__ Place tile_place(const ProductArgs& p, int bm, int bn
   Place at;
   at.part = blockIdx.x / tiles;
   const int t = xcd_place(blockIdx.x - at.part * tiles, tiles);
-  constexpr int G = 8;
+  constexpr int G = 4;
   const int group = t / (G * p.tiles_n), first = group * G;
   const int height = min(G, p.tiles_m - first), in = t - group * G * p.tiles_n;
   at.m0 = (int64_t)(first + in % height) * bm;
@@ -292,11 +304,11 @@ __device__ __forceinline__ void finish_tile(const ProductArgs& p, int part, int6
 template <typename T, int BM, int BN, int WM, int WN, bool AS, bool BS, int ACT>
 __global__ void __launch_bounds__(64 * WM * WN, 2)
 product_kernel(const ProductArgs p) {
-  constexpr int NW = WM * WN, TM = BM / WM, TN = BN / WN, MI = TM / 16, NI = TN / 16, W = 4 * NI;
-  using OA = Operand<T, BM, NW, AS, false, 1>;
+  constexpr int NW = WM * WN, HM = BM / 2, TM = HM / WM, TN = BN / WN, MI = TM / 16, NI = TN / 16, W = 4 * NI;
+  using OA = Operand<T, HM, NW, AS, false, 1>;
   using OB = Operand<T, BN, NW, BS, true, NI>;
-  constexpr int kHalf = OA::kBytes + OB::kBytes;
-  __shared__ __align__(1024) char lds[2 * kHalf];
+  constexpr int kSlot = 2 * OA::kBytes + OB::kBytes, kPending = 2 * OA::kLoads + OB::kLoads;
+  __shared__ __align__(1024) char lds[2 * kSlot];
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN;
@@ -308,40 +320,37 @@ product_kernel(const ProductArgs p) {
   a.init(p.A, p.lda, at.m0, p.M, k0, k1, wave, lane);
   b.init(p.B, p.ldb, at.n0, p.N, k0, k1, wave, lane);
 
-  f32x4 acc[MI][NI];
+  f32x4 acc[2][MI][NI];
 #pragma unroll
-  for (int i = 0; i < MI; ++i)
-#pragma unroll
-    for (int j = 0; j < NI; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int i = 0; i < 2 * MI * NI; ++i) (&acc[0][0][0])[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   const int steps = (int)((k1 - k0 + OA::kStep - 1) / OA::kStep);
+  const int64_t half = (AS ? HM : HM * p.lda) * (int)sizeof(T);
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)reinterpret_cast<uintptr_t>(to_lds(lds)));
-  auto load = [&](int s) {
-    const uint32_t at = lds0 + (s & 1) * kHalf;
-    const int64_t k_left = k1 - k0 - (int64_t)s * OA::kStep;
-    a.load(at, s, k_left, wave, lane);
-    b.load(at + OA::kBytes, s, k_left, wave, lane);
+  // Steps past the end bring zeros and no traffic, so that the number of loads
+  // in flight is the same at every barrier.
+  auto load_a = [&](int s, int h) {
+    a.load(lds0 + (s & 1) * kSlot + h * OA::kBytes, s, k1 - k0 - (int64_t)s * OA::kStep, wave, lane, h * half);
   };
-  // Half of A's tiles of a half step, and B's tiles, in two sets of registers.
-  constexpr int HI = MI / 2;
-  u32x4 fa[2][HI], fb[2][NI];
-  auto read_a = [&](int s, int kk, int h) {
+  auto load_b = [&](int s) {
+    b.load(lds0 + (s & 1) * kSlot + 2 * OA::kBytes, s, k1 - k0 - (int64_t)s * OA::kStep, wave, lane, 0);
+  };
+  u32x4 fa[2][MI], fb[2][NI];  // by half of k
+  auto read_a = [&](int s, int h, int kk) {
 #pragma unroll
-    for (int i = 0; i < HI; ++i)
-      fa[h][i] = OA::frag(lds + (s & 1) * kHalf, wm * TM, h * HI + i, kk, lane);
+    for (int i = 0; i < MI; ++i)
+      fa[kk][i] = OA::frag(lds + (s & 1) * kSlot + h * OA::kBytes, wm * TM, i, kk, lane);
   };
   auto read_b = [&](int s, int kk) {
 #pragma unroll
-    for (int j = 0; j < NI; ++j) fb[kk][j] = OB::frag(lds + (s & 1) * kHalf + OA::kBytes, wn * TN, j, kk, lane);
+    for (int j = 0; j < NI; ++j) fb[kk][j] = OB::frag(lds + (s & 1) * kSlot + 2 * OA::kBytes, wn * TN, j, kk, lane);
   };
-  auto multiply = [&](int kk, int h) {
-    Frag<T>::template mma_tiles<HI, NI>(fb[kk], fa[h], acc + h * HI);
-  };
-  // The reads of one phase, one after every few of its matrix instructions.
+  // The multiplication of a phase, one of its reads after every few matrix instructions.
   constexpr int kPerA = !AS ? 1 : sizeof(T) == 4 ? 4 : 2, kPerB = !BS ? 1 : sizeof(T) == 4 ? 4 : 2;
-  constexpr int kMma = HI * NI * (sizeof(T) == 4 ? 4 : 1);
-  auto interleave = [&](auto with_b) {
-    constexpr int reads = HI * kPerA + (decltype(with_b)::value ? NI * kPerB : 0);
+  constexpr int kMma = MI * NI * (sizeof(T) == 4 ? 4 : 1);
+  auto multiply = [&](int h, int kk, auto with_b) {
+    Frag<T>::template mma_tiles<MI, NI>(fb[kk], fa[kk], acc[h]);
+    constexpr int reads = MI * kPerA + (decltype(with_b)::value ? NI * kPerB : 0);
     constexpr int between = kMma / reads > 1 ? kMma / reads : 1;
 #pragma unroll
     for (int i = 0; i < reads; ++i) {
@@ -350,30 +359,30 @@ product_kernel(const ProductArgs p) {
     }
     __builtin_amdgcn_sched_barrier(0);
   };
-  load(0);
-  step_barrier(lds);
-  load(1);
+  load_a(0, 0), load_b(0), load_a(0, 1);
+  load_a(1, 0), load_b(1), load_a(1, 1);
+  step_barrier<kPending + OA::kLoads>(lds);
   read_a(0, 0, 0);
   read_b(0, 0);
   __builtin_amdgcn_sched_barrier(0);
   for (int s = 0; s < steps; ++s) {
     read_a(s, 0, 1);
-    multiply(0, 0);
-    interleave(std::false_type{});
-    read_a(s, 1, 0);
     read_b(s, 1);
-    multiply(0, 1);
-    interleave(std::true_type{});
-    read_a(s, 1, 1);
-    multiply(1, 0);
-    interleave(std::false_type{});
-    step_barrier(lds);
-    load(s + 2);  // past the end: zeros, no traffic
+    multiply(0, 0, std::true_type{});
+    step_barrier<kPending>(lds);
+    load_a(s + 2, 0);
+    load_b(s + 2);
     __builtin_amdgcn_sched_barrier(0);
-    read_a(s + 1, 0, 0);  // after the last step: what an earlier step left, not used
+    read_a(s, 1, 0);
+    multiply(0, 1, std::false_type{});
+    read_a(s, 1, 1);
+    multiply(1, 0, std::false_type{});
+    step_barrier<kPending>(lds);
+    load_a(s + 2, 1);
+    __builtin_amdgcn_sched_barrier(0);
+    read_a(s + 1, 0, 0);  // after the last step: zeros, not used
     read_b(s + 1, 0);
-    multiply(1, 1);
-    interleave(std::true_type{});
+    multiply(1, 1, std::true_type{});
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // nothing arrives in LDS after the block's end
 
@@ -384,9 +393,9 @@ product_kernel(const ProductArgs p) {
   for (int i = 0; i < W; ++i) bias[i] = 0.f;
   if (p.splits == 1 && p.bias) load_as<T, W>(static_cast<const T*>(p.bias) + n, p.N - n, bias);
 #pragma unroll
-  for (int i = 0; i < MI; ++i) {
-    const int64_t m = at.m0 + wm * TM + 16 * i + (lane & 15);
-    if (m < p.M) finish_tile<T, ACT, NI>(p, at.part, m, n, acc[i], bias);
+  for (int i = 0; i < 2 * MI; ++i) {
+    const int64_t m = at.m0 + i / MI * HM + wm * TM + 16 * (i % MI) + (lane & 15);
+    if (m < p.M) finish_tile<T, ACT, NI>(p, at.part, m, n, acc[i / MI][i % MI], bias);
   }
 }
 
