@@ -328,7 +328,7 @@ enum gmm_activation { GMM_ACT_NONE = 0, GMM_ACT_RELU = 1, GMM_ACT_GELU = 2, GMM_
  * float, rounded once per output. Y may be
  * residual itself; no other output may overlap an input. Where a row of X is
  * a multiple of 16 bytes long, X and W must be 16-byte aligned (rows of other
- * lengths may start at any element). N < 2^31. The workspace must hold
+ * lengths may start at any element). N <= 2^30. The workspace must hold
  * gmm_linear_workspace_bytes(N, d_in, d_out, x_dtype, 0) bytes. */
 int gmm_linear(const void* X, int32_t x_dtype, int64_t N, int32_t d_in, const void* W, int32_t d_out,
                const void* bias, int32_t act, const void* residual, void* Y, int32_t y_dtype, float* pre,

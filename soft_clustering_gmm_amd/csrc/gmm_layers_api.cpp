@@ -13,8 +13,10 @@
 namespace gmm {
 
 constexpr int kMaxWidth = 65536;             // d_in, d_out, width, hidden
+constexpr int64_t kMaxRows = 1 << 30;        // rows of a linear layer's call
 constexpr int64_t kLaunchRows = 1 << 20;     // rows of one launch (the grid's size)
 constexpr int64_t kDzRows = 16;              // rows per column-sum chunk, at least
+constexpr int64_t kDzMostRows = 8192;        // and at most: they are added one after the other
 constexpr int64_t kDzBlocks = 2048;          // blocks of the column sums, where the rows allow it
 
 static size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
@@ -150,6 +152,7 @@ static BackwardPlan backward_plan(int64_t N, int d_in, int d_out, int e, bool pl
   b.own_dz = !(plain_dz && b.lz == d_out) && (want_dx || want_dw);
   const int64_t across = ceil_div(d_out, 64 * (16 / e));
   b.chunk = std::max(kDzRows, ceil_div(ceil_div(N * across, kDzBlocks), kDzRows) * kDzRows);
+  b.chunk = std::min(b.chunk, kDzMostRows);
   b.chunks = ceil_div(N, b.chunk);
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -182,7 +185,7 @@ static int check_ws(const void* ws, size_t have, size_t need) {
 static int check_linear(int64_t N, int32_t d_in, int32_t d_out, int32_t x_dtype, int32_t y_dtype, int32_t act) {
   if (!dtype_ok(x_dtype) || (y_dtype != x_dtype && y_dtype != GMM_F32) || !act_ok(act)) return GMM_EINVAL;
   if (N < 0 || d_in < 1 || d_out < 1) return GMM_EINVAL;
-  if (d_in > kMaxWidth || d_out > kMaxWidth || N >= (1ll << 31)) return GMM_EUNSUPPORTED;
+  if (d_in > kMaxWidth || d_out > kMaxWidth || N > kMaxRows) return GMM_EUNSUPPORTED;
   return GMM_OK;
 }
 

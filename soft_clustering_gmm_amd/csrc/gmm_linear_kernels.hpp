@@ -56,8 +56,9 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 // zeros. Written out because the compiler makes every transposing LDS read
 // wait for such loads in flight, which would undo the double buffering; the
 // kernel's own waits are in step_barrier(). Nothing is returned in registers.
+// The wait states cover M0, and a buffer word that a vector instruction wrote.
 __device__ __forceinline__ void load_to_lds(uint32_t lds, uint32_t offset, i32x4 buffer) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                :
                : "s"(lds), "v"(offset), "s"(buffer));
 }
@@ -91,10 +92,12 @@ struct Operand {
   static constexpr int kLoads = kBytes / 1024 / NWAVES;  // wave loads of 1 KB
   static constexpr int kRowChunks = BR * (int)sizeof(T) / 16;  // k-strided: chunks per k
 
-  const char* base;      // element (first row of the tile, first k of the part)
+  uintptr_t base;        // element (first row of the tile, first k of the part)
   int64_t step_bytes;    // from one step to the next
-  int64_t left;          // bytes from base to the operand's end (k-strided: to the end of the part's k range)
+  int64_t left;          // bytes from base to the end of the operand's rows (of the part's k)
+  int rows_left;         // k-strided: elements from the tile's first row to the end of a k
   uint32_t off[kLoads];  // byte offset of this lane's chunk from base
+  static constexpr uint32_t kNowhere = 0x80000000u;  // beyond any buffer: zeros
 
   static __device__ __forceinline__ int key(int k) {
     if (kRowChunks == 4) return (k & 2);  // 64-byte rows: four of k are 256 bytes by themselves
@@ -109,15 +112,22 @@ struct Operand {
     return ((ch % 8) ^ (PERM ? key_rows_perm<NI>(r) : key_rows(r))) * kPer;
   }
 
+  // The same for its first row (k-strided).
+  static __device__ __forceinline__ int chunk_row(int j, int wave, int lane) {
+    const int ch = (wave * kLoads + j) * 64 + lane;
+    return ((ch % kRowChunks) ^ key(ch / kRowChunks)) * kPer;
+  }
+
   __device__ __forceinline__ void init(const void* p, int64_t ld, int64_t r0, int64_t rows, int64_t k0, int64_t k1,
                                        int wave, int lane) {
     const int e = sizeof(T);
     if (STRIDED) {
-      base = static_cast<const char*>(p) + (k0 * ld + r0) * e;
+      base = reinterpret_cast<uintptr_t>(p) + (k0 * ld + r0) * e;
       step_bytes = kStep * ld * e;
       left = ((k1 - k0) * ld - r0) * e;
+      rows_left = (int)(ld - r0);
     } else {
-      base = static_cast<const char*>(p) + (r0 * ld + k0) * e;
+      base = reinterpret_cast<uintptr_t>(p) + (r0 * ld + k0) * e;
       step_bytes = kStepBytes;
       left = ((rows - r0) * ld - k0) * e;
     }
@@ -125,30 +135,32 @@ struct Operand {
     for (int j = 0; j < kLoads; ++j) {
       const int ch = (wave * kLoads + j) * 64 + lane;  // chunk of the tile in LDS order
       if (STRIDED) {
-        const int k = ch / kRowChunks, c = (ch % kRowChunks) ^ key(k);
-        off[j] = (uint32_t)(k * ld * e + 16 * c);
+        off[j] = (uint32_t)(ch / kRowChunks * ld * e + chunk_row(j, wave, lane) * e);
       } else {
         off[j] = (uint32_t)((ch / 8) * ld * e + chunk_k(j, wave, lane) * e);
       }
     }
   }
 
-  // Loads of step `step` of the part, of whose k `k_left` remain, `ahead` bytes
-  // further on (the other half of a tile).
-  __device__ __forceinline__ void load(uint32_t lds, int64_t step, int64_t k_left, int wave, int lane,
+  // Loads of step `step` of the part, of whose k `k_left` remain, from row
+  // `skip` of the tile on (its other half), `ahead` bytes further. What is read
+  // is inside the operand: k is held to k_left and the rows of a k-strided one
+  // to rows_left; a k-contiguous one's rows past the last are beyond the buffer,
+  // whose size is that seen from step 0.
+  __device__ __forceinline__ void load(uint32_t lds, int step, int k_left, int wave, int lane, int skip,
                                        int64_t ahead) const {
-    const uintptr_t b = reinterpret_cast<uintptr_t>(base) + step * step_bytes + ahead;
-    int64_t n = left - step * step_bytes - ahead;
-    n = n < 0 ? 0 : n > 0x7fffffff ? 0x7fffffff : n;
+    const uintptr_t b = base + step * step_bytes + ahead;
+    const int64_t n = left - ahead;
     i32x4 buffer;
     buffer[0] = (int)(uint32_t)b;
     buffer[1] = (int)((uint32_t)(b >> 32) & 0xffff);
-    buffer[2] = (int)n;
+    buffer[2] = n < 0 ? 0 : n > 0x7fffffff ? 0x7fffffff : (int)n;
     buffer[3] = 0x00027000;
-    const int left_here = (int)(k_left < kStep ? k_left : kStep);
 #pragma unroll
-    for (int j = 0; j < kLoads; ++j)
-      load_to_lds(lds + (wave * kLoads + j) * 1024, chunk_k(j, wave, lane) < left_here ? off[j] : 0x80000000u, buffer);
+    for (int j = 0; j < kLoads; ++j) {
+      const bool inside = chunk_k(j, wave, lane) < k_left && (!STRIDED || chunk_row(j, wave, lane) < rows_left - skip);
+      load_to_lds(lds + (wave * kLoads + j) * 1024, inside ? off[j] : kNowhere, buffer);
+    }
   }
 
   // Fragment of the 16 rows of tile i (of a wave whose rows start at w0), k
@@ -324,16 +336,18 @@ product_kernel(const ProductArgs p) {
 #pragma unroll
   for (int i = 0; i < 2 * MI * NI; ++i) (&acc[0][0][0])[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  const int steps = (int)((k1 - k0 + OA::kStep - 1) / OA::kStep);
+  const int k_all = (int)(k1 - k0);  // at most 2^30
+  const int steps = (k_all + OA::kStep - 1) / OA::kStep;
   const int64_t half = (AS ? HM : HM * p.lda) * (int)sizeof(T);
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)reinterpret_cast<uintptr_t>(to_lds(lds)));
   // Steps past the end bring zeros and no traffic, so that the number of loads
   // in flight is the same at every barrier.
   auto load_a = [&](int s, int h) {
-    a.load(lds0 + (s & 1) * kSlot + h * OA::kBytes, s, k1 - k0 - (int64_t)s * OA::kStep, wave, lane, h * half);
+    a.load(lds0 + (s & 1) * kSlot + h * OA::kBytes, s, k_all - s * OA::kStep, wave, lane, h * HM,
+           h * half);
   };
   auto load_b = [&](int s) {
-    b.load(lds0 + (s & 1) * kSlot + 2 * OA::kBytes, s, k1 - k0 - (int64_t)s * OA::kStep, wave, lane, 0);
+    b.load(lds0 + (s & 1) * kSlot + 2 * OA::kBytes, s, k_all - s * OA::kStep, wave, lane, 0, 0);
   };
   u32x4 fa[2][MI], fb[2][NI];  // by half of k
   auto read_a = [&](int s, int h, int kk) {
