@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "../../include/gmm.h"
 
 namespace gmm {
@@ -168,23 +170,31 @@ __device__ __forceinline__ void stream_rows(const T* const* brow, const T* const
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[t][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   const int steps = (K + kStep - 1) / kStep, per = (steps + NW - 1) / NW;
-  const int s1 = min(steps, (wave + 1) * per);
-  int k = wave * per * kStep + g * P;
+  const int s1 = min(steps, (wave + 1) * per), whole = min(s1, K / kStep);  // whole steps, and all of them
   int s = wave * per;
-  for (; s + U <= s1 && (s + U) * kStep <= K; s += U, k += U * kStep) {
-    u32x4 fb[U][NT], fa[U][RT];
+  auto batch = [&](auto steps_in_flight) {
+    constexpr int V = decltype(steps_in_flight)::value;
+    const int k = s * kStep + g * P;
+    u32x4 fb[V][NT], fa[V][RT];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int u = 0; u < V; ++u)
 #pragma unroll
       for (int j = 0; j < NT; ++j) fb[u][j] = load16(brow[j] + k + u * kStep);
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int u = 0; u < V; ++u)
 #pragma unroll
       for (int t = 0; t < RT; ++t) fa[u][t] = load16(arow[t] + k + u * kStep);
 #pragma unroll
-    for (int u = 0; u < U; ++u) Frag<T>::template mma_tiles<RT, NT>(fb[u], fa[u], acc);
-  }
-  for (; s < s1; ++s, k += kStep) {
+    for (int u = 0; u < V; ++u) Frag<T>::template mma_tiles<RT, NT>(fb[u], fa[u], acc);
+    s += V;
+  };
+  while (s + U <= whole) batch(std::integral_constant<int, U>{});
+  // what is left in halves: each batch is one round trip to memory
+  if (U > 4 && s + 4 <= whole) batch(std::integral_constant<int, 4>{});
+  if (U > 2 && s + 2 <= whole) batch(std::integral_constant<int, 2>{});
+  if (U > 1 && s < whole) batch(std::integral_constant<int, 1>{});
+  if (s < s1) {  // the step at the end of the rows
+    const int k = s * kStep + g * P;
     u32x4 fb[NT], fa[RT];
 #pragma unroll
     for (int j = 0; j < NT; ++j) fb[j] = load_frag<T>(brow[j] + k, K - k);
