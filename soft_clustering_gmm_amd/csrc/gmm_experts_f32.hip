@@ -7,13 +7,6 @@
 namespace gmm {
 GMM_EXPERTS_TYPE(float)
 
-// Orders this wave's LDS accesses (all lanes) before its later ones.
-__device__ __forceinline__ void wave_lds_order() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
-
 struct Best {
   double s;
   int k;

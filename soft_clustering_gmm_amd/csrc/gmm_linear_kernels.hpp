@@ -40,8 +40,7 @@ __device__ __forceinline__ lds_ptr to_lds(const void* p) {
 // (m) as its second, so a lane's results are 4 consecutive n of one m; the
 // 16 instruction rows of tile i of a wave's NI tiles stand for
 //   n = (r / 4) * 4 NI + 4 i + r % 4,
-// so over the NI tiles a lane owns 4 NI consecutive n and stores whole
-// 16-byte pieces straight from its registers.
+// so over the NI tiles a lane owns 4 NI consecutive n.
 //
 // LDS layouts, in 16-byte chunks, the chunk's place XORed with a key of its
 // row so that the fragment reads of a wave spread over the banks:
@@ -256,9 +255,16 @@ __device__ __forceinline__ void store_row(void* p, int64_t at, int n, bool is_f3
     store_as<T, W>(static_cast<T*>(p) + at, n, v);
 }
 
+// The residual of W consecutive n of one row, where there is one.
+template <typename T, int W>
+__device__ __forceinline__ void load_residual(const ProductArgs& p, int64_t m, int n, float* res) {
+  if (p.residual) load_row<T, W>(p.residual, m * p.N + n, p.N - n, p.c_f32, res);
+}
+
 // z + bias -> pre, act(.) + residual -> C for W consecutive n of one row.
 template <typename T, int ACT, int W>
-__device__ __forceinline__ void finish_row(const ProductArgs& p, int64_t m, int n, float* z, const float* bias) {
+__device__ __forceinline__ void finish_row(const ProductArgs& p, int64_t m, int n, float* z, const float* bias,
+                                           const float* res) {
   const int64_t at = m * p.N + n;
   const int left = p.N - n;
 #pragma unroll
@@ -266,12 +272,9 @@ __device__ __forceinline__ void finish_row(const ProductArgs& p, int64_t m, int 
   if (p.pre) store_as<float, W>(p.pre + at, left, z);
 #pragma unroll
   for (int i = 0; i < W; ++i) z[i] = act_value<ACT>(z[i]);
-  if (p.residual) {
-    float r[W];
-    load_row<T, W>(p.residual, at, left, p.c_f32, r);
+  if (p.residual)
 #pragma unroll
-    for (int i = 0; i < W; ++i) z[i] += r[i];
-  }
+    for (int i = 0; i < W; ++i) z[i] += res[i];
   store_row<T, W>(p.C, at, left, p.c_f32, z);
 }
 
@@ -297,26 +300,10 @@ __device__ __forceinline__ Place tile_place(const ProductArgs& p, int bm, int bn
   return at;
 }
 
-// One row of a lane's results (4 NI consecutive n) to C or the partial sums.
-template <typename T, int ACT, int NI>
-__device__ __forceinline__ void finish_tile(const ProductArgs& p, int part, int64_t m, int n, const f32x4* acc,
-                                            const float* bias) {
-  constexpr int W = 4 * NI;
-  float z[W];
-#pragma unroll
-  for (int j = 0; j < NI; ++j)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) z[4 * j + q] = acc[j][q];
-  if (p.splits == 1)
-    finish_row<T, ACT, W>(p, m, n, z, bias);
-  else
-    store_as<float, W>(p.partial + ((int64_t)part * p.M + m) * p.N + n, p.N - n, z);
-}
-
 template <typename T, int BM, int BN, int WM, int WN, bool AS, bool BS, int ACT>
 __global__ void __launch_bounds__(64 * WM * WN, 2)
 product_kernel(const ProductArgs p) {
-  constexpr int NW = WM * WN, HM = BM / 2, TM = HM / WM, TN = BN / WN, MI = TM / 16, NI = TN / 16, W = 4 * NI;
+  constexpr int NW = WM * WN, HM = BM / 2, TM = HM / WM, TN = BN / WN, MI = TM / 16, NI = TN / 16;
   using OA = Operand<T, HM, NW, AS, false, 1>;
   using OB = Operand<T, BN, NW, BS, true, NI>;
   constexpr int kSlot = 2 * OA::kBytes + OB::kBytes, kPending = 2 * OA::kLoads + OB::kLoads;
@@ -398,18 +385,53 @@ product_kernel(const ProductArgs p) {
     read_b(s + 1, 0);
     multiply(1, 1, std::true_type{});
   }
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // nothing arrives in LDS after the block's end
+  step_barrier<0>(lds);  // nobody reads the slots, and nothing arrives in them any more
 
-  const int n = at.n0 + wn * TN + (lane >> 4) * W;
-  if (n >= p.N) return;
-  float bias[W];
+  // The results go through LDS, 16 rows of m at a time in memory of the wave's
+  // own, so that 16 (TN / 4) neighbouring lanes access one row: whole lines for
+  // C, residual and pre. (Straight from the registers, 16 bytes of a row every
+  // 4 NI n, an epilogue with residual and pre took 88 us on top of 132 at 4096 x
+  // 8192 x 2048 in bfloat16.) Padded rows spread the writes over the banks.
+  constexpr int kRow = TN * 4 + 16, kChunks = TN / 4, kRows = 64 / kChunks;
+  static_assert(NW * 16 * kRow <= 2 * kSlot, "fits the slots");
+  char* mine = lds + wave * 16 * kRow;
+  const int n = at.n0 + wn * TN + lane % kChunks * 4;
+  const bool whole = p.splits == 1;
+  float bias[4] = {0.f, 0.f, 0.f, 0.f};
+  if (whole && p.bias && n < p.N) load_as<T, 4>(static_cast<const T*>(p.bias) + n, p.N - n, bias);
+  // The next 16 rows' residual is on its way while these are finished: C may be
+  // the residual, so the compiler keeps a load behind the stores before it.
+  constexpr int Q = 16 / kRows;
+  float res[2][Q][4];
+  auto row_of = [&](int i, int q) {
+    return at.m0 + i / MI * HM + wm * TM + 16 * (i % MI) + q * kRows + lane / kChunks;
+  };
+  auto fetch = [&](int i) {
 #pragma unroll
-  for (int i = 0; i < W; ++i) bias[i] = 0.f;
-  if (p.splits == 1 && p.bias) load_as<T, W>(static_cast<const T*>(p.bias) + n, p.N - n, bias);
+    for (int q = 0; q < Q; ++q)
+      if (whole && row_of(i, q) < p.M && n < p.N) load_residual<T, 4>(p, row_of(i, q), n, res[i & 1][q]);
+  };
+  fetch(0);
 #pragma unroll
   for (int i = 0; i < 2 * MI; ++i) {
-    const int64_t m = at.m0 + i / MI * HM + wm * TM + 16 * (i % MI) + (lane & 15);
-    if (m < p.M) finish_tile<T, ACT, NI>(p, at.part, m, n, acc[i / MI][i % MI], bias);
+    if (i + 1 < 2 * MI) fetch(i + 1);
+#pragma unroll
+    for (int j = 0; j < NI; ++j)
+      *reinterpret_cast<f32x4*>(mine + (lane & 15) * kRow + (lane >> 4) * 16 * NI + 16 * j) = acc[i / MI][i % MI][j];
+    wave_lds_order();
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const f32x4 v = *reinterpret_cast<const f32x4*>(mine + (q * kRows + lane / kChunks) * kRow + lane % kChunks * 16);
+      const int64_t m = row_of(i, q);
+      if (m < p.M && n < p.N) {
+        float z[4] = {v[0], v[1], v[2], v[3]};
+        if (whole)
+          finish_row<T, ACT, 4>(p, m, n, z, bias, res[i & 1][q]);
+        else
+          store_as<float, 4>(p.partial + ((int64_t)at.part * p.M + m) * p.N + n, p.N - n, z);
+      }
+    }
+    wave_lds_order();
   }
 }
 
@@ -451,7 +473,9 @@ __global__ void __launch_bounds__(256) product_reduce_kernel(const ProductArgs p
       for (int k = 0; k < W; ++k)
         z[k] = (red[0][mine][k] + red[1][mine][k]) + (red[2][mine][k] + red[3][mine][k]);
       if (p.bias) load_as<T, W>(static_cast<const T*>(p.bias) + col, W, bias);
-      finish_row<T, ACT, W>(p, row, col, z, bias);
+      float res[W];
+      load_residual<T, W>(p, row, col, res);
+      finish_row<T, ACT, W>(p, row, col, z, bias, res);
     }
   }
 }
@@ -490,7 +514,9 @@ __global__ void __launch_bounds__(64 * NW) few_kernel(const FewArgs p) {
     e.pre = p.pre;
     e.c_f32 = p.c_f32;
     float bias = p.bias ? (float)static_cast<const T*>(p.bias)[n0 + n] : 0.f;
-    finish_row<T, ACT, 1>(e, m, n0 + n, &z, &bias);
+    float res;
+    load_residual<T, 1>(e, m, n0 + n, &res);
+    finish_row<T, ACT, 1>(e, m, n0 + n, &z, &bias, &res);
   }
 }
 

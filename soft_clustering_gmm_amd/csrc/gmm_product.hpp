@@ -136,6 +136,13 @@ __device__ __forceinline__ float act_slope(float z) {
   return 1.f;
 }
 
+// Orders this wave's LDS accesses (all lanes) before its later ones.
+__device__ __forceinline__ void wave_lds_order() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // 16 bytes from an address of any alignment (the hardware's unaligned loads).
 __device__ __forceinline__ u32x4 load16(const void* p) {
   u32x4 v;
