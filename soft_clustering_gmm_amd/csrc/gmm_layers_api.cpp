@@ -191,7 +191,7 @@ static int check_linear(int64_t N, int32_t d_in, int32_t d_out, int32_t x_dtype,
 
 template <typename T>
 static hipError_t linear_forward(const T* X, int64_t N, int d_in, const T* W, int d_out, const T* bias, int act,
-                                 const void* residual, void* Y, int y_f32, float* pre, char* ws, hipStream_t s) {
+                                 const void* residual, void* Y, int y_f32, void* pre, char* ws, hipStream_t s) {
   const LinearPlan l = linear_plan(N, d_in, d_out, sizeof(T));
   if (l.few) {
     const FewArgs f{X, W, (int)N, d_out, d_in, bias, residual, Y, pre, y_f32};
@@ -220,7 +220,7 @@ static hipError_t linear_forward(const T* X, int64_t N, int d_in, const T* W, in
     const size_t at = (size_t)r * d_out * ey;
     p.C = static_cast<char*>(Y) + at;
     p.residual = residual ? static_cast<const char*>(residual) + at : nullptr;
-    p.pre = pre ? pre + r * d_out : nullptr;
+    p.pre = pre ? static_cast<char*>(pre) + at : nullptr;
     e = run_product<T>(r == 0 ? l.cut : choose_cut(rows, d_out, d_in, sizeof(T)), false, false, act, p, s);
     if (e != hipSuccess) return e;
   }
@@ -229,7 +229,7 @@ static hipError_t linear_forward(const T* X, int64_t N, int d_in, const T* W, in
 
 template <typename T>
 static hipError_t linear_gradients(const void* dY, int y_f32, const T* X, int64_t N, int d_in, const T* W, int d_out,
-                                   const float* pre, int act, T* dX, T* dW, T* db, char* ws, hipStream_t s) {
+                                   const void* pre, int act, T* dX, T* dW, T* db, char* ws, hipStream_t s) {
   const bool plain = act == GMM_ACT_NONE && (y_f32 != 0) == (sizeof(T) == 4) && aligned16(dY);
   const BackwardPlan b = backward_plan(N, d_in, d_out, sizeof(T), plain, dX != nullptr, dW != nullptr, db != nullptr);
   T* z = reinterpret_cast<T*>(ws + b.o_z);
@@ -351,7 +351,7 @@ size_t gmm_linear_workspace_bytes(int64_t N, int32_t d_in, int32_t d_out, int32_
 }
 
 int gmm_linear(const void* X, int32_t x_dtype, int64_t N, int32_t d_in, const void* W, int32_t d_out,
-               const void* bias, int32_t act, const void* residual, void* Y, int32_t y_dtype, float* pre,
+               const void* bias, int32_t act, const void* residual, void* Y, int32_t y_dtype, void* pre,
                void* workspace, size_t ws_bytes, void* stream) {
   int st = check_linear(N, d_in, d_out, x_dtype, y_dtype, act);
   if (st) return st;
@@ -369,7 +369,7 @@ int gmm_linear(const void* X, int32_t x_dtype, int64_t N, int32_t d_in, const vo
 }
 
 int gmm_linear_backward(const void* dY, int32_t y_dtype, const void* X, int32_t x_dtype, int64_t N, int32_t d_in,
-                        const void* W, int32_t d_out, const float* pre, int32_t act, void* dX, void* dW, void* db,
+                        const void* W, int32_t d_out, const void* pre, int32_t act, void* dX, void* dW, void* db,
                         void* workspace, size_t ws_bytes, void* stream) {
   int st = check_linear(N, d_in, d_out, x_dtype, y_dtype, act);
   if (st) return st;

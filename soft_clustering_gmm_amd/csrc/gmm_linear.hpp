@@ -24,8 +24,8 @@ struct ProductArgs {
   const void* bias;      // element type of the operands
   const void* residual;  // type of C
   void* C;
-  float* pre;
-  int c_f32;             // C and residual are float (else the operands' type)
+  void* pre;             // type of C
+  int c_f32;             // C, residual and pre are float (else the operands' type)
   float* partial;        // [splits][M][N]
 };
 
@@ -47,7 +47,7 @@ struct FewArgs {
   const void* bias;
   const void* residual;
   void* C;
-  float* pre;
+  void* pre;
   int c_f32;
 };
 
@@ -74,7 +74,7 @@ hipError_t launch_reduce(int act, const ProductArgs& p, hipStream_t s);
 // behind), and per-chunk column sums of the unrounded dZ in db_part; dZ or
 // db_part may be null. The two copies run in the same launch.
 template <typename T>
-hipError_t launch_dz(int act, const void* dY, const float* pre, int y_f32, int64_t rows, int cols, T* dZ, int64_t ldz,
+hipError_t launch_dz(int act, const void* dY, const void* pre, int y_f32, int64_t rows, int cols, T* dZ, int64_t ldz,
                      float* db_part, int64_t chunk_rows, const PadJob& px, const PadJob& pw, hipStream_t s);
 template <typename T>
 hipError_t launch_db(const float* db_part, int64_t chunks, int cols, T* db, hipStream_t s);

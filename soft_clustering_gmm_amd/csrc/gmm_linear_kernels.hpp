@@ -269,7 +269,7 @@ __device__ __forceinline__ void finish_row(const ProductArgs& p, int64_t m, int 
   const int left = p.N - n;
 #pragma unroll
   for (int i = 0; i < W; ++i) z[i] += bias[i];
-  if (p.pre) store_as<float, W>(p.pre + at, left, z);
+  if (p.pre) store_row<T, W>(p.pre, at, left, p.c_f32, z);
 #pragma unroll
   for (int i = 0; i < W; ++i) z[i] = act_value<ACT>(z[i]);
   if (p.residual)
@@ -557,7 +557,7 @@ __global__ void __launch_bounds__(256) zero_kernel(T* p, int64_t n) {
 // blocks copy X and W to padded rows, where the products need that.
 template <typename T, int ACT, int V, int CG>
 __global__ void __launch_bounds__(256)
-dz_kernel(const void* __restrict__ dY, const float* __restrict__ pre, int y_f32, int64_t rows, int cols,
+dz_kernel(const void* __restrict__ dY, const void* __restrict__ pre, int y_f32, int64_t rows, int cols,
           T* __restrict__ dZ, int64_t ldz, float* __restrict__ db_part, int64_t chunk_rows, int across, int pads,
           const PadJob px, const PadJob pw) {
   constexpr int RG = 256 / CG;
@@ -584,7 +584,7 @@ dz_kernel(const void* __restrict__ dY, const float* __restrict__ pre, int y_f32,
       for (int u = 0; u < U; ++u)
         if (r + u * RG < r1) {
           load_row<T, V>(dY, (r + u * RG) * cols + c, left, y_f32, v[u]);
-          if (ACT != GMM_ACT_NONE) load_as<float, V>(pre + (r + u * RG) * cols + c, left, z[u]);
+          if (ACT != GMM_ACT_NONE) load_row<T, V>(pre, (r + u * RG) * cols + c, left, y_f32, z[u]);
         }
 #pragma unroll
       for (int u = 0; u < U; ++u)
@@ -716,7 +716,7 @@ hipError_t launch_reduce(int act, const ProductArgs& p, hipStream_t s) {
 }
 
 template <typename T, int ACT, int V>
-static void launch_dz_columns(const void* dY, const float* pre, int y_f32, int64_t rows, int cols, T* dZ, int64_t ldz,
+static void launch_dz_columns(const void* dY, const void* pre, int y_f32, int64_t rows, int cols, T* dZ, int64_t ldz,
                               float* db_part, int64_t chunk_rows, const PadJob& px, const PadJob& pw, hipStream_t s) {
   const int64_t groups = (cols + V - 1) / V, chunks = (rows + chunk_rows - 1) / chunk_rows;
   const int64_t pieces = (px.rows * px.ld + pw.rows * pw.ld) / Frag<T>::kPer;
@@ -732,7 +732,7 @@ static void launch_dz_columns(const void* dY, const float* pre, int y_f32, int64
 }
 
 template <typename T>
-hipError_t launch_dz(int act, const void* dY, const float* pre, int y_f32, int64_t rows, int cols, T* dZ, int64_t ldz,
+hipError_t launch_dz(int act, const void* dY, const void* pre, int y_f32, int64_t rows, int cols, T* dZ, int64_t ldz,
                      float* db_part, int64_t chunk_rows, const PadJob& px, const PadJob& pw, hipStream_t s) {
   return with_act(act, [&](auto a) {
     launch_dz_columns<T, decltype(a)::value, Frag<T>::kPer>(dY, pre, y_f32, rows, cols, dZ, ldz, db_part, chunk_rows,
@@ -753,7 +753,7 @@ hipError_t launch_db(const float* db_part, int64_t chunks, int cols, T* db, hipS
   template hipError_t launch_pad<T>(const PadJob&, const PadJob&, hipStream_t);                                    \
   template hipError_t launch_zero<T>(T*, int64_t, hipStream_t);                                                    \
   template hipError_t launch_reduce<T>(int, const ProductArgs&, hipStream_t);                                      \
-  template hipError_t launch_dz<T>(int, const void*, const float*, int, int64_t, int, T*, int64_t, float*, int64_t, \
+  template hipError_t launch_dz<T>(int, const void*, const void*, int, int64_t, int, T*, int64_t, float*, int64_t, \
                                    const PadJob&, const PadJob&, hipStream_t);                                                                   \
   template hipError_t launch_db<T>(const float*, int64_t, int, T*, hipStream_t);
 

@@ -445,10 +445,10 @@ def linear_workspace(N: int, d_in: int, d_out: int, dtype, device, *, backward: 
 
 
 def linear(X, W, *, bias=None, act: int = ACT_NONE, residual=None, out_dtype=None, want_pre: bool = False, ws=None):
-    """Y = act(X W^T + bias) + residual; returns (Y, pre), pre = X W^T + bias (float32) or None.
+    """Y = act(X W^T + bias) + residual; returns (Y, pre), pre = X W^T + bias or None.
 
-    X N x d_in, W d_out x d_in and bias d_out share one type; Y and residual are N x d_out of out_dtype (X's type,
-    the default, or float32)."""
+    X N x d_in, W d_out x d_in and bias d_out share one type; Y, residual and pre are N x d_out of out_dtype
+    (X's type, the default, or float32)."""
     N, d_in = _matrix(X, "X")
     dev, t = X.device, X.dtype
     if dev.index != torch.cuda.current_device():
@@ -464,7 +464,7 @@ def linear(X, W, *, bias=None, act: int = ACT_NONE, residual=None, out_dtype=Non
         raise ValueError(f"out_dtype must be {t} or float32, got {out_dtype}")
     _optional(residual, "residual", out_dtype, (N, d_out), dev)
     Y = torch.empty(N, d_out, dtype=out_dtype, device=dev)
-    pre = torch.empty(N, d_out, dtype=torch.float32, device=dev) if want_pre else None
+    pre = torch.empty(N, d_out, dtype=out_dtype, device=dev) if want_pre else None
     if ws is None and _linear_bytes(N, d_in, d_out, xt, 0) != WORKSPACE_NONE:
         ws = linear_workspace(N, d_in, d_out, t, dev)
     _check("gmm_linear", lib().gmm_linear(
@@ -492,7 +492,7 @@ def linear_backward(dY, X, W, *, pre=None, act: int = ACT_NONE, want_dx: bool = 
     _need(dY, "dY", yt, (N, d_out), dev)
     if pre is None and act != ACT_NONE:
         raise ValueError("pre is needed with an activation")
-    _optional(pre, "pre", torch.float32, (N, d_out), dev)
+    _optional(pre, "pre", yt, (N, d_out), dev)
     dX = torch.empty_like(X) if want_dx else None
     dW = torch.empty_like(W) if want_dw else None
     db = torch.empty(d_out, dtype=t, device=dev) if want_db else None

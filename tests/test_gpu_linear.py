@@ -49,7 +49,7 @@ def test_forward(G, i, dtype):
         X, W, b, R, _ = inputs(N, d_in, d_out, TYPES[dtype], out, i % 3 != 1, i % 2 == 0, seed=i)
         Y, pre = G.linear(X, W, bias=b, act=act_of(G, name), residual=R, out_dtype=out, want_pre=True)
         y, z, zb = oracle.linear(X, W, b, name, R)
-        oracle.check(pre, z, zb + oracle.rounding(z, torch.float32), f"pre {name}")
+        oracle.check(pre, z, zb + oracle.rounding(z, out), f"pre {name}")
         oracle.check(Y, y, oracle.y_bound(y, z, zb, name, out), f"y {name}")
         again, none = G.linear(X, W, bias=b, act=act_of(G, name), residual=R, out_dtype=out)
         assert none is None and torch.equal(again, Y)  # the same with and without pre, and every time
