@@ -1,6 +1,7 @@
 /*
  * gmm.h — C-ABI of libgmm_mi355x.so: the fused Gaussian-mixture EM E-step for
- * MI355X (gfx950), with its M-step, EM loop and top-2 assignment.
+ * MI355X (gfx950), with its M-step, EM loop and top-2 assignment, and the
+ * learned products around it: a linear layer and a layer of experts.
  *
  * The operation (pages: "Turbo-GMM: FlashAttention-Inspired GPU-Accelerated
  * Gaussian Mixture Model", abstract; "Flash-GMM: a memory-efficient kernel for
@@ -46,7 +47,7 @@ extern "C" {
 
 enum gmm_status {
   GMM_OK = 0,
-  GMM_EINVAL = -1,        /* null pointer, negative size, bad dtype or regime */
+  GMM_EINVAL = -1,        /* null pointer, negative size, bad dtype, regime or activation, misaligned matrix */
   GMM_EUNSUPPORTED = -2,  /* shape beyond the limits above, or regime not possible */
   GMM_EWORKSPACE = -3,    /* workspace NULL, too small or misaligned */
   GMM_EHIP = -4,          /* a HIP launch failed (see hipGetLastError) */

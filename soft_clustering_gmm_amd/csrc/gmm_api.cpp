@@ -301,10 +301,11 @@ int gmm_version(void) { return 10000; }
 const char* gmm_error_string(int code) {
   switch (code) {
     case GMM_OK: return "ok";
-    case GMM_EINVAL: return "invalid argument (null pointer, negative size, bad dtype or regime)";
+    case GMM_EINVAL: return "invalid argument (null pointer, negative size, bad dtype, regime or activation, misaligned matrix)";
     case GMM_EUNSUPPORTED:
-      return "unsupported shape or regime (1<=d<=128, 1<=K<=65536; single sweep needs K<=256, small-K K<=16 and d<=64)";
-    case GMM_EWORKSPACE: return "workspace missing, misaligned (256 B) or smaller than gmm_workspace_bytes()";
+      return "unsupported shape or regime (1<=d<=128, 1<=K<=65536; single sweep needs K<=256, small-K K<=16 and d<=64; "
+             "layers: widths<=65536, linear N<=2^30, experts N<=128 and top<=8)";
+    case GMM_EWORKSPACE: return "workspace missing, misaligned (256 B) or smaller than the call's workspace query says";
     case GMM_EHIP: return "HIP launch failed";
     case GMM_ESCRATCH:
       return "the allocation-free E-step needs more scratch for this shape than its static array holds "

@@ -388,28 +388,31 @@ product_kernel(const ProductArgs p) {
   step_barrier<0>(lds);  // nobody reads the slots, and nothing arrives in them any more
 
   // The results go through LDS, 16 rows of m at a time in memory of the wave's
-  // own, so that 16 (TN / 4) neighbouring lanes access one row: whole lines for
-  // C, residual and pre. (Straight from the registers, 16 bytes of a row every
-  // 4 NI n, an epilogue with residual and pre took 88 us on top of 132 at 4096 x
-  // 8192 x 2048 in bfloat16.) Padded rows spread the writes over the banks.
-  constexpr int kRow = TN * 4 + 16, kChunks = TN / 4, kRows = 64 / kChunks;
+  // own, so that neighbouring lanes access one row: whole lines for C, residual
+  // and pre. Straight from the registers, 4 NI n of a row per lane, the product
+  // to 96 float columns (262144 x 1024 rows) took 152 us, so 141; a bfloat16 one
+  // with no residual is 2% slower this way (8192 x 16384: 921 against 940).
+  // Padded rows spread the writes over the banks.
+  constexpr int W = Frag<T>::kPer;  // n of a lane: 16 bytes of the operands' type
+  constexpr int kRow = TN * 4 + 16, kChunks = TN / W, kRows = 64 / kChunks, Q = 16 / kRows;
   static_assert(NW * 16 * kRow <= 2 * kSlot, "fits the slots");
   char* mine = lds + wave * 16 * kRow;
-  const int n = at.n0 + wn * TN + lane % kChunks * 4;
+  const int n = at.n0 + wn * TN + lane % kChunks * W;
   const bool whole = p.splits == 1;
-  float bias[4] = {0.f, 0.f, 0.f, 0.f};
-  if (whole && p.bias && n < p.N) load_as<T, 4>(static_cast<const T*>(p.bias) + n, p.N - n, bias);
+  float bias[W];
+#pragma unroll
+  for (int i = 0; i < W; ++i) bias[i] = 0.f;
+  if (whole && p.bias && n < p.N) load_as<T, W>(static_cast<const T*>(p.bias) + n, p.N - n, bias);
   // The next 16 rows' residual is on its way while these are finished: C may be
   // the residual, so the compiler keeps a load behind the stores before it.
-  constexpr int Q = 16 / kRows;
-  float res[2][Q][4];
+  float res[2][Q][W];
   auto row_of = [&](int i, int q) {
     return at.m0 + i / MI * HM + wm * TM + 16 * (i % MI) + q * kRows + lane / kChunks;
   };
   auto fetch = [&](int i) {
 #pragma unroll
     for (int q = 0; q < Q; ++q)
-      if (whole && row_of(i, q) < p.M && n < p.N) load_residual<T, 4>(p, row_of(i, q), n, res[i & 1][q]);
+      if (whole && row_of(i, q) < p.M && n < p.N) load_residual<T, W>(p, row_of(i, q), n, res[i & 1][q]);
   };
   fetch(0);
 #pragma unroll
@@ -421,14 +424,20 @@ product_kernel(const ProductArgs p) {
     wave_lds_order();
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
-      const f32x4 v = *reinterpret_cast<const f32x4*>(mine + (q * kRows + lane / kChunks) * kRow + lane % kChunks * 16);
+      float z[W];
+      const char* from = mine + (q * kRows + lane / kChunks) * kRow + lane % kChunks * W * 4;
+#pragma unroll
+      for (int k = 0; k < W; k += 4) {
+        const f32x4 v = *reinterpret_cast<const f32x4*>(from + 4 * k);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) z[k + c] = v[c];
+      }
       const int64_t m = row_of(i, q);
       if (m < p.M && n < p.N) {
-        float z[4] = {v[0], v[1], v[2], v[3]};
         if (whole)
-          finish_row<T, ACT, 4>(p, m, n, z, bias, res[i & 1][q]);
+          finish_row<T, ACT, W>(p, m, n, z, bias, res[i & 1][q]);
         else
-          store_as<float, 4>(p.partial + ((int64_t)at.part * p.M + m) * p.N + n, p.N - n, z);
+          store_as<float, W>(p.partial + ((int64_t)at.part * p.M + m) * p.N + n, p.N - n, z);
       }
     }
     wave_lds_order();

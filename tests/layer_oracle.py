@@ -1,4 +1,5 @@
-"""Plain 64-bit forms of the linear layer, its gradients and the layer of experts, on the CPU, with the error
+"""Plain 64-bit forms of the linear layer, its gradients and the layer of experts (on the CPU, or where a test of
+large shapes puts ON), with the error
 bounds that the library's arithmetic allows. Shares no code with the library."""
 import math
 
@@ -12,8 +13,11 @@ ACTS = ("none", "relu", "gelu", "silu")
 FUNCTION = 2.0 ** -20
 
 
+ON = "cpu"
+
+
 def wide(t):
-    return None if t is None else t.detach().cpu().double()
+    return None if t is None else t.detach().to(ON).double()
 
 
 def act(z, name):

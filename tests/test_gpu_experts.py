@@ -182,6 +182,51 @@ def test_captured_layer(G):
         torch.cuda.synchronize()
 
 
+def test_two_graphs_share_a_workspace(G):
+    """Two captured layers of different sizes on one workspace, replayed in turn: each call sets up what it reads."""
+    sets = [layer(T, 128, 64, K, 24, torch.float16, True, True, True, seed=T) for T, K in ((5, 9), (33, 4))]
+    ws = torch.empty(max(G.expert_workspace(T, 128, K, 64, 24, 2, torch.float16, "cuda").numel()
+                         for T, K in ((5, 9), (33, 4))), dtype=torch.uint8, device="cuda")
+    ws.fill_(255)
+    call = [lambda s=s, o=o: G.expert_layer(*[s[k] for k in ("X", "P", "mu", "var", "logw", "W1", "W2")], ws=ws, **o)
+            for s, o in sets]
+    want = [[t.clone() for t in c()] for c in call]
+    torch.cuda.synchronize()
+    graphs, got = [], []
+    for c in call:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got.append(c())
+        graphs.append(g)
+    for _ in range(3):
+        for g, a, b in zip(graphs, got, want):
+            g.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_weights_past_32_bit_offsets(G):
+    """300 experts of 2 x 1800 x 4096 and 4096 x 1800: the last one's weights lie past 2^31 elements."""
+    K, F, D = 300, 1800, 4096
+    W1 = torch.zeros(K, 2 * F, D, dtype=torch.bfloat16, device="cuda")
+    W2 = torch.zeros(K, D, F, dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(0)
+    for k in (0, K - 1):
+        W1[k].normal_(generator=g).mul_(D ** -0.5)
+        W2[k].normal_(generator=g).mul_(F ** -0.5)
+    X = torch.randn(3, D, generator=g, device="cuda").bfloat16()
+    idx = torch.tensor([[K - 1, 0], [K - 1, -1], [7, K - 1]], dtype=torch.int32, device="cuda")
+    wts = torch.tensor([[0.75, 0.25], [1.0, 0.0], [0.5, 0.5]], device="cuda")
+    for top in (2, 1):  # the gathering product, and the one by expert (more picks)
+        i, w, x = (idx, wts, X) if top == 2 else (idx.repeat(4, 1), wts.repeat(4, 1), X.repeat(4, 1))
+        y = G.expert_rows(x.contiguous(), i.contiguous(), w.contiguous(), W1, W2)
+        keep = torch.tensor([0, 7, K - 1])
+        small = {0: 0, 7: 1, K - 1: 2, -1: -1}
+        j = torch.tensor([[small[int(v)] for v in r] for r in i.cpu()])
+        y64, bound = oracle.experts(x, j, w, W1[keep], None, W2[keep], None, "silu", True, None)
+        oracle.check(y, y64, bound, "y")
+
+
 def test_refusals(G):
     s, opt = layer(4, 64, 40, 6, 12, torch.float16, True, True, True, seed=0)
     args = [s[k] for k in ("P", "mu", "var", "logw", "W1", "W2")]

@@ -74,6 +74,67 @@ def test_backward(G, i, dtype):
     assert two[0] is None and torch.equal(two[1], dW) and torch.equal(two[2], db)
 
 
+# Sizes whose products take the 256-row and the 128-row tiles, each a little short of whole tiles, with rows of whole
+# 16-byte pieces and without
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N,d_in,d_out", [(8190, 4088, 4090), (4094, 2041, 2040), (4090, 1016, 8190)])
+def test_large_tiles(G, monkeypatch, N, d_in, d_out, dtype):
+    monkeypatch.setattr(oracle, "ON", "cuda")
+    t = TYPES[dtype]
+    X, W, b, R, dY = inputs(N, d_in, d_out, t, t, True, True, seed=N)
+    Y, pre = G.linear(X, W, bias=b, act=G.ACT_SILU, residual=R, want_pre=True)
+    y, z, zb = oracle.linear(X, W, b, "silu", R)
+    oracle.check(pre, z, zb + oracle.rounding(z, t), "pre")
+    oracle.check(Y, y, oracle.y_bound(y, z, zb, "silu", t), "y")
+    del y, z, zb
+    got = G.linear_backward(dY, X, W, pre=pre, act=G.ACT_SILU)
+    want, bounds = oracle.gradients(dY, X, W, pre, "silu")
+    for g, w, bd, what in zip(got, want, bounds, ("dx", "dw", "db")):
+        oracle.check(g, w, bd + oracle.rounding(w.abs() + bd, t), what)
+        # the bounds are those of the worst signs; the 2-norm stays near the roundings': dZ's and the output's
+        off = float((g.double() - w).norm() / w.norm())
+        assert off <= (1e-5 if dtype == "f32" else 2 * oracle.EPS[t] / 2), (what, off)
+
+
+def test_more_rows_than_a_launch_and_elements_than_32_bits(G):
+    """2^20 + 77 rows of 2080: two launches, offsets past 2^31 elements; rows at both ends and at the seam, and the
+    gradients against sums in 64 bits."""
+    N, d_in, d_out = (1 << 20) + 77, 2080, 24
+    g = torch.Generator(device="cuda").manual_seed(0)
+    X = torch.randn(N, d_in, generator=g, device="cuda", dtype=torch.float16)
+    W = torch.randn(d_out, d_in, generator=g, device="cuda", dtype=torch.float16) * d_in ** -0.5
+    dY = torch.randn(N, d_out, generator=g, device="cuda", dtype=torch.float16)
+    Y, _ = G.linear(X, W)
+    dX, dW, db = G.linear_backward(dY, X, W)
+    rows = torch.tensor([0, 1, (1 << 20) - 1, 1 << 20, N - 2, N - 1], device="cuda")
+    y, z, zb = oracle.linear(X[rows], W, None, "none", None)
+    oracle.check(Y[rows], y, oracle.y_bound(y, z, zb, "none", torch.float16), "y")
+    want, bounds = oracle.gradients(dY[rows], X[rows], W, None, "none")
+    oracle.check(dX[rows], want[0], bounds[0] + oracle.rounding(want[0].abs() + bounds[0], torch.float16), "dx")
+    w64 = torch.zeros(d_out, d_in, dtype=torch.float64, device="cuda")
+    for r in range(0, N, 1 << 17):
+        w64 += torch.mm(dY[r:r + (1 << 17)].double().t().contiguous(), X[r:r + (1 << 17)].double())
+    # float sums of 2^20 terms of either sign: far below the output's own rounding of half a step
+    assert float((dW.double() - w64).norm() / w64.norm()) <= oracle.EPS[torch.float16] / 2
+    b64 = dY.double().sum(0)
+    assert float((db.double() - b64).norm() / b64.norm()) <= oracle.EPS[torch.float16] / 2
+
+
+def test_two_streams_at_once(G):
+    """Calls that overlap on two streams, each with its own workspace."""
+    sets = [inputs(700, 1030, 260, torch.bfloat16, torch.bfloat16, True, True, seed=s) for s in (1, 2)]
+    alone = [G.linear(X, W, bias=b, act=G.ACT_GELU, residual=R)[0] for X, W, b, R, _ in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = []
+        for s, (X, W, b, R, _) in zip(streams, sets):
+            with torch.cuda.stream(s):
+                got.append(G.linear(X, W, bias=b, act=G.ACT_GELU, residual=R)[0])
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, c) for a, c in zip(alone, got))
+
+
 @pytest.mark.parametrize("name", oracle.ACTS)
 def test_gradients_against_differences(G, name):
     """sum(Y dY) by central differences along random directions of X, W and bias, h = 2^-5. The difference's own
