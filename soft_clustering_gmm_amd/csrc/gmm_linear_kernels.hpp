@@ -659,6 +659,10 @@ static void launch_tile(int variant, const ProductArgs& p, hipStream_t s) {
   const dim3 grid(p.tiles_m * p.tiles_n * p.splits);
   if (variant == kTile256)
     product_kernel<T, 256, 256, 2, 4, AS, BS, ACT><<<grid, 512, 0, s>>>(p);
+  else if (variant == kTile128 && sizeof(T) == 4)
+    // single precision is matrix-bound, and one block on a CU is common: two
+    // waves a SIMD (4096 x 1024 x 1024 with its epilogue: 82.4 us against 83.8)
+    product_kernel<T, 128, 128, 2, 4, AS, BS, ACT><<<grid, 512, 0, s>>>(p);
   else if (variant == kTile128)
     product_kernel<T, 128, 128, 2, 2, AS, BS, ACT><<<grid, 256, 0, s>>>(p);
   else
