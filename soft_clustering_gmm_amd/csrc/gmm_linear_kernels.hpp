@@ -37,10 +37,7 @@ __device__ __forceinline__ lds_ptr to_lds(const void* p) {
 // instead of 8 the loads took 546.
 //
 // The matrix instruction gets B's rows (n) as its first operand and A's rows
-// (m) as its second, so a lane's results are 4 consecutive n of one m; the
-// 16 instruction rows of tile i of a wave's NI tiles stand for
-//   n = (r / 4) * 4 NI + 4 i + r % 4,
-// so over the NI tiles a lane owns 4 NI consecutive n.
+// (m) as its second, so a lane's results are 4 consecutive n of one m.
 //
 // LDS layouts, in 16-byte chunks, the chunk's place XORed with a key of its
 // row so that the fragment reads of a wave spread over the banks:
@@ -69,21 +66,7 @@ __device__ __forceinline__ void step_barrier(const void* lds) {
   asm volatile("s_waitcnt vmcnt(%1) lgkmcnt(0)\n\ts_barrier" : : "v"(to_lds(lds)), "n"(PENDING) : "memory");
 }
 
-template <int NI>
-__device__ __forceinline__ int key_rows_perm(int n) {  // rows in the order above
-  return (n & 3) | (((n / (4 * NI)) & 1) << 2);
-}
-__device__ __forceinline__ int key_rows(int r) { return r & 7; }  // rows in natural order
-// k-strided tiles of 2-byte elements: the transposing read takes, per 16
-// lanes, 4 values of k x 16 rows. Natural rows: 32 bytes of each k, moved
-// apart by the key. Permuted rows: 8 bytes every 4 NI elements of each k.
-__device__ __forceinline__ int key_k(int k) { return (k & 3) << 1; }
-template <int NI>
-__device__ __forceinline__ int key_k_perm(int k) {
-  return NI == 4 ? (k & 1) | ((k & 2) << 2) : (k & 1) << 2;
-}
-
-template <typename T, int BR, int NWAVES, bool STRIDED, bool PERM, int NI>
+template <typename T, int BR, int NWAVES, bool STRIDED>
 struct Operand {
   static constexpr int kPer = Frag<T>::kPer;
   static constexpr int kStep = kStepBytes / (int)sizeof(T);  // k per step
@@ -98,9 +81,15 @@ struct Operand {
   uint32_t off[kLoads];  // byte offset of this lane's chunk from base
   static constexpr uint32_t kNowhere = 0x80000000u;  // beyond any buffer: zeros
 
+  // Key of a k-strided tile's k. A k is 64, 128, 256 or 512 bytes; what 32 lanes
+  // read at once should be 256 different bytes of the banks' 256.
+  // 2-byte elements (transposing reads): 32 bytes of each of k = 0..3 and 8..11.
+  // 4-byte elements: 64 bytes of each of k = 0, 4, 8, 12.
   static __device__ __forceinline__ int key(int k) {
-    if (kRowChunks == 4) return (k & 2);  // 64-byte rows: four of k are 256 bytes by themselves
-    return PERM ? key_k_perm<NI>(k) : key_k(k);
+    if (sizeof(T) == 4) return kRowChunks >= 16 ? (k & 12) : (k & 4);
+    if (kRowChunks >= 16) return ((k & 3) << 1) | (k & 8);
+    if (kRowChunks == 8) return (k & 2) | ((k & 8) >> 1);
+    return (k & 8) >> 2;
   }
 
   // First k, within the step, of the chunk that this lane brings in load j.
@@ -108,7 +97,7 @@ struct Operand {
     const int ch = (wave * kLoads + j) * 64 + lane;
     if (STRIDED) return ch / kRowChunks;
     const int r = ch / 8;
-    return ((ch % 8) ^ (PERM ? key_rows_perm<NI>(r) : key_rows(r))) * kPer;
+    return ((ch % 8) ^ (r & 7)) * kPer;
   }
 
   // The same for its first row (k-strided).
@@ -167,12 +156,12 @@ struct Operand {
   static __device__ __forceinline__ u32x4 frag(const char* lds, int w0, int i, int kk, int lane) {
     const int r = lane & 15, g = lane >> 4;
     if (!STRIDED) {
-      const int row = w0 + (PERM ? (r >> 2) * 4 * NI + 4 * i + (r & 3) : 16 * i + r);
-      const int c = (4 * kk + g) ^ (PERM ? key_rows_perm<NI>(row) : key_rows(row));
+      const int row = w0 + 16 * i + r;
+      const int c = (4 * kk + g) ^ (row & 7);
       return *reinterpret_cast<const u32x4*>(lds + row * kStepBytes + 16 * c);
     }
     if constexpr (sizeof(T) == 4) {
-      const int row = w0 + (PERM ? (r >> 2) * 4 * NI + 4 * i + (r & 3) : 16 * i + r);
+      const int row = w0 + 16 * i + r;
       u32x4 v;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -184,7 +173,7 @@ struct Operand {
     } else {
       // Two transposing reads: over 16 lanes, lane t gives the address of 4
       // consecutive rows of k = t / 4, and receives 4 consecutive k of row t.
-      const int row = w0 + (PERM ? (r & 3) * 4 * NI + 4 * i : 16 * i + 4 * (r & 3));
+      const int row = w0 + 16 * i + 4 * (r & 3);
       u32x4 v;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -304,8 +293,8 @@ template <typename T, int BM, int BN, int WM, int WN, bool AS, bool BS, int ACT>
 __global__ void __launch_bounds__(64 * WM * WN, 2)
 product_kernel(const ProductArgs p) {
   constexpr int NW = WM * WN, HM = BM / 2, TM = HM / WM, TN = BN / WN, MI = TM / 16, NI = TN / 16;
-  using OA = Operand<T, HM, NW, AS, false, 1>;
-  using OB = Operand<T, BN, NW, BS, true, NI>;
+  using OA = Operand<T, HM, NW, AS>;
+  using OB = Operand<T, BN, NW, BS>;
   constexpr int kSlot = 2 * OA::kBytes + OB::kBytes, kPending = 2 * OA::kLoads + OB::kLoads;
   __shared__ __align__(1024) char lds[2 * kSlot];
 
@@ -389,7 +378,7 @@ product_kernel(const ProductArgs p) {
 
   // The results go through LDS, 16 rows of m at a time in memory of the wave's
   // own, so that neighbouring lanes access one row: whole lines for C, residual
-  // and pre. Straight from the registers, 4 NI n of a row per lane, the product
+  // and pre. Straight from the registers, 16 n of a row per lane, the product
   // to 96 float columns (262144 x 1024 rows) took 152 us, so 141; a bfloat16 one
   // with no residual is 2% slower this way (8192 x 16384: 921 against 940).
   // Padded rows spread the writes over the banks.
@@ -420,7 +409,7 @@ product_kernel(const ProductArgs p) {
     if (i + 1 < 2 * MI) fetch(i + 1);
 #pragma unroll
     for (int j = 0; j < NI; ++j)
-      *reinterpret_cast<f32x4*>(mine + (lane & 15) * kRow + (lane >> 4) * 16 * NI + 16 * j) = acc[i / MI][i % MI][j];
+      *reinterpret_cast<f32x4*>(mine + (lane & 15) * kRow + 64 * j + (lane >> 4) * 16) = acc[i / MI][i % MI][j];
     wave_lds_order();
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
