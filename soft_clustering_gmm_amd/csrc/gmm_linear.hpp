@@ -35,9 +35,9 @@ constexpr int kTileRows[kTileVariants] = {256, 128, 64};
 constexpr int kStepBytes = 128;  // bytes of k per step and operand row
 
 // Few rows: C[m][n] of at most kFewRows rows, operands of any alignment,
-// B (the weights) streamed once (bfloat16, 8192 x 16384 weights: 16 rows 61 us
-// by this stream, 17 to 64 rows with the rows of A 4 tiles deep 82 to 146, 65
-// rows by the tiled product 57).
+// B (the weights) streamed once (bfloat16, 8192 x 16384 weights: 16 rows 49 us
+// by this stream; 17 to 64 rows, with the rows of A 4 tiles deep, 82 to 146, by
+// the tiled product 46 to 56).
 constexpr int kFewRows = 16;
 
 struct FewArgs {
