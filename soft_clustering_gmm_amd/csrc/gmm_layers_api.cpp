@@ -98,6 +98,7 @@ template <typename T>
 static hipError_t run_product(const Cut& c, bool as, bool bs, int act, ProductArgs& p, hipStream_t s) {
   set_cut(p, c);
   hipError_t e = launch_product<T>(c.variant, as, bs, act, p, s);
+  p.sum_blocks = 0;  // once
   if (e == hipSuccess && c.splits > 1) e = launch_reduce<T>(act, p, s);
   return e;
 }
@@ -243,7 +244,6 @@ static hipError_t linear_gradients(const void* dY, int y_f32, const T* X, int64_
                      s);
   else if (px.rows || pw.rows)
     e = launch_pad<T>(px, pw, s);
-  if (e == hipSuccess && db) e = launch_db<T>(part, b.chunks, d_out, db, s);
   if (e != hipSuccess) return e;
   const T* dZ = b.own_dz ? z : static_cast<const T*>(dY);
   ProductArgs p{};
@@ -251,6 +251,14 @@ static hipError_t linear_gradients(const void* dY, int y_f32, const T* X, int64_
   p.c_f32 = sizeof(T) == 4;
   p.N = d_in;
   p.ldb = b.lx;
+  if (db) {  // summed beside the first product
+    p.sums = part;
+    p.sums_out = db;
+    p.sums_rows = b.chunks;
+    p.sums_cols = d_out;
+    p.sum_blocks = (int)ceil_div(d_out, kSumCols);
+  }
+  if (!dX && !dW) return db ? launch_column_sums<T>(p, s) : hipSuccess;
   if (dX) {  // dX = dZ W
     p.B = b.pad ? ws + b.o_w : static_cast<const void*>(W);
     p.lda = b.lz;

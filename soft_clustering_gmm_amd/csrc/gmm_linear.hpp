@@ -27,7 +27,14 @@ struct ProductArgs {
   void* pre;             // type of C
   int c_f32;             // C, residual and pre are float (else the operands' type)
   float* partial;        // [splits][M][N]
+  // column sums that ride along in blocks of their own (sum_blocks of them, 0:
+  // none): sums_out[c] = sum over sums_rows rows of sums[.][c]
+  const float* sums;
+  void* sums_out;        // type of the operands
+  int64_t sums_rows;
+  int sums_cols, sum_blocks;
 };
+constexpr int kSumCols = 16;  // columns of such a block
 
 // Tile variants of the product kernel.
 enum { kTile256 = 0, kTile128 = 1, kTile64 = 2, kTileVariants = 3 };
@@ -76,7 +83,8 @@ hipError_t launch_reduce(int act, const ProductArgs& p, hipStream_t s);
 template <typename T>
 hipError_t launch_dz(int act, const void* dY, const void* pre, int y_f32, int64_t rows, int cols, T* dZ, int64_t ldz,
                      float* db_part, int64_t chunk_rows, const PadJob& px, const PadJob& pw, hipStream_t s);
+// The column sums of `p` alone.
 template <typename T>
-hipError_t launch_db(const float* db_part, int64_t chunks, int cols, T* db, hipStream_t s);
+hipError_t launch_column_sums(const ProductArgs& p, hipStream_t s);
 
 }  // namespace gmm

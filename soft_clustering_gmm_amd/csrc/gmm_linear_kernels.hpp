@@ -289,6 +289,36 @@ __device__ __forceinline__ Place tile_place(const ProductArgs& p, int bm, int bn
   return at;
 }
 
+// Column sums: kSumCols columns a block, kSumSlices rows at a time by its first
+// 256 threads, in the same order whatever kernel they ride in.
+constexpr int kSumSlices = 256 / kSumCols;
+template <typename T>
+__device__ __forceinline__ void column_sums(const ProductArgs& p, int block, float (*red)[kSumCols + 1]) {
+  const int x = threadIdx.x % kSumCols, y = threadIdx.x / kSumCols;
+  const int c = block * kSumCols + x;
+  if (y < kSumSlices) {
+    float sum = 0.f;
+    if (c < p.sums_cols) {
+#pragma unroll 8
+      for (int64_t i = y; i < p.sums_rows; i += kSumSlices) sum += p.sums[i * p.sums_cols + c];
+    }
+    red[y][x] = sum;
+  }
+  __syncthreads();
+  if (y == 0 && c < p.sums_cols) {
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kSumSlices; ++i) sum += red[i][x];
+    static_cast<T*>(p.sums_out)[c] = (T)sum;
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) column_sums_kernel(const ProductArgs p) {
+  __shared__ float red[kSumSlices][kSumCols + 1];
+  column_sums<T>(p, blockIdx.x, red);
+}
+
 template <typename T, int BM, int BN, int WM, int WN, bool AS, bool BS, int ACT>
 __global__ void __launch_bounds__(64 * WM * WN, 2)
 product_kernel(const ProductArgs p) {
@@ -300,6 +330,10 @@ product_kernel(const ProductArgs p) {
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN;
+  if ((int)blockIdx.x >= p.tiles_m * p.tiles_n * p.splits) {
+    column_sums<T>(p, blockIdx.x - p.tiles_m * p.tiles_n * p.splits, reinterpret_cast<float(*)[kSumCols + 1]>(lds));
+    return;
+  }
   const Place at = tile_place(p, BM, BN);
   const int64_t k0 = at.k0, k1 = at.k1;
 
@@ -609,30 +643,6 @@ dz_kernel(const void* __restrict__ dY, const void* __restrict__ pre, int y_f32, 
   }
 }
 
-// Column sums of the chunks' sums: 16 columns a block, 64 chunks at a time.
-template <typename T>
-__global__ void __launch_bounds__(1024) db_kernel(const float* part, int64_t chunks, int cols, T* db) {
-  constexpr int Y = 64;
-  __shared__ float red[Y][17];
-  const int x = threadIdx.x & 15, y = threadIdx.x >> 4;
-  const int c = blockIdx.x * 16 + x;
-  float sum = 0.f;
-  if (c < cols) {
-#pragma unroll 4
-    for (int64_t i = y; i < chunks; i += Y) sum += part[i * cols + c];
-  }
-  red[y][x] = sum;
-  __syncthreads();
-  if (threadIdx.x < 64) {  // a wave: 4 threads a column, 16 of the sums each
-    sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < Y / 4; ++i) sum += red[y * (Y / 4) + i][x];
-    sum += __shfl_xor(sum, 16);
-    sum += __shfl_xor(sum, 32);
-    if (y == 0 && c < cols) db[c] = (T)sum;
-  }
-}
-
 // --------------------------------------------------------------------------- launchers
 
 template <typename F>
@@ -645,7 +655,7 @@ hipError_t with_act(int act, F&& f) {
 
 template <typename T, bool AS, bool BS, int ACT>
 static void launch_tile(int variant, const ProductArgs& p, hipStream_t s) {
-  const dim3 grid(p.tiles_m * p.tiles_n * p.splits);
+  const dim3 grid(p.tiles_m * p.tiles_n * p.splits + p.sum_blocks);
   if (variant == kTile256)
     product_kernel<T, 256, 256, 2, 4, AS, BS, ACT><<<grid, 512, 0, s>>>(p);
   else if (variant == kTile128 && sizeof(T) == 4)
@@ -744,8 +754,8 @@ hipError_t launch_dz(int act, const void* dY, const void* pre, int y_f32, int64_
 }
 
 template <typename T>
-hipError_t launch_db(const float* db_part, int64_t chunks, int cols, T* db, hipStream_t s) {
-  db_kernel<T><<<(cols + 15) / 16, 1024, 0, s>>>(db_part, chunks, cols, db);
+hipError_t launch_column_sums(const ProductArgs& p, hipStream_t s) {
+  column_sums_kernel<T><<<p.sum_blocks, 256, 0, s>>>(p);
   return hipGetLastError();
 }
 
@@ -757,6 +767,6 @@ hipError_t launch_db(const float* db_part, int64_t chunks, int cols, T* db, hipS
   template hipError_t launch_reduce<T>(int, const ProductArgs&, hipStream_t);                                      \
   template hipError_t launch_dz<T>(int, const void*, const void*, int, int64_t, int, T*, int64_t, float*, int64_t, \
                                    const PadJob&, const PadJob&, hipStream_t);                                                                   \
-  template hipError_t launch_db<T>(const float*, int64_t, int, T*, hipStream_t);
+  template hipError_t launch_column_sums<T>(const ProductArgs&, hipStream_t);
 
 }  // namespace gmm

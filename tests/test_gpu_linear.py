@@ -72,6 +72,8 @@ def test_backward(G, i, dtype):
     two = G.linear_backward(dY, X, W, pre=pre, act=act_of(G, name), want_dx=False)
     assert torch.equal(one[0], dX) and one[1] is None and one[2] is None
     assert two[0] is None and torch.equal(two[1], dW) and torch.equal(two[2], db)
+    three = G.linear_backward(dY, X, W, pre=pre, act=act_of(G, name), want_dx=False, want_dw=False)
+    assert torch.equal(three[2], db)
 
 
 # Sizes whose products take the 256-row and the 128-row tiles, each a little short of whole tiles, with rows of whole
