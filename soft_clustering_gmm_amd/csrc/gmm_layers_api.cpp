@@ -97,6 +97,7 @@ static void set_cut(ProductArgs& p, const Cut& c) {
 template <typename T>
 static hipError_t run_product(const Cut& c, bool as, bool bs, int act, ProductArgs& p, hipStream_t s) {
   set_cut(p, c);
+  p.c_stream = p.M * p.N * (p.c_f32 ? 4 : (int64_t)sizeof(T)) >= kStreamBytes;
   hipError_t e = launch_product<T>(c.variant, as, bs, act, p, s);
   p.sum_blocks = 0;  // once
   if (e == hipSuccess && c.splits > 1) e = launch_reduce<T>(act, p, s);

@@ -26,6 +26,7 @@ struct ProductArgs {
   void* C;
   void* pre;             // type of C
   int c_f32;             // C, residual and pre are float (else the operands' type)
+  int c_stream;          // C is written past the caches (kStreamBytes)
   float* partial;        // [splits][M][N]
   // column sums that ride along in blocks of their own (sum_blocks of them, 0:
   // none): sums_out[c] = sum over sums_rows rows of sums[.][c]
@@ -35,6 +36,12 @@ struct ProductArgs {
   int sums_cols, sum_blocks;
 };
 constexpr int kSumCols = 16;  // columns of such a block
+
+// Outputs from this size on are written past the caches, a quarter of whose last
+// level they would fill (100 MB, the product of 262144 x 1024 rows to 96 float
+// columns: 135 us against 139; 268 MB, 8192 x 4096 to 16384: 909 against 913; a
+// training step of 2 MB outputs, which the next call finds there: 42 against 40).
+constexpr int64_t kStreamBytes = 64ll << 20;
 
 // Tile variants of the product kernel.
 enum { kTile256 = 0, kTile128 = 1, kTile64 = 2, kTileVariants = 3 };

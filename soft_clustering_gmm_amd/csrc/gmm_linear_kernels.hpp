@@ -209,7 +209,8 @@ __device__ __forceinline__ void load_as(const E* q, int n, float* out) {
   }
 }
 
-template <typename E, int W>
+// STREAM: past the caches' replacement, for what is too large to be found there.
+template <typename E, int W, bool STREAM = false>
 __device__ __forceinline__ void store_as(E* q, int n, const float* v) {
   constexpr int P = 16 / sizeof(E) < W ? 16 / sizeof(E) : W;
   if (n >= W) {
@@ -218,7 +219,14 @@ __device__ __forceinline__ void store_as(E* q, int n, const float* v) {
       E e[P];
 #pragma unroll
       for (int k = 0; k < P; ++k) e[k] = (E)v[i + k];
-      __builtin_memcpy(q + i, e, sizeof(e));
+      if constexpr (STREAM && sizeof(e) == 16) {
+        typedef u32x4 any_u32x4 __attribute__((aligned(2)));
+        u32x4 w;
+        __builtin_memcpy(&w, e, 16);
+        __builtin_nontemporal_store(w, reinterpret_cast<any_u32x4*>(q + i));
+      } else {
+        __builtin_memcpy(q + i, e, sizeof(e));
+      }
     }
   } else {
 #pragma unroll
@@ -236,12 +244,12 @@ __device__ __forceinline__ void load_row(const void* p, int64_t at, int n, bool 
     load_as<T, W>(static_cast<const T*>(p) + at, n, out);
 }
 
-template <typename T, int W>
+template <typename T, int W, bool STREAM = false>
 __device__ __forceinline__ void store_row(void* p, int64_t at, int n, bool is_f32, const float* v) {
   if (is_f32)
-    store_as<float, W>(static_cast<float*>(p) + at, n, v);
+    store_as<float, W, STREAM>(static_cast<float*>(p) + at, n, v);
   else
-    store_as<T, W>(static_cast<T*>(p) + at, n, v);
+    store_as<T, W, STREAM>(static_cast<T*>(p) + at, n, v);
 }
 
 // The residual of W consecutive n of one row, where there is one.
@@ -264,7 +272,10 @@ __device__ __forceinline__ void finish_row(const ProductArgs& p, int64_t m, int 
   if (p.residual)
 #pragma unroll
     for (int i = 0; i < W; ++i) z[i] += res[i];
-  store_row<T, W>(p.C, at, left, p.c_f32, z);
+  if (p.c_stream)
+    store_row<T, W, true>(p.C, at, left, p.c_f32, z);
+  else
+    store_row<T, W>(p.C, at, left, p.c_f32, z);
 }
 
 // A block's tile and part of the contraction. Tiles go in groups of 4 tile
@@ -545,6 +556,7 @@ __global__ void __launch_bounds__(64 * NW) few_kernel(const FewArgs p) {
     e.C = p.C;
     e.pre = p.pre;
     e.c_f32 = p.c_f32;
+    e.c_stream = 0;
     float bias = p.bias ? (float)static_cast<const T*>(p.bias)[n0 + n] : 0.f;
     float res;
     load_residual<T, 1>(e, m, n0 + n, &res);
