@@ -48,7 +48,7 @@ struct ExpertArgs {
   int32_t* row_of;      // [T * top] row of the pick at a place
   int32_t* ord;         // [T * top] which of the experts with picks the place belongs to
   float* weight;        // [T * top] combination weight of the pick at a place
-  float* scale;         // [T] largest weight of a row (1 if that is 0)
+  float* scale;         // [T] largest weight of a row, repeats added (1 if that is 0)
   int32_t* expert;      // [T * top] experts with picks, increasing
   int32_t* first;       // [T * top + 1] their first places
   int32_t* count;       // [kCounts]

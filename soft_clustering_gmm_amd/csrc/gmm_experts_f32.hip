@@ -17,6 +17,7 @@ struct ListScratch {
   int key[kMaxPicks];   // expert * kMaxPicks + number of a listed pick, INT_MAX: none
   int idx[kMaxPicks];
   float wts[kMaxPicks];
+  float sum[kMaxPicks];  // of a listed pick and its repeats
   int head[kMaxPicks + 1];  // by place: the expert of the pick, INT_MAX behind the last
   int waves[16];
 };
@@ -24,8 +25,9 @@ struct ListScratch {
 // The picks in the order of their experts (a pick's place: how many picks have
 // a lower expert, or the same and a lower number), and each expert's places.
 // A row's further picks of an expert that it has picked already add their
-// weight to the first. A thread a pick, with its expert and weight (-1 behind
-// the last); ONE: at most 64 picks, and only the first wave calls.
+// weight to the first; the row's scale is the largest of these sums, so that no
+// weight is more than 1 of it. A thread a pick, with its expert and weight (-1
+// behind the last); ONE: at most 64 picks, and only the first wave calls.
 template <bool ONE>
 __device__ __forceinline__ void expert_lists(const ExpertArgs& p, ListScratch& l, int idx, float wt) {
   static_assert(65536ll * kMaxPicks < INT_MAX, "keys fit");
@@ -52,6 +54,7 @@ __device__ __forceinline__ void expert_lists(const ExpertArgs& p, ListScratch& l
       }
   }
   l.key[i] = mine;
+  l.sum[i] = w;
   sync();
   const bool some = mine != INT_MAX;
   if (i < n) {
@@ -69,7 +72,7 @@ __device__ __forceinline__ void expert_lists(const ExpertArgs& p, ListScratch& l
   }
   if (i < p.T) {
     for (int q = i * p.top; q < (i + 1) * p.top; ++q)
-      if (l.key[q] != INT_MAX) most = fmaxf(most, fabsf(l.wts[q]));
+      if (l.key[q] != INT_MAX) most = fmaxf(most, fabsf(l.sum[q]));
     p.scale[i] = most > 0.f ? most : 1.f;
   }
   sync();
