@@ -200,9 +200,10 @@ __global__ void __launch_bounds__(256) expert_combine_kernel(const ExpertArgs p)
 // columns of the matrix instruction are the rows of the call, and a block runs
 // `cols` columns of Y (at most 16; fewer where that fills the chip) through all
 // experts with picks, one long contraction over (expert, k) that its waves
-// split evenly. Column t of an expert that row t did not pick is zero; the
-// weights are in h already, as parts of the row's largest, which stands before
-// the whole sum.
+// split evenly. Every expert's part is summed by itself and added only in the
+// columns of the rows that picked it: zeros in the other columns would not keep
+// out what is not a number in its weights. The weights are in h already, as
+// parts of the row's largest, which stands before the whole sum.
 template <typename T, int NW>
 __global__ void __launch_bounds__(64 * NW) expert_gather_kernel(const ExpertArgs p, int cols) {
   constexpr int P = Frag<T>::kPer, kStep = 4 * P, U = 8, kMost = kGatherPicks;
@@ -226,17 +227,23 @@ __global__ void __launch_bounds__(64 * NW) expert_gather_kernel(const ExpertArgs
   const int t0 = wave * per, t1 = min(total, t0 + per);
   const int64_t brow = min(n0 + r % cols, p.D - 1);
   const T *W2 = static_cast<const T*>(p.W2), *h = static_cast<const T*>(p.h);
-  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f}, sum = {0.f, 0.f, 0.f, 0.f};
   int a = t0 / spe, s = t0 - a * spe;  // the expert and the step in it
   for (int t = t0; t < t1; t += U) {
     u32x4 fb[U], fa[U];
+    int place[U];
+    bool last[U];  // step of the expert, or of the wave: the same for all lanes
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       fb[u] = fa[u] = u32x4{0, 0, 0, 0};
+      place[u] = -1;
+      last[u] = false;
       if (t + u < t1) {
-        const int k = s * kStep + g * P, place = at[a][r];
+        const int k = s * kStep + g * P;
+        place[u] = at[a][r];
         fb[u] = load_frag<T>(W2 + ((int64_t)expert[a] * p.D + brow) * p.F + k, p.F - k);
-        if (place >= 0) fa[u] = load_frag<T>(h + (int64_t)place * p.F + k, p.F - k);
+        if (place[u] >= 0) fa[u] = load_frag<T>(h + (int64_t)place[u] * p.F + k, p.F - k);
+        last[u] = s + 1 == spe || t + u + 1 == t1;
         if (++s == spe) {
           s = 0;
           ++a;
@@ -244,10 +251,19 @@ __global__ void __launch_bounds__(64 * NW) expert_gather_kernel(const ExpertArgs
       }
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) acc = Frag<T>::mma(fb[u], fa[u], acc);
+    for (int u = 0; u < U; ++u) {
+      acc = Frag<T>::mma(fb[u], fa[u], acc);
+      if (last[u]) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          sum[q] += place[u] >= 0 ? acc[q] : 0.f;
+          acc[q] = 0.f;
+        }
+      }
+    }
   }
 #pragma unroll
-  for (int q = 0; q < 4; ++q) red[wave][r][4 * g + q] = acc[q];
+  for (int q = 0; q < 4; ++q) red[wave][r][4 * g + q] = sum[q];
   __syncthreads();
   if (i < 256) {
     const int n = i & 15, c = n0 + n, row = i >> 4;
