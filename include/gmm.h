@@ -353,7 +353,8 @@ int gmm_linear_backward(const void* dY, int32_t y_dtype, const void* X, int32_t 
 
 /* Workspace bytes for gmm_linear (backward = 0) or gmm_linear_backward
  * (backward = 1); 0 for arguments outside the limits. 256 means that the call
- * needs none and takes a NULL workspace too. */
+ * needs none and takes a NULL workspace too; a call that needs one is told 512
+ * or more. */
 size_t gmm_linear_workspace_bytes(int64_t N, int32_t d_in, int32_t d_out, int32_t x_dtype, int32_t backward);
 
 /* Layer of experts gated by the mixture's posterior (a mixture of experts),

@@ -17,6 +17,7 @@ constexpr int64_t kMaxRows = 1 << 30;        // rows of a linear layer's call
 constexpr int64_t kLaunchRows = 1 << 20;     // rows of one launch (the grid's size)
 constexpr int64_t kDzRows = 16;              // rows per column-sum chunk, at least
 constexpr int64_t kDzMostRows = 8192;        // and at most: they are added one after the other
+constexpr size_t kNoWorkspace = 256;         // what the linear layer's query reports where none is needed
 constexpr int64_t kDzBlocks = 2048;          // blocks of the column sums, where the rows allow it
 
 static size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
@@ -356,7 +357,7 @@ size_t gmm_linear_workspace_bytes(int64_t N, int32_t d_in, int32_t d_out, int32_
   const size_t b = N == 0 ? 0
                    : backward ? backward_plan(N, d_in, d_out, e, false, true, true, true).bytes
                               : linear_plan(N, d_in, d_out, e).bytes;
-  return std::max<size_t>(b, 256);
+  return b == 0 ? kNoWorkspace : std::max(b, 2 * kNoWorkspace);  // a need of 256 bytes is not taken for none
 }
 
 int gmm_linear(const void* X, int32_t x_dtype, int64_t N, int32_t d_in, const void* W, int32_t d_out,
