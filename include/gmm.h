@@ -325,7 +325,9 @@ enum gmm_activation { GMM_ACT_NONE = 0, GMM_ACT_RELU = 1, GMM_ACT_GELU = 2, GMM_
  * X is N x d_in, W is d_out x d_in, bias d_out; Y, residual and pre are
  * N x d_out of y_dtype, which is x_dtype or GMM_F32. bias, residual and pre
  * are nullable; pre receives z, which gmm_linear_backward needs unless act is
- * GMM_ACT_NONE. All arithmetic is float, rounded once per output (a pre of 2
+ * GMM_ACT_NONE. All arithmetic is float, rounded once per output; gelu and silu
+ * are within 2^-20 of their value where Y is float, within 2^-16 before its
+ * rounding otherwise, also far down their negative tails (a pre of 2
  * bytes moves the gradients' error from 1.41 to 1.45 times that of their own
  * rounding; in float it would cost a fifth of the forward's time). Y may be
  * residual itself; no other output may overlap an input. Where a row of X is

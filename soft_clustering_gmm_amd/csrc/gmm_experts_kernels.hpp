@@ -333,15 +333,10 @@ static void launch_experts_act(const ExpertArgs& p, hipStream_t s) {
 
 template <typename T>
 hipError_t launch_experts(int act, const ExpertArgs& p, hipStream_t s) {
-  if (act == GMM_ACT_RELU)
-    launch_experts_act<T, GMM_ACT_RELU>(p, s);
-  else if (act == GMM_ACT_GELU)
-    launch_experts_act<T, GMM_ACT_GELU>(p, s);
-  else if (act == GMM_ACT_SILU)
-    launch_experts_act<T, GMM_ACT_SILU>(p, s);
-  else
-    launch_experts_act<T, GMM_ACT_NONE>(p, s);
-  return hipGetLastError();
+  return with_act<T, false>(act, false, [&](auto a) {
+    launch_experts_act<T, decltype(a)::value>(p, s);
+    return hipGetLastError();
+  });
 }
 
 #define GMM_EXPERTS_TYPE(T)                                          \

@@ -657,14 +657,6 @@ dz_kernel(const void* __restrict__ dY, const void* __restrict__ pre, int y_f32, 
 
 // --------------------------------------------------------------------------- launchers
 
-template <typename F>
-hipError_t with_act(int act, F&& f) {
-  if (act == GMM_ACT_RELU) return f(std::integral_constant<int, GMM_ACT_RELU>{});
-  if (act == GMM_ACT_GELU) return f(std::integral_constant<int, GMM_ACT_GELU>{});
-  if (act == GMM_ACT_SILU) return f(std::integral_constant<int, GMM_ACT_SILU>{});
-  return f(std::integral_constant<int, GMM_ACT_NONE>{});
-}
-
 template <typename T, bool AS, bool BS, int ACT>
 static void launch_tile(int variant, const ProductArgs& p, hipStream_t s) {
   const dim3 grid(p.tiles_m * p.tiles_n * p.splits + p.sum_blocks);
@@ -683,7 +675,7 @@ static void launch_tile(int variant, const ProductArgs& p, hipStream_t s) {
 template <typename T>
 hipError_t launch_product(int variant, bool a_strided, bool b_strided, int act, const ProductArgs& p, hipStream_t s) {
   if (!a_strided && !b_strided)
-    return with_act(act, [&](auto a) {
+    return with_act<T, true>(act, p.c_f32, [&](auto a) {
       launch_tile<T, false, false, decltype(a)::value>(variant, p, s);
       return hipGetLastError();
     });
@@ -697,7 +689,7 @@ hipError_t launch_product(int variant, bool a_strided, bool b_strided, int act, 
 
 template <typename T>
 hipError_t launch_few(int act, const FewArgs& p, hipStream_t s) {
-  return with_act(act, [&](auto a) {
+  return with_act<T, true>(act, p.c_f32, [&](auto a) {
     constexpr int ACT = decltype(a)::value;
     // more than two blocks a CU: two tiles a block, which halves what is read
     // of A; a single row is one address for all lanes and costs little
@@ -729,7 +721,7 @@ hipError_t launch_zero(T* p, int64_t n, hipStream_t s) {
 
 template <typename T>
 hipError_t launch_reduce(int act, const ProductArgs& p, hipStream_t s) {
-  return with_act(act, [&](auto a) {
+  return with_act<T, true>(act, p.c_f32, [&](auto a) {
     constexpr int ACT = decltype(a)::value;
     if (p.N % 4 == 0)
       product_reduce_kernel<T, ACT, 4><<<blocks_for(p.M * (p.N / 4) * 4), 256, 0, s>>>(p);
@@ -758,7 +750,7 @@ static void launch_dz_columns(const void* dY, const void* pre, int y_f32, int64_
 template <typename T>
 hipError_t launch_dz(int act, const void* dY, const void* pre, int y_f32, int64_t rows, int cols, T* dZ, int64_t ldz,
                      float* db_part, int64_t chunk_rows, const PadJob& px, const PadJob& pw, hipStream_t s) {
-  return with_act(act, [&](auto a) {
+  return with_act<T, false>(act, false, [&](auto a) {
     launch_dz_columns<T, decltype(a)::value, Frag<T>::kPer>(dY, pre, y_f32, rows, cols, dZ, ldz, db_part, chunk_rows,
                                                             px, pw, s);
     return hipGetLastError();

@@ -86,54 +86,121 @@ struct Frag<__bf16> {
   }
 };
 
-// Activations in single precision. A NaN z stays NaN.
-//
-// gelu is z Phi(z). The tail of the normal distribution is taken from Abramowitz
-// and Stegun, Handbook of Mathematical Functions, 7.1.26:
-//   erfc(x) = (a1 t + ... + a5 t^5) exp(-x^2),  t = 1 / (1 + p x),  x >= 0,
-// within 1.5e-7, which is 0.75e-7 of Phi: below half a step of single precision
-// next to 1. With x = |z| / sqrt 2 the exponential is also the density's, which
-// the slope needs. It takes a third of erff's instructions.
+// Activations in single precision. A NaN z stays NaN. Float results take the
+// FULL forms of gelu and silu (within 2^-20 of the value); results that are
+// rounded to 2 bytes are within 2^-16 of it before, a thirty-second of half's
+// half step, in fewer instructions. The form is part of the kernel: with both
+// behind a branch the bfloat16 product of 8192 x 4096 to 16384 with gelu took
+// 965 us against 912. The kernels' ACT is one of gmm_activation or these:
+enum { kGeluFull = 4, kSiluFull = 5 };
+
+// gelu is z Phi(z). With x = |z| the lower tail of the normal distribution is
+//   Phi(-x) = exp(-x^2 / 2) r(x),  r(x) = erfc(x / sqrt 2) exp(x^2 / 2) / 2,
+// where r falls slowly, like 1 / x, and t P(t), t = 1 / (1 + p x), with a
+// polynomial P fits it with the smallest largest relative error over x = 0..14,
+// beyond which the exponential is 0: of degree 8 with p = 0.2625 within 1.8e-8,
+// of degree 6 with p = 0.265 within 6.3e-7. (A small absolute error of erfc is
+// not enough: gelu's negative values are the tail itself.) The exponential is
+// also the density's, which the slope needs.
 struct Normal {
   float cdf, e;  // Phi(z), exp(-z^2 / 2)
 };
+
+// 2^(h + lo) for a small lo, the rounding errors of h.
+__device__ __forceinline__ float exp2_of(float h, float lo) {
+  const float e = __builtin_amdgcn_exp2f(h);
+  return fmaf(e, 0.69314718055994531f * lo, e);
+}
+
+template <bool FULL>
 __device__ __forceinline__ Normal normal_of(float z) {
-  const float x = fabsf(z) * 0.70710678118654752f;
-  const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, x, 1.f));
-  const float e = __builtin_amdgcn_exp2f(-0.72134752044448170f * z * z);
-  float q = fmaf(1.061405429f, t, -1.453152027f);
-  q = fmaf(q, t, 1.421413741f);
-  q = fmaf(q, t, -0.284496736f);
-  q = fmaf(q, t, 0.254829592f);
-  const float tail = 0.5f * q * t * e;
+  float tail, e;
+  if (FULL) {
+    const float x = fminf(fabsf(z), 16.f);  // from here on the exponential is 0
+    const float d = fmaf(0.2625f, x, 1.f), t0 = __builtin_amdgcn_rcpf(d), t = fmaf(fmaf(-d, t0, 1.f), t0, t0);
+    // -x^2 / 2 in units of log 2, with what its roundings leave
+    constexpr float kHigh = 0.721347511f, kLow = 9.62981495e-9f;
+    const float s = x * x, h = -kHigh * s;
+    e = exp2_of(h, fmaf(-kHigh, fmaf(x, x, -s), fmaf(-kLow, s, fmaf(-kHigh, s, -h))));
+    float q = fmaf(0.0307454728f, t, -0.148810312f);
+    q = fmaf(q, t, 0.234761387f);
+    q = fmaf(q, t, -0.133391514f);
+    q = fmaf(q, t, 0.149138391f);
+    q = fmaf(q, t, 0.0558492616f);
+    q = fmaf(q, t, 0.102818556f);
+    q = fmaf(q, t, 0.104138888f);
+    q = fmaf(q, t, 0.104749881f);
+    tail = q * t * e;
+  } else {
+    const float t = __builtin_amdgcn_rcpf(fmaf(0.265f, fabsf(z), 1.f));
+    e = __builtin_amdgcn_exp2f(-0.72134752044448170f * z * z);
+    float q = fmaf(-0.0677870363f, t, 0.195273101f);
+    q = fmaf(q, t, -0.0663629025f);
+    q = fmaf(q, t, 0.142493322f);
+    q = fmaf(q, t, 0.0829465911f);
+    q = fmaf(q, t, 0.107836783f);
+    q = fmaf(q, t, 0.105599836f);
+    tail = q * t * e;
+  }
   return {z < 0.f ? tail : 1.f - tail, e};
 }
 
-// 1 / (1 + exp(-z)): a far negative z gives 1 / inf = 0.
-__device__ __forceinline__ float logistic(float z) {
-  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504088896341f * z));
+// 1 / (1 + exp(-z)) and 1 / (1 + exp(z)).
+struct Logistic {
+  float q, p;
+};
+template <bool FULL>
+__device__ __forceinline__ Logistic logistic(float z) {
+  if (FULL) {
+    const float x = fminf(fabsf(z), 128.f);  // from here on the exponential is 0
+    constexpr float kHigh = 1.44269502f, kLow = 1.92596299e-8f;
+    const float h = -kHigh * x, e = exp2_of(h, fmaf(-kLow, x, fmaf(-kHigh, x, -h)));
+    const float near = 1.f / (1.f + e), far = e / (1.f + e);
+    return z < 0.f ? Logistic{far, near} : Logistic{near, far};
+  }
+  // a far negative z gives 1 / inf = 0
+  const float q = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504088896341f * z));
+  return {q, 1.f - q};
 }
 
 template <int ACT>
 __device__ __forceinline__ float act_value(float z) {
   if (ACT == GMM_ACT_RELU) return z < 0.f ? 0.f : z;
-  if (ACT == GMM_ACT_GELU) return z * normal_of(z).cdf;
-  if (ACT == GMM_ACT_SILU) return z * logistic(z);
+  if (ACT == GMM_ACT_GELU || ACT == kGeluFull) return z * normal_of<ACT == kGeluFull>(z).cdf;
+  if (ACT == GMM_ACT_SILU || ACT == kSiluFull) return z * logistic<ACT == kSiluFull>(z).q;
   return z;
 }
 
 template <int ACT>
 __device__ __forceinline__ float act_slope(float z) {
   if (ACT == GMM_ACT_RELU) return z > 0.f ? 1.f : z == z ? 0.f : z;
-  if (ACT == GMM_ACT_GELU) {
-    const Normal n = normal_of(z);
+  if (ACT == GMM_ACT_GELU || ACT == kGeluFull) {
+    const Normal n = normal_of<ACT == kGeluFull>(z);
     return fmaf(0.39894228040143268f * z, n.e, n.cdf);
   }
-  if (ACT == GMM_ACT_SILU) {
-    const float q = logistic(z);
-    return q * (1.f + z * (1.f - q));
+  if (ACT == GMM_ACT_SILU || ACT == kSiluFull) {
+    const Logistic l = logistic<ACT == kSiluFull>(z);
+    return l.q * (1.f + z * l.p);
   }
   return 1.f;
+}
+
+// f with the activation's form for results of type T, or float where `to_float`
+// (only if MIXED).
+template <typename T, bool MIXED, typename F>
+hipError_t with_act(int act, bool to_float, F&& f) {
+  if (act == GMM_ACT_RELU) return f(std::integral_constant<int, GMM_ACT_RELU>{});
+  if constexpr (MIXED || sizeof(T) == 4) {
+    if (to_float || sizeof(T) == 4) {
+      if (act == GMM_ACT_GELU) return f(std::integral_constant<int, kGeluFull>{});
+      if (act == GMM_ACT_SILU) return f(std::integral_constant<int, kSiluFull>{});
+    }
+  }
+  if constexpr (sizeof(T) != 4) {
+    if (act == GMM_ACT_GELU) return f(std::integral_constant<int, GMM_ACT_GELU>{});
+    if (act == GMM_ACT_SILU) return f(std::integral_constant<int, GMM_ACT_SILU>{});
+  }
+  return f(std::integral_constant<int, GMM_ACT_NONE>{});
 }
 
 // Orders this wave's LDS accesses (all lanes) before its later ones.
