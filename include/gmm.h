@@ -343,7 +343,9 @@ int gmm_linear(const void* X, int32_t x_dtype, int64_t N, int32_t d_in, const vo
  *   dZ = dY act'(pre),  dX = dZ W,  dW = dZ^T X,  db = sum_n dZ_n
  * (the residual's gradient is dY). dX (N x d_in), dW (d_out x d_in) and db
  * (d_out) have type x_dtype; each is nullable, and what only the others need
- * may be NULL too (W without dX, X without dW). relu's slope at 0 is 0. The
+ * may be NULL too (W without dX, X without dW). relu's slope at 0 is 0; the
+ * slopes at an infinite pre (a z beyond the range of half) are their limits, 0
+ * and 1. The
  * products take dZ rounded to x_dtype, as the matrix instructions do, and
  * accumulate in float; db sums the unrounded dZ in float. Sums run in a fixed
  * order. N = 0 gives dW = 0 and db = 0. Alignment of X and W as above. The

@@ -171,14 +171,22 @@ __device__ __forceinline__ float act_value(float z) {
   return z;
 }
 
+// z held to +-most; a NaN stays one.
+__device__ __forceinline__ float within(float z, float most) { return z > most ? most : z < -most ? -most : z; }
+
+// The slopes are constant beyond 16 and 128, where the exponentials are 0. z is
+// held to that range because a pre of 2 bytes may be infinite where z was not,
+// and infinity times 0 is not the slope's limit.
 template <int ACT>
 __device__ __forceinline__ float act_slope(float z) {
   if (ACT == GMM_ACT_RELU) return z > 0.f ? 1.f : z == z ? 0.f : z;
   if (ACT == GMM_ACT_GELU || ACT == kGeluFull) {
+    z = within(z, 16.f);
     const Normal n = normal_of<ACT == kGeluFull>(z);
     return fmaf(0.39894228040143268f * z, n.e, n.cdf);
   }
   if (ACT == GMM_ACT_SILU || ACT == kSiluFull) {
+    z = within(z, 128.f);
     const Logistic l = logistic<ACT == kSiluFull>(z);
     return l.q * (1.f + z * l.p);
   }
