@@ -345,10 +345,12 @@ int gmm_linear(const void* X, int32_t x_dtype, int64_t N, int32_t d_in, const vo
  * (d_out) have type x_dtype; each is nullable, and what only the others need
  * may be NULL too (W without dX, X without dW). relu's slope at 0 is 0; the
  * slopes at an infinite pre (a z beyond the range of half) are their limits, 0
- * and 1. The
- * products take dZ rounded to x_dtype, as the matrix instructions do, and
- * accumulate in float; db sums the unrounded dZ in float. Sums run in a fixed
- * order. N = 0 gives dW = 0 and db = 0. Alignment of X and W as above. The
+ * and 1. The products take dZ rounded to x_dtype, as the matrix instructions
+ * do, and accumulate in float; for half operands and a float dY it is scaled
+ * by a power of two first, set by its largest finite value and taken back from
+ * the sums, so that a dY of any size keeps half's 11 bits (a half dY is taken
+ * as it is, in half's range). db sums the unrounded dZ in float. Sums run in a
+ * fixed order. N = 0 gives dW = 0 and db = 0. Alignment of X and W as above. The
  * workspace must hold gmm_linear_workspace_bytes(N, d_in, d_out, x_dtype, 1)
  * bytes. */
 int gmm_linear_backward(const void* dY, int32_t y_dtype, const void* X, int32_t x_dtype, int64_t N, int32_t d_in,

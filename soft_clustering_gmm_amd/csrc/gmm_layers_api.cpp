@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "gmm_experts.hpp"
 #include "gmm_linear.hpp"
@@ -138,12 +139,12 @@ static LinearPlan linear_plan(int64_t N, int d_in, int d_out, int e) {
 }
 
 // Workspace of the backward pass: [dZ] [padded X] [padded W] [partial sums of
-// dX, then of dW] [column sums].
+// dX, then of dW] [column sums] [range of dZ and its scale's inverse].
 struct BackwardPlan {
   int64_t lx, lz;  // row lengths of X and W, of dZ
   bool pad, own_dz;
   int64_t chunk, chunks;  // rows per column sum
-  size_t o_z, o_x, o_w, o_part, o_db, bytes;
+  size_t o_z, o_x, o_w, o_part, o_db, o_range, bytes;
 };
 
 static BackwardPlan backward_plan(int64_t N, int d_in, int d_out, int e, bool plain_dz, bool want_dx, bool want_dw,
@@ -175,6 +176,7 @@ static BackwardPlan backward_plan(int64_t N, int d_in, int d_out, int e, bool pl
   b.o_w = take(b.pad && want_dx ? (size_t)d_out * b.lx * e : 0);
   b.o_part = take(part);
   b.o_db = take(want_db ? (size_t)b.chunks * d_out * sizeof(float) : 0);
+  b.o_range = take(e == 2 ? (kRangeBlocks + 1) * sizeof(float) : 0);
   b.bytes = off;
   return b;
 }
@@ -241,9 +243,18 @@ static hipError_t linear_gradients(const void* dY, int y_f32, const T* X, int64_
   PadJob px{}, pw{};
   if (b.pad && dW) px = PadJob{X, ws + b.o_x, N, b.lx, d_in};
   if (b.pad && dX) pw = PadJob{W, ws + b.o_w, d_out, b.lx, d_in};
+  // Half does not hold every float: dZ is scaled for the products.
+  float* range = nullptr;
+  if constexpr (std::is_same<T, _Float16>::value)
+    if (y_f32 && b.own_dz) {
+      range = reinterpret_cast<float*>(ws + b.o_range);
+      e = launch_dz_range<T>(act, static_cast<const float*>(dY), static_cast<const float*>(pre), N * d_out, range, s);
+      if (e != hipSuccess) return e;
+    }
+  float* unscale = range ? range + kRangeBlocks : nullptr;
   if (b.own_dz || db)
     e = launch_dz<T>(act, dY, pre, y_f32, N, d_out, b.own_dz ? z : nullptr, b.lz, db ? part : nullptr, b.chunk, px, pw,
-                     s);
+                     range, unscale, s);
   else if (px.rows || pw.rows)
     e = launch_pad<T>(px, pw, s);
   if (e != hipSuccess) return e;
@@ -253,6 +264,7 @@ static hipError_t linear_gradients(const void* dY, int y_f32, const T* X, int64_
   p.c_f32 = sizeof(T) == 4;
   p.N = d_in;
   p.ldb = b.lx;
+  p.unscale = unscale;
   if (db) {  // summed beside the first product
     p.sums = part;
     p.sums_out = db;

@@ -34,6 +34,7 @@ struct ProductArgs {
   void* sums_out;        // type of the operands
   int64_t sums_rows;
   int sums_cols, sum_blocks;
+  const float* unscale;  // C = *unscale times the product, where not null (gradients of half operands)
 };
 constexpr int kSumCols = 16;  // columns of such a block
 
@@ -86,10 +87,17 @@ template <typename T>
 hipError_t launch_reduce(int act, const ProductArgs& p, hipStream_t s);
 // dZ = dY act'(pre) in the operands' type, rows of ldz elements (zeros
 // behind), and per-chunk column sums of the unrounded dZ in db_part; dZ or
-// db_part may be null. The two copies run in the same launch.
+// db_part may be null. The two copies run in the same launch. Where `range` is
+// not null (launch_dz_range has filled it), dZ is scaled by a power of two and
+// *unscale receives its inverse.
 template <typename T>
 hipError_t launch_dz(int act, const void* dY, const void* pre, int y_f32, int64_t rows, int cols, T* dZ, int64_t ldz,
-                     float* db_part, int64_t chunk_rows, const PadJob& px, const PadJob& pw, hipStream_t s);
+                     float* db_part, int64_t chunk_rows, const PadJob& px, const PadJob& pw, const float* range,
+                     float* unscale, hipStream_t s);
+// range[0..kRangeBlocks): their largest is the largest finite |dY act'(pre)|.
+constexpr int kRangeBlocks = 256;
+template <typename T>
+hipError_t launch_dz_range(int act, const float* dY, const float* pre, int64_t n, float* range, hipStream_t s);
 // The column sums of `p` alone.
 template <typename T>
 hipError_t launch_column_sums(const ProductArgs& p, hipStream_t s);

@@ -3,4 +3,5 @@
 
 namespace gmm {
 GMM_LINEAR_TYPE(_Float16)
+template hipError_t launch_dz_range<_Float16>(int, const float*, const float*, int64_t, float*, hipStream_t);
 }  // namespace gmm

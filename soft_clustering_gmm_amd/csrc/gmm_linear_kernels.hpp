@@ -2,6 +2,7 @@
 // (gmm_linear_f32.hip, gmm_linear_f16.hip, gmm_linear_bf16.hip).
 #pragma once
 
+#include <cfloat>
 #include <type_traits>
 
 #include "gmm_linear.hpp"
@@ -330,6 +331,10 @@ __global__ void __launch_bounds__(256) column_sums_kernel(const ProductArgs p) {
   column_sums<T>(p, blockIdx.x, red);
 }
 
+// Products that may be unscaled: the gradients' of half operands (B k-strided).
+template <typename T, bool BS>
+constexpr bool kScaled = BS && std::is_same<T, _Float16>::value;
+
 template <typename T, int BM, int BN, int WM, int WN, bool AS, bool BS, int ACT>
 __global__ void __launch_bounds__(64 * WM * WN, 2)
 product_kernel(const ProductArgs p) {
@@ -433,6 +438,7 @@ product_kernel(const ProductArgs p) {
   char* mine = lds + wave * 16 * kRow;
   const int n = at.n0 + wn * TN + lane % kChunks * W;
   const bool whole = p.splits == 1;
+  const float unscale = kScaled<T, BS> && whole && p.unscale ? *p.unscale : 1.f;
   float bias[W];
 #pragma unroll
   for (int i = 0; i < W; ++i) bias[i] = 0.f;
@@ -466,6 +472,9 @@ product_kernel(const ProductArgs p) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) z[k + c] = v[c];
       }
+      if (kScaled<T, BS>)
+#pragma unroll
+        for (int k = 0; k < W; ++k) z[k] *= unscale;
       const int64_t m = row_of(i, q);
       if (m < p.M && n < p.N) {
         if (whole)
@@ -488,6 +497,7 @@ __global__ void __launch_bounds__(256) product_reduce_kernel(const ProductArgs p
   const int per_row = (p.N + W - 1) / W;
   const int64_t total = p.M * per_row, part = p.M * p.N;
   const int quarter = (p.splits + 3) / 4, s0 = wave * quarter, s1 = min(p.splits, s0 + quarter);
+  const float unscale = kScaled<T, ACT == GMM_ACT_NONE> && p.unscale ? *p.unscale : 1.f;
   for (int64_t i0 = blockIdx.x * 64ll; i0 < total; i0 += gridDim.x * 64ll) {
     const int64_t i = i0 + lane, m = i / per_row;
     const int n = (int)(i - m * per_row) * W;
@@ -514,7 +524,7 @@ __global__ void __launch_bounds__(256) product_reduce_kernel(const ProductArgs p
       const int col = (int)(at - row * per_row) * W;
 #pragma unroll
       for (int k = 0; k < W; ++k)
-        z[k] = (red[0][mine][k] + red[1][mine][k]) + (red[2][mine][k] + red[3][mine][k]);
+        z[k] = unscale * ((red[0][mine][k] + red[1][mine][k]) + (red[2][mine][k] + red[3][mine][k]));
       if (p.bias) load_as<T, W>(static_cast<const T*>(p.bias) + col, W, bias);
       float res[W];
       load_residual<T, W>(p, row, col, res);
@@ -595,22 +605,87 @@ __global__ void __launch_bounds__(256) zero_kernel(T* p, int64_t n) {
   for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < n; i += gridDim.x * 256ll) p[i] = (T)0.f;
 }
 
+// The largest finite |dY act'(pre)|, in parts, for the scale of a half dZ. One
+// more read of dY and pre, by a block of 16 waves a CU: the backward pass of half
+// operands and a float dY takes 388 us with it and 334 without at 4096 x 2048 to
+// 8192 (268 MB, 4.9 TB/s), 31 and 26 at 1001 x 516 to 1000.
+constexpr int kRangeThreads = 1024;
+template <int ACT>
+__global__ void __launch_bounds__(kRangeThreads)
+dz_range_kernel(const float* __restrict__ dY, const float* __restrict__ pre, int64_t n, float* __restrict__ range) {
+  constexpr int U = 4, V = 4;  // 4 loads of 16 bytes in flight
+  __shared__ float red[kRangeThreads / 64];
+  const int64_t stride = (int64_t)kRangeBlocks * kRangeThreads * V;
+  float most = 0.f;
+  for (int64_t i = ((int64_t)blockIdx.x * kRangeThreads + threadIdx.x) * V; i < n; i += U * stride) {
+    float v[U][V], z[U][V];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t at = i + u * stride;
+      const int left = at < n ? (int)min((int64_t)V, n - at) : 0;
+      load_as<float, V>(dY + at, left, v[u]);
+      if (ACT != GMM_ACT_NONE) load_as<float, V>(pre + at, left, z[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        const float a = fabsf(ACT == GMM_ACT_NONE ? v[u][k] : v[u][k] * act_slope<ACT>(z[u][k]));
+        if (a <= FLT_MAX) most = fmaxf(most, a);
+      }
+  }
+#pragma unroll
+  for (int o = 32; o; o >>= 1) most = fmaxf(most, __shfl_xor(most, o));
+  if (threadIdx.x % 64 == 0) red[threadIdx.x / 64] = most;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < kRangeThreads / 64; ++w) most = fmaxf(most, red[w]);
+    range[blockIdx.x] = most;
+  }
+}
+
+// The power of two that brings the largest of `range` into [2^13, 2^14), in every
+// thread of a block of kRangeBlocks: half then holds dZ with its 11 bits down to
+// 2^-28 of the largest, wherever dY lies, and nothing overflows. 1 for no values.
+__device__ __forceinline__ int dz_scale(const float* range) {
+  __shared__ float red[kRangeBlocks / 64];
+  float most = range[threadIdx.x];
+#pragma unroll
+  for (int o = 32; o; o >>= 1) most = fmaxf(most, __shfl_xor(most, o));
+  if (threadIdx.x % 64 == 0) red[threadIdx.x / 64] = most;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kRangeBlocks / 64; ++w) most = fmaxf(most, red[w]);
+  if (!(most > 0.f)) return 0;
+  int e;
+  frexpf(most, &e);
+  return min(126, max(-126, 14 - e));  // the scale and its inverse are normal
+}
+
 // dZ and the column sums of a chunk of rows. A thread owns V consecutive
-// columns (16 bytes of the operands' type), 256 / CG
-// rows go at a time; the rows' sums meet in LDS at the end. The last `pads`
-// blocks copy X and W to padded rows, where the products need that.
-template <typename T, int ACT, int V, int CG>
+// columns (16 bytes of the operands' type), 256 / CG rows go at a time; the
+// rows' sums meet in LDS at the end. The last `pads`
+// blocks copy X and W to padded rows, where the products need that. SCALED: dZ
+// is scaled by dz_scale, the column sums are not.
+template <typename T, int ACT, int V, int CG, bool SCALED>
 __global__ void __launch_bounds__(256)
 dz_kernel(const void* __restrict__ dY, const void* __restrict__ pre, int y_f32, int64_t rows, int cols,
           T* __restrict__ dZ, int64_t ldz, float* __restrict__ db_part, int64_t chunk_rows, int across, int pads,
-          const PadJob px, const PadJob pw) {
+          const PadJob px, const PadJob pw, const float* __restrict__ range, float* __restrict__ unscale) {
   constexpr int RG = 256 / CG;
+  static_assert(kRangeBlocks == 256, "a thread each");
   __shared__ float red[RG][CG * V];
   const int pad = (int)blockIdx.x - ((int)gridDim.x - pads);
   if (pad >= 0) {
     pad_rows<T>(px, pad * 256ll + threadIdx.x, pads * 256ll);
     pad_rows<T>(pw, pad * 256ll + threadIdx.x, pads * 256ll);
     return;
+  }
+  float scale = 1.f;
+  if (SCALED) {
+    const int e = dz_scale(range);
+    scale = ldexpf(1.f, e);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *unscale = ldexpf(1.f, -e);
   }
   const int bx = blockIdx.x % across, by = blockIdx.x / across;
   const int cg = threadIdx.x % CG, rg = threadIdx.x / CG;
@@ -638,6 +713,9 @@ dz_kernel(const void* __restrict__ dY, const void* __restrict__ pre, int y_f32, 
             for (int i = 0; i < V; ++i) v[u][i] *= act_slope<ACT>(z[u][i]);
 #pragma unroll
           for (int i = 0; i < V; ++i) sum[i] += v[u][i];
+          if (SCALED)
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[u][i] *= scale;
           if (dZ) store_as<T, V>(dZ + (r + u * RG) * ldz + c, (int)min((int64_t)V, ldz - c), v[u]);
         }
     }
@@ -731,28 +809,46 @@ hipError_t launch_reduce(int act, const ProductArgs& p, hipStream_t s) {
   });
 }
 
-template <typename T, int ACT, int V>
+template <typename T, int ACT, bool SCALED>
 static void launch_dz_columns(const void* dY, const void* pre, int y_f32, int64_t rows, int cols, T* dZ, int64_t ldz,
-                              float* db_part, int64_t chunk_rows, const PadJob& px, const PadJob& pw, hipStream_t s) {
+                              float* db_part, int64_t chunk_rows, const PadJob& px, const PadJob& pw, const float* range,
+                              float* unscale, hipStream_t s) {
+  constexpr int V = Frag<T>::kPer;
   const int64_t groups = (cols + V - 1) / V, chunks = (rows + chunk_rows - 1) / chunk_rows;
-  const int64_t pieces = (px.rows * px.ld + pw.rows * pw.ld) / Frag<T>::kPer;
+  const int64_t pieces = (px.rows * px.ld + pw.rows * pw.ld) / V;
   const int pads = pieces ? (int)blocks_for(pieces) : 0;
   const int across = groups > 16 ? (int)((groups + 63) / 64) : 1;
   const unsigned grid = (unsigned)(across * chunks + pads);
   if (groups > 16)
-    dz_kernel<T, ACT, V, 64><<<grid, 256, 0, s>>>(dY, pre, y_f32, rows, cols, dZ, ldz, db_part, chunk_rows, across,
-                                                  pads, px, pw);
+    dz_kernel<T, ACT, V, 64, SCALED><<<grid, 256, 0, s>>>(dY, pre, y_f32, rows, cols, dZ, ldz, db_part, chunk_rows,
+                                                          across, pads, px, pw, range, unscale);
   else  // narrow rows: more of them at a time
-    dz_kernel<T, ACT, V, 16><<<grid, 256, 0, s>>>(dY, pre, y_f32, rows, cols, dZ, ldz, db_part, chunk_rows, across,
-                                                  pads, px, pw);
+    dz_kernel<T, ACT, V, 16, SCALED><<<grid, 256, 0, s>>>(dY, pre, y_f32, rows, cols, dZ, ldz, db_part, chunk_rows,
+                                                          across, pads, px, pw, range, unscale);
 }
 
 template <typename T>
 hipError_t launch_dz(int act, const void* dY, const void* pre, int y_f32, int64_t rows, int cols, T* dZ, int64_t ldz,
-                     float* db_part, int64_t chunk_rows, const PadJob& px, const PadJob& pw, hipStream_t s) {
+                     float* db_part, int64_t chunk_rows, const PadJob& px, const PadJob& pw, const float* range,
+                     float* unscale, hipStream_t s) {
   return with_act<T, false>(act, false, [&](auto a) {
-    launch_dz_columns<T, decltype(a)::value, Frag<T>::kPer>(dY, pre, y_f32, rows, cols, dZ, ldz, db_part, chunk_rows,
-                                                            px, pw, s);
+    constexpr int ACT = decltype(a)::value;
+    if constexpr (std::is_same<T, _Float16>::value) {
+      if (range) {
+        launch_dz_columns<T, ACT, true>(dY, pre, y_f32, rows, cols, dZ, ldz, db_part, chunk_rows, px, pw, range, unscale,
+                                        s);
+        return hipGetLastError();
+      }
+    }
+    launch_dz_columns<T, ACT, false>(dY, pre, y_f32, rows, cols, dZ, ldz, db_part, chunk_rows, px, pw, range, unscale, s);
+    return hipGetLastError();
+  });
+}
+
+template <typename T>
+hipError_t launch_dz_range(int act, const float* dY, const float* pre, int64_t n, float* range, hipStream_t s) {
+  return with_act<T, false>(act, false, [&](auto a) {
+    dz_range_kernel<decltype(a)::value><<<kRangeBlocks, kRangeThreads, 0, s>>>(dY, pre, n, range);
     return hipGetLastError();
   });
 }
@@ -770,7 +866,7 @@ hipError_t launch_column_sums(const ProductArgs& p, hipStream_t s) {
   template hipError_t launch_zero<T>(T*, int64_t, hipStream_t);                                                    \
   template hipError_t launch_reduce<T>(int, const ProductArgs&, hipStream_t);                                      \
   template hipError_t launch_dz<T>(int, const void*, const void*, int, int64_t, int, T*, int64_t, float*, int64_t, \
-                                   const PadJob&, const PadJob&, hipStream_t);                                                                   \
+                                   const PadJob&, const PadJob&, const float*, float*, hipStream_t);               \
   template hipError_t launch_column_sums<T>(const ProductArgs&, hipStream_t);
 
 }  // namespace gmm

@@ -1,0 +1,105 @@
+"""Gradients of a layer of half operands from a float dY of any size: dZ is taken in half for the products, but scaled by
+a power of two first, so what counts is its size beside its largest value, not half's range."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from tests import layer_oracle as oracle  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+HALF = torch.float16
+
+
+def make(N, d_in, d_out, size, x_size, w_size, seed, lean=0.0):
+    g = torch.Generator().manual_seed(seed)
+
+    def normal(*shape, scale, t):
+        return ((torch.randn(*shape, generator=g) + lean) * scale).to(t).cuda()
+    return (normal(N, d_in, scale=x_size, t=HALF), normal(d_out, d_in, scale=w_size, t=HALF),
+            normal(N, d_out, scale=size, t=torch.float32))
+
+
+def check(got, dY, X, W, pre, name):
+    x, w, dz = oracle.wide(X), oracle.wide(W), oracle.wide(dY)
+    fn = torch.zeros_like(dz)
+    if name != "none":
+        z = oracle.wide(pre)
+        fn = dz.abs() * oracle.FUNCTION * z.abs().clamp(min=1.0)
+        dz = dz * oracle.slope(z, name)
+    # scaled so that the largest lies in [2^13, 2^14): half a step of 2^-11, and of the smallest step, 2^-24
+    per = dz.abs() * 2.0 ** -11 + dz.abs().max() * 2.0 ** -38 + fn + 2.0 ** -23 * dz.abs()
+    want = (dz @ w, dz.T @ x, dz.sum(0))
+    bound = (per @ w.abs() + oracle.sum_bound(dz.abs() + per, w.T, w.shape[0]),
+             per.T @ x.abs() + oracle.sum_bound((dz.abs() + per).T, x.T, x.shape[0]),
+             fn.sum(0) + (x.shape[0] + 8) * 2.0 ** -23 * dz.abs().sum(0))
+    for g, v, b, what in zip(got, want, bound, ("dx", "dw", "db")):
+        assert v.abs().max() < 65504, "the case itself has to fit"
+        oracle.check(g, v, b + oracle.rounding(v.abs() + b, HALF), what)
+
+
+# a mean loss over many rows; a large loss scale; whole and odd rows, few rows, split contractions of dW and of dX
+@pytest.mark.parametrize("name", ["none", "silu", "gelu"])
+@pytest.mark.parametrize("N,d_in,d_out", [(20000, 40, 24), (3001, 45, 67), (5, 64, 32), (40, 24, 8192), (300, 264, 520)])
+@pytest.mark.parametrize("size", ["small", "large"])
+def test_float_dy_of_any_size(N, d_in, d_out, size, name):
+    from soft_clustering_gmm_amd import gmm as G
+    act = getattr(G, "ACT_" + name.upper())
+    pre = None if name == "none" else torch.randn(N, d_out, generator=torch.Generator().manual_seed(1)).cuda()
+    if size == "small":  # below half's smallest step; the sums are not
+        X, W, dY = make(N, d_in, d_out, 1e-9, 30.0, 300.0, seed=N, lean=1.0)
+    else:  # beyond half's largest value; pairs of rows cancel in db, which would not fit
+        X, W, dY = make(N, d_in, d_out, 5e5, 1e-4, 1e-4, seed=N)
+        pairs = N // 2 * 2
+        dY[1:pairs:2] = -dY[0:pairs:2]
+        dY[pairs:] = 0
+        if pre is not None:
+            pre[1:pairs:2] = pre[0:pairs:2]
+    got = G.linear_backward(dY, X, W, pre=pre, act=act)
+    check(got, dY, X, W, pre, name)
+    one = G.linear_backward(dY, X, W, pre=pre, act=act, want_dw=False, want_db=False)
+    two = G.linear_backward(dY, X, W, pre=pre, act=act, want_dx=False, want_db=False)
+    assert torch.equal(one[0], got[0]) and torch.equal(two[1], got[1])
+
+
+def test_no_and_infinite_values():
+    from soft_clustering_gmm_amd import gmm as G
+    X, W, dY = make(300, 40, 24, 1e-9, 30.0, 300.0, seed=0, lean=1.0)
+    for g in G.linear_backward(torch.zeros_like(dY), X, W):
+        assert (g == 0).all()
+    want = G.linear_backward(dY, X, W)
+    for odd in (float("inf"), float("nan")):
+        bad = dY.clone()
+        bad[7, 3] = odd
+        dX, dW, db = G.linear_backward(bad, X, W)
+        rows, cols = torch.arange(300, device="cuda") != 7, torch.arange(24, device="cuda") != 3
+        assert not dX[7].isfinite().any() and not dW[3].isfinite().any() and not db[3].isfinite()
+        # the largest finite value sets the scale: here it is where it was, or the roundings are those of another scale
+        assert torch.equal(db[cols], want[2][cols])
+        off = (dX[rows].double() - want[0][rows].double()).abs()
+        assert (off <= want[0][rows].double().abs() * 2.0 ** -9 + 2.0 ** -20).all()
+        assert dW[cols].isfinite().all()
+
+
+def test_captured_and_one_scale_at_a_time():
+    """Replays with gradients of very different sizes, each with its own scale."""
+    from soft_clustering_gmm_amd import gmm as G
+    X, W, dY = make(900, 72, 40, 1.0, 1.0, 1.0, seed=2)
+    ws = G.linear_workspace(900, 72, 40, HALF, X.device, backward=True)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        G.linear_backward(dY, X, W, ws=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = G.linear_backward(dY, X, W, ws=ws)
+    base = dY.clone()
+    for scale in (1.0, 2.0 ** -20, 2.0 ** 4, 0.0, 2.0 ** -10):
+        dY.copy_(base * scale)
+        graph.replay()
+        torch.cuda.synchronize()
+        kept = [t.clone() for t in got]
+        for a, b in zip(kept, G.linear_backward(dY, X, W, ws=ws)):
+            assert torch.equal(a, b), scale
+        torch.cuda.synchronize()
