@@ -402,7 +402,9 @@ def kmeans_iterate(X, C, iters: int, *, ws=None):
     return hist[:iters]
 
 
-# A layer's call is often shorter than its launch: sizes are looked up once, and the stream is torch's raw handle.
+# A layer's call is often shorter than its launch: sizes are looked up once, and the stream is torch's raw handle (its
+# tensors are on a GPU, so torch's part of it is initialised).
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
@@ -420,6 +422,62 @@ def _matrix(t, name):
 def _optional(t, name, dtype, shape, device):
     if t is not None:
         _need(t, name, dtype, shape, device)
+
+
+_grad_mode = torch.is_grad_enabled
+
+
+def _tracked(*tensors):
+    """Whether torch would record a graph for these inputs."""
+    if _grad_mode():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                return True
+    return False
+
+
+class _Linear(torch.autograd.Function):
+    """linear in torch's graph: its backward pass is linear_backward."""
+
+    @staticmethod
+    def forward(ctx, X, W, bias, residual, act, out_dtype, want_pre, ws):
+        need = act != ACT_NONE and any(ctx.needs_input_grad[:3])
+        Y, pre = linear(X, W, bias=bias, act=act, residual=residual, out_dtype=out_dtype, want_pre=want_pre or need,
+                        ws=ws)
+        ctx.act = act
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(X, W, pre if need else None)
+        if not want_pre:
+            return Y, None
+        ctx.mark_non_differentiable(pre)
+        return Y, pre
+
+    @staticmethod
+    def backward(ctx, dY, _):
+        if torch.is_grad_enabled():  # create_graph: the gradients would count as constants
+            raise NotImplementedError("gmm.linear has no second derivatives")
+        need = ctx.needs_input_grad
+        grads = (None, None, None)
+        if dY is not None and any(need[:3]):
+            X, W, pre = ctx.saved_tensors
+            grads = linear_backward(dY.contiguous(), X, W, pre=pre, act=ctx.act, want_dx=need[0], want_dw=need[1],
+                                    want_db=need[2])
+        return (*grads, dY if need[3] else None, None, None, None, None)
+
+
+class _ForwardOnly(torch.autograd.Function):
+    """A call without a backward pass in torch's graph: it says so there, rather than leave its inputs out."""
+
+    @staticmethod
+    def forward(ctx, name, call, *tensors):
+        ctx.name = name
+        ctx.set_materialize_grads(False)
+        return call()
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise NotImplementedError(f"gmm.{ctx.name} has no backward pass: call it on detached tensors or under "
+                                  "torch.no_grad()")
 
 
 @functools.lru_cache(maxsize=4096)
@@ -448,10 +506,15 @@ def linear(X, W, *, bias=None, act: int = ACT_NONE, residual=None, out_dtype=Non
     """Y = act(X W^T + bias) + residual; returns (Y, pre), pre = X W^T + bias or None.
 
     X N x d_in, W d_out x d_in and bias d_out share one type; Y, residual and pre are N x d_out of out_dtype
-    (X's type, the default, or float32)."""
+    (X's type, the default, or float32). Y carries gradients to X, W, bias and residual that require them (first
+    derivatives; pre carries none). A captured step calls linear_backward itself, under torch.no_grad()."""
+    # as _tracked, written out: a one-row call is as long as its host time
+    if _grad_mode() and (X.requires_grad or W.requires_grad or bias is not None and bias.requires_grad
+                         or residual is not None and residual.requires_grad):
+        return _Linear.apply(X, W, bias, residual, act, out_dtype, want_pre, ws)
     N, d_in = _matrix(X, "X")
     dev, t = X.device, X.dtype
-    if dev.index != torch.cuda.current_device():
+    if dev.index != _current_device():
         with torch.cuda.device(dev):
             return linear(X, W, bias=bias, act=act, residual=residual, out_dtype=out_dtype, want_pre=want_pre, ws=ws)
     xt = _xtype(X)
@@ -479,7 +542,7 @@ def linear_backward(dY, X, W, *, pre=None, act: int = ACT_NONE, want_dx: bool = 
     (not needed with ACT_NONE). The residual's gradient is dY."""
     N, d_in = _matrix(X, "X")
     dev, t = X.device, X.dtype
-    if dev.index != torch.cuda.current_device():
+    if dev.index != _current_device():
         with torch.cuda.device(dev):
             return linear_backward(dY, X, W, pre=pre, act=act, want_dx=want_dx, want_dw=want_dw, want_db=want_db,
                                    ws=ws)
@@ -528,9 +591,13 @@ def _experts_args(X, W1, W2, b1, b2, glu, residual):
 def expert_layer(X, P, mu, var, logw, W1, W2, *, b1=None, b2=None, act: int = ACT_SILU, glu: bool = True,
                  top: int = 2, border_threshold: float = 0.0, renorm: bool = False, residual=None, ws=None):
     """Layer of experts gated by the mixture's posterior at P x, for at most 128 rows: returns
-    (Y[N,D], idx[N,top] int32, resp[N,top] float32)."""
+    (Y[N,D], idx[N,top] int32, resp[N,top] float32). It has no backward pass."""
+    if _tracked(X, P, mu, var, logw, W1, W2, b1, b2, residual):
+        return _ForwardOnly.apply("expert_layer", lambda: expert_layer(
+            X, P, mu, var, logw, W1, W2, b1=b1, b2=b2, act=act, glu=glu, top=top, border_threshold=border_threshold,
+            renorm=renorm, residual=residual, ws=ws), X, P, mu, var, logw, W1, W2, b1, b2, residual)
     N, D, K, F, dev, xt = _experts_args(X, W1, W2, b1, b2, glu, residual)
-    if dev.index != torch.cuda.current_device():
+    if dev.index != _current_device():
         with torch.cuda.device(dev):
             return expert_layer(X, P, mu, var, logw, W1, W2, b1=b1, b2=b2, act=act, glu=glu, top=top,
                                 border_threshold=border_threshold, renorm=renorm, residual=residual, ws=ws)
@@ -554,9 +621,13 @@ def expert_layer(X, P, mu, var, logw, W1, W2, *, b1=None, b2=None, act: int = AC
 def expert_rows(X, idx, wts, W1, W2, *, b1=None, b2=None, act: int = ACT_SILU, glu: bool = True, residual=None,
                 ws=None):
     """The experts of expert_layer for given picks (idx N x top int32, wts N x top float32, for instance those of
-    assign_top2): returns Y[N,D]. A pick outside [0, K) is skipped."""
+    assign_top2): returns Y[N,D]. A pick outside [0, K) is skipped. It has no backward pass."""
+    if _tracked(X, wts, W1, W2, b1, b2, residual):
+        return _ForwardOnly.apply("expert_rows", lambda: expert_rows(
+            X, idx, wts, W1, W2, b1=b1, b2=b2, act=act, glu=glu, residual=residual, ws=ws), X, wts, W1, W2, b1, b2,
+            residual)
     N, D, K, F, dev, xt = _experts_args(X, W1, W2, b1, b2, glu, residual)
-    if dev.index != torch.cuda.current_device():
+    if dev.index != _current_device():
         with torch.cuda.device(dev):
             return expert_rows(X, idx, wts, W1, W2, b1=b1, b2=b2, act=act, glu=glu, residual=residual, ws=ws)
     if idx.dim() != 2:
