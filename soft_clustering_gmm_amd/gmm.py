@@ -496,6 +496,15 @@ def _scratch(nbytes, device, what):
     return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
+def _space(ws, device):
+    """(address, bytes) of a caller's workspace."""
+    if ws is None:
+        return None, 0
+    if ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"ws: expected a contiguous tensor on {device}, got {tuple(ws.stride())} on {ws.device}")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
 def linear_workspace(N: int, d_in: int, d_out: int, dtype, device, *, backward: bool = False) -> torch.Tensor:
     """A device workspace for linear (or linear_backward) with operands of this torch dtype."""
     return _scratch(_linear_bytes(N, d_in, d_out, _DTYPES[dtype], int(backward)), device,
@@ -532,7 +541,7 @@ def linear(X, W, *, bias=None, act: int = ACT_NONE, residual=None, out_dtype=Non
         ws = linear_workspace(N, d_in, d_out, t, dev)
     _check("gmm_linear", lib().gmm_linear(
         X.data_ptr(), xt, N, d_in, W.data_ptr(), d_out, _at(bias), act, _at(residual), Y.data_ptr(),
-        _DTYPES[out_dtype], _at(pre), _at(ws), 0 if ws is None else ws.numel(), _raw_stream(dev.index)))
+        _DTYPES[out_dtype], _at(pre), *_space(ws, dev), _raw_stream(dev.index)))
     return Y, pre
 
 
@@ -563,7 +572,7 @@ def linear_backward(dY, X, W, *, pre=None, act: int = ACT_NONE, want_dx: bool = 
         ws = linear_workspace(N, d_in, d_out, t, dev, backward=True)
     _check("gmm_linear_backward", lib().gmm_linear_backward(
         dY.data_ptr(), _DTYPES[yt], X.data_ptr(), xt, N, d_in, W.data_ptr(), d_out, _at(pre), act, _at(dX), _at(dW),
-        _at(db), ws.data_ptr(), ws.numel(), _raw_stream(dev.index)))
+        _at(db), *_space(ws, dev), _raw_stream(dev.index)))
     return dX, dW, db
 
 
@@ -614,7 +623,7 @@ def expert_layer(X, P, mu, var, logw, W1, W2, *, b1=None, b2=None, act: int = AC
     _check("gmm_expert_layer", lib().gmm_expert_layer(
         X.data_ptr(), xt, N, D, P.data_ptr(), d, mu.data_ptr(), var.data_ptr(), logw.data_ptr(), K, top,
         border_threshold, renorm, W1.data_ptr(), _at(b1), W2.data_ptr(), _at(b2), F, act, glu, _at(residual),
-        Y.data_ptr(), idx.data_ptr(), resp.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(dev.index)))
+        Y.data_ptr(), idx.data_ptr(), resp.data_ptr(), *_space(ws, dev), _raw_stream(dev.index)))
     return Y, idx, resp
 
 
@@ -640,7 +649,7 @@ def expert_rows(X, idx, wts, W1, W2, *, b1=None, b2=None, act: int = ACT_SILU, g
     Y = torch.empty(N, D, dtype=X.dtype, device=dev)
     _check("gmm_expert_rows", lib().gmm_expert_rows(
         X.data_ptr(), xt, N, D, idx.data_ptr(), wts.data_ptr(), top, K, W1.data_ptr(), _at(b1), W2.data_ptr(),
-        _at(b2), F, act, glu, _at(residual), Y.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(dev.index)))
+        _at(b2), F, act, glu, _at(residual), Y.data_ptr(), *_space(ws, dev), _raw_stream(dev.index)))
     return Y
 
 
