@@ -16,8 +16,6 @@ namespace gmm {
 
 typedef double f64x4 __attribute__((ext_vector_type(4)));
 
-typedef double f64x4 __attribute__((ext_vector_type(4)));
-
 // c_k = logw_k - 1/2 (d log 2 pi + sum_j log var_kj), 16 components a block of
 // 256 threads, 16 lanes each. The sum is the logarithm of the product of the
 // mantissas (at least 2^-128) and the sum of the exponents: one logarithm a

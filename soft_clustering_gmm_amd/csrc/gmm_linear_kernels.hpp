@@ -57,7 +57,8 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ void load_to_lds(uint32_t lds, uint32_t offset, i32x4 buffer) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                :
-               : "s"(lds), "v"(offset), "s"(buffer));
+               : "s"(lds), "v"(offset), "s"(buffer)
+               : "m0");
 }
 
 // All but the last PENDING loads of this wave have arrived in LDS and its LDS
