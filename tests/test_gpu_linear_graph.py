@@ -90,3 +90,17 @@ def test_experts_say_that_they_have_no_gradients():
         with torch.no_grad():
             assert not G.expert_rows(X, idx, resp, W1, W2, residual=X).requires_grad
         t.requires_grad_(False)
+
+
+@pytest.mark.parametrize("N", [0, 1, 19])
+def test_empty_few_and_unaligned_batches(N):
+    """Rows of odd length from inside a batch, and gradients that start off a 16-byte border."""
+    from soft_clustering_gmm_amd import gmm as G
+    (X, W, b, R), dY = leaves(N + 3, 45, 33, torch.float16, torch.float32)
+    Y, _ = G.linear(X[3:], W, bias=b, act=G.ACT_SILU, residual=R[3:], out_dtype=torch.float32)
+    got = torch.autograd.grad(Y, (X, W, b, R), dY[3:])
+    with torch.no_grad():
+        _, pre = G.linear(X[3:], W, bias=b, act=G.ACT_SILU, out_dtype=torch.float32, want_pre=True)
+        want = G.linear_backward(dY[3:], X[3:], W, pre=pre, act=G.ACT_SILU)
+    assert torch.equal(got[0][3:], want[0]) and (got[0][:3] == 0).all() and torch.equal(got[3][3:], dY[3:])
+    assert torch.equal(got[1], want[1]) and torch.equal(got[2], want[2])
