@@ -380,7 +380,9 @@ size_t gmm_linear_workspace_bytes(int64_t N, int32_t d_in, int32_t d_out, int32_
  * K x F (K x 2F), W2 K x D x F, b2 K x D; b1, b2 and residual are nullable.
  * idx (N x top int32) and resp (N x top float) receive the picks and their r,
  * -1 and 0 for a dropped or missing one. The gate is computed in double
- * precision; a is rounded to x_dtype between the two products. A row whose
+ * precision; a is rounded to x_dtype between the two products, so in half
+ * act(g) u has to stay below 65504. What is not a number in an expert's weights
+ * reaches the rows that picked it and no others. A row whose
  * posterior is not a number (NaN or infinite features) has no picks and a y
  * of NaN. Y may be X or residual itself. The workspace must hold
  * gmm_expert_workspace_bytes(N, D, K, F, d, top, x_dtype) bytes. */

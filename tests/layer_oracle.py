@@ -1,6 +1,6 @@
 """Plain 64-bit forms of the linear layer, its gradients and the layer of experts (on the CPU, or where a test of
-large shapes puts ON), with the error
-bounds that the library's arithmetic allows. Shares no code with the library."""
+large shapes puts ON), with worst-case error bounds of the library's arithmetic (tests/layer_bounds.py has those that
+are relative to the value, and those of the 2-norm). Shares no code with the library."""
 import math
 
 import torch
@@ -8,8 +8,8 @@ import torch
 EPS = {torch.float32: 2.0 ** -23, torch.float16: 2.0 ** -10, torch.bfloat16: 2.0 ** -7}
 TINY = {torch.float32: 2.0 ** -149, torch.float16: 2.0 ** -24, torch.bfloat16: 2.0 ** -133}
 ACTS = ("none", "relu", "gelu", "silu")
-# The functions' own float error: value and slope within 2^-20 of max(1, |z|)
-# (erf and exp within a few units of the last place, times |z| in the argument).
+# The functions' own error: value and slope within 2^-20 of max(1, |z|). That is their bound for float results (2^-20
+# of the value); for results of 2 bytes the tail of the normal distribution is off by half of 6.3e-7 at most.
 FUNCTION = 2.0 ** -20
 
 
@@ -90,7 +90,7 @@ def gradients(dY, X, W, pre, name):
 
 
 def gate(X, P, mu, var, logw, top, threshold, renorm):
-    """(idx, resp, weights, gap): gap is the smallest distance, per row, of a decision of the row from its border."""
+    """(idx, resp, weights) of every row's picks, -1 and 0 for a dropped or missing one."""
     f = wide(X) @ wide(P).T
     m, v = wide(mu), wide(var)
     s = wide(logw) - 0.5 * ((2 * math.pi * v).log().sum(1) + ((f[:, None] - m) ** 2 / v).sum(2))
