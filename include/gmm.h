@@ -348,9 +348,10 @@ int gmm_linear(const void* X, int32_t x_dtype, int64_t N, int32_t d_in, const vo
  * and 1. The products take dZ rounded to x_dtype, as the matrix instructions
  * do, and accumulate in float; for half operands and a float dY it is scaled
  * by a power of two first, set by its largest finite value and taken back from
- * the sums, so that a dY of any size keeps half's 11 bits (a half dY is taken
- * as it is, in half's range). db sums the unrounded dZ in float. Sums run in a
- * fixed order. N = 0 gives dW = 0 and db = 0. Alignment of X and W as above. The
+ * the sums, so that it keeps half's 11 bits down to 2^-29 of that value
+ * whatever the size of dY (a half dY is taken as it is, in half's range). db
+ * sums the unrounded dZ in float. Sums run in a fixed order. N = 0 gives dW = 0
+ * and db = 0. Alignment of X and W as above. The
  * workspace must hold gmm_linear_workspace_bytes(N, d_in, d_out, x_dtype, 1)
  * bytes. */
 int gmm_linear_backward(const void* dY, int32_t y_dtype, const void* X, int32_t x_dtype, int64_t N, int32_t d_in,

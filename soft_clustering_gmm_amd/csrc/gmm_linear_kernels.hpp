@@ -645,9 +645,10 @@ dz_range_kernel(const float* __restrict__ dY, const float* __restrict__ pre, int
   }
 }
 
-// The power of two that brings the largest of `range` into [2^13, 2^14), in every
-// thread of a block of kRangeBlocks: half then holds dZ with its 11 bits down to
-// 2^-28 of the largest, wherever dY lies, and nothing overflows. 1 for no values.
+// The exponent of the largest power of two that keeps the largest of `range`
+// within half's 65504, in every thread of a block of kRangeBlocks: half then
+// holds dZ with its 11 bits down to 2^-29 of the largest, wherever dY lies, and
+// what half holds as it is loses nothing. 0 for no values.
 __device__ __forceinline__ int dz_scale(const float* range) {
   __shared__ float red[kRangeBlocks / 64];
   float most = range[threadIdx.x];
@@ -659,8 +660,8 @@ __device__ __forceinline__ int dz_scale(const float* range) {
   for (int w = 0; w < kRangeBlocks / 64; ++w) most = fmaxf(most, red[w]);
   if (!(most > 0.f)) return 0;
   int e;
-  frexpf(most, &e);
-  return min(126, max(-126, 14 - e));  // the scale and its inverse are normal
+  const float m = frexpf(most, &e);
+  return min(126, max(-126, (m > 65504.f / 65536.f ? 15 : 16) - e));  // the scale and its inverse are normal
 }
 
 // dZ and the column sums of a chunk of rows. A thread owns V consecutive

@@ -27,8 +27,8 @@ def check(got, dY, X, W, pre, name):
         z = oracle.wide(pre)
         fn = dz.abs() * oracle.FUNCTION * z.abs().clamp(min=1.0)
         dz = dz * oracle.slope(z, name)
-    # scaled so that the largest lies in [2^13, 2^14): half a step of 2^-11, and of the smallest step, 2^-24
-    per = dz.abs() * 2.0 ** -11 + dz.abs().max() * 2.0 ** -38 + fn + 2.0 ** -23 * dz.abs()
+    # scaled so that the largest lies above 32752: half a step of 2^-11, and of the smallest step, 2^-24
+    per = dz.abs() * 2.0 ** -11 + dz.abs().max() * 2.0 ** -39 + fn + 2.0 ** -23 * dz.abs()
     want = (dz @ w, dz.T @ x, dz.sum(0))
     bound = (per @ w.abs() + oracle.sum_bound(dz.abs() + per, w.T, w.shape[0]),
              per.T @ x.abs() + oracle.sum_bound((dz.abs() + per).T, x.T, x.shape[0]),
@@ -60,6 +60,22 @@ def test_float_dy_of_any_size(N, d_in, d_out, size, name):
     one = G.linear_backward(dY, X, W, pre=pre, act=act, want_dw=False, want_db=False)
     two = G.linear_backward(dY, X, W, pre=pre, act=act, want_dx=False, want_db=False)
     assert torch.equal(one[0], got[0]) and torch.equal(two[1], got[1])
+
+
+@pytest.mark.parametrize("largest", [65504.0, 65472.0, 32768.0, 32767.0, 30000.0, 9000.0, 1.0])
+def test_what_half_holds_is_not_rounded_more(largest):
+    """dX by a weight of ones on the diagonal is dZ itself: a float dY within half's range comes back as half rounds it,
+    small values beside large ones too."""
+    from soft_clustering_gmm_amd import gmm as G
+    n = 64
+    g = torch.Generator().manual_seed(3)
+    dY = (torch.randn(40, n, generator=g) * torch.logspace(-7, 0, 40)[:, None]).clamp(-largest, largest)
+    dY[5, 7] = largest
+    X, W = torch.ones(40, n, dtype=HALF), torch.eye(n, dtype=HALF)
+    dX, _, _ = G.linear_backward(dY.cuda(), X.cuda(), W.cuda())
+    # a dY above half's smallest normal value comes back exactly; smaller ones keep at least half's steps
+    off = (dX.cpu().double() - dY.double()).abs()
+    assert (off <= (dY.half().double() - dY.double()).abs() + 2.0 ** -25 * (dY.abs() < 2.0 ** -14)).all()
 
 
 def test_no_and_infinite_values():
