@@ -408,6 +408,82 @@ int gmm_expert_rows(const void* X, int32_t x_dtype, int64_t N, int32_t D, const 
 size_t gmm_expert_workspace_bytes(int64_t N, int32_t D, int32_t K, int32_t F, int32_t d, int32_t top,
                                   int32_t x_dtype);
 
+/* ---------------------------------------------------------------------------
+ * A training step of what stands around the mixture: the norm between linear
+ * layers, the loss of a linear head on the mixture's picks with its gradients,
+ * and the update of the parameters. Conventions as above. */
+
+/* Layer norm:
+ *   mean = sum x / D,  rstd = 1 / sqrt(sum (x - mean)^2 / D + eps)
+ *   y = (x - mean) rstd gamma + beta
+ * X and Y are N x D, 1 <= D <= 65536, N <= 2^30. y_dtype is x_dtype, or any
+ * type where x_dtype is GMM_F32 (a float residual stream in front of half or
+ * bfloat16 products). gamma and beta (D) have type w_dtype, which is y_dtype or
+ * GMM_F32; each is nullable (1 and 0). stats (nullable, N x 2 float) receives
+ * mean and rstd, which the backward call needs. eps > 0. Arithmetic is float
+ * (the squares of a row's deviations have to sum to less than 3.4e38), rounded
+ * once per output; rows may start at any element. What is not finite in a row
+ * reaches that row alone. Y may be X itself where their types agree. */
+int gmm_layer_norm(const void* X, int32_t x_dtype, int64_t N, int32_t D, const void* gamma, const void* beta,
+                   int32_t w_dtype, float eps, void* Y, int32_t y_dtype, float* stats, void* stream);
+
+/* Gradients of gmm_layer_norm for dY (N x D of y_dtype) and the stats that the
+ * forward call wrote. With h = (x - mean) rstd and k = dY gamma:
+ *   dX = rstd (k - mean(k) - h mean(k h)),  dgamma = sum_n dY h,  dbeta = sum_n dY
+ * dX (N x D of x_dtype), dgamma and dbeta (D of w_dtype) are each nullable; dX
+ * may be X itself, or dY where their types agree. Sums are float and run in a fixed
+ * order. N = 0 gives dgamma = 0 and dbeta = 0. The workspace must hold
+ * gmm_layer_norm_workspace_bytes(N, D, x_dtype) bytes; without dgamma and dbeta
+ * it may be NULL. */
+int gmm_layer_norm_backward(const void* dY, int32_t y_dtype, const void* X, int32_t x_dtype, int64_t N, int32_t D,
+                            const float* stats, const void* gamma, int32_t w_dtype, void* dX, void* dgamma, void* dbeta,
+                            void* workspace, size_t ws_bytes, void* stream);
+
+/* Workspace bytes for gmm_layer_norm_backward; 0 for arguments outside the limits. */
+size_t gmm_layer_norm_workspace_bytes(int64_t N, int32_t D, int32_t x_dtype);
+
+/* One AdamW step over `count` tensors, in place. With g = grad * *grad_factor
+ * and the step's number n (from 1):
+ *   m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2
+ *   p = p - l weight_decay p - l (m / (1 - beta1^n)) / (sqrt(v / (1 - beta2^n)) + eps)
+ * with l = lr * *lr_factor. sizes, params and grads are HOST arrays of `count`
+ * entries (read before the call returns): elements, parameter (p_dtype,
+ * device) and gradient (g_dtype, which is p_dtype or GMM_F32) of each tensor, at
+ * any element's address. A tensor whose gradient is NULL is left as it is, state
+ * included. lr_factor and grad_factor are device floats, NULL for 1; they and
+ * step are what may change between the replays of a captured call.
+ *
+ * The state of all tensors lies behind one another: the part of a tensor starts
+ * at a multiple of 256 elements, in the tensors' order, and
+ * gmm_adamw_state_elements() elements hold them all; what lies between two parts
+ * is not touched. m and v are arrays of state_bits = 32 (float) or 8. master
+ * (float, nullable) holds the parameters as float: with it the step is taken
+ * there, and params receive its rounding. With 8 bits, m and sqrt(v) are held in
+ * e4m3 and m_scale and v_scale (a float for each 256 elements of the state)
+ * hold their scales, the block's largest finite value / 448; an entry that is not
+ * finite is held as NaN and reaches no other, one of v that is not 0 is held as
+ * 2^-9 scale at least, and blocks below 1e-35 are held as 0. Which neighbour a
+ * value is rounded to is decided by 16 bits of a hash of the element's place
+ * and the step's number, in proportion to the distances (rounded to the nearest,
+ * a moving average would not move): x = place ^ (n * 0x9E3779B1) in 32 bits,
+ * x = (x ^ x >> 16) * 0x7FEB352D, x = (x ^ x >> 15) * 0x846CA68B, x ^= x >> 16;
+ * the low half is m's, the high half v's, and the larger neighbour is taken where
+ * the half / 65536 and the share beyond the smaller come to 1 or more. The step
+ * itself is taken from the unrounded m and v.
+ *
+ * step (device, 2 int64, 8-byte aligned) holds the number of steps done, which the
+ * call counts up by one, and a word for the library's own use that has to be 0 between calls. All
+ * arithmetic is float, the powers of beta double. m, v and master are 16-byte
+ * aligned. beta1 and beta2 from 0 to below 1, eps > 0, lr and weight_decay >= 0.
+ * No parameter may overlap another tensor of the call. */
+int gmm_adamw_step(int32_t count, const int64_t* sizes, void* const* params, int32_t p_dtype,
+                   const void* const* grads, int32_t g_dtype, float* master, void* m, void* v, int32_t state_bits,
+                   float* m_scale, float* v_scale, int64_t* step, double lr, double beta1, double beta2, double eps,
+                   double weight_decay, const float* lr_factor, const float* grad_factor, void* stream);
+
+/* Elements of the state of `count` tensors (a multiple of 256); -1 for a negative count or size. */
+int64_t gmm_adamw_state_elements(int32_t count, const int64_t* sizes);
+
 #ifdef __cplusplus
 }
 #endif

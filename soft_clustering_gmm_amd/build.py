@@ -14,7 +14,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libgmm_mi355x.so")
 SOURCES = ["gmm_kernels.hip", "gmm_lists.hip", "gmm_api.cpp", "gmm_peaks.hip",
-           "gmm_layers_api.cpp", *(f"gmm_{k}_{t}.hip" for k in ("linear", "experts") for t in ("f32", "f16", "bf16"))]
+           "gmm_layers_api.cpp", "gmm_training_api.cpp", "gmm_adamw.hip",
+           *(f"gmm_{k}_{t}.hip" for k in ("linear", "experts", "norm") for t in ("f32", "f16", "bf16"))]
 ARCH = "gfx950"
 
 # Packed fp32 VALU ops are disabled for all device code; the kernels' fp32

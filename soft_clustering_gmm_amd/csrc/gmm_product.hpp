@@ -1,5 +1,5 @@
-// Device code shared by the product kernels (the linear layer and the layer
-// of experts): element types, matrix instructions, activations.
+// Device code shared by the kernels of the layers: element types, loads and
+// stores, matrix instructions, activations.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -236,6 +236,68 @@ __device__ __forceinline__ u32x4 load_frag(const T* p, int n) {
 #pragma unroll
   for (int i = 0; i < Frag<T>::kPer; ++i) u.e[i] = i < n ? p[i] : (T)0.f;
   return u.v;
+}
+
+// W consecutive values of a row, n of them inside it, as floats; whole ones in
+// 16-byte accesses of any alignment.
+template <typename E, int W>
+__device__ __forceinline__ void load_as(const E* q, int n, float* out) {
+  constexpr int P = 16 / sizeof(E) < W ? 16 / sizeof(E) : W;
+  if (n >= W) {
+#pragma unroll
+    for (int i = 0; i < W; i += P) {
+      E e[P];
+      __builtin_memcpy(e, q + i, sizeof(e));
+#pragma unroll
+      for (int k = 0; k < P; ++k) out[i + k] = (float)e[k];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < W; ++i) out[i] = i < n ? (float)q[i] : 0.f;
+  }
+}
+
+// STREAM: past the caches' replacement, for what is too large to be found there.
+template <typename E, int W, bool STREAM = false>
+__device__ __forceinline__ void store_as(E* q, int n, const float* v) {
+  constexpr int P = 16 / sizeof(E) < W ? 16 / sizeof(E) : W;
+  if (n >= W) {
+#pragma unroll
+    for (int i = 0; i < W; i += P) {
+      E e[P];
+#pragma unroll
+      for (int k = 0; k < P; ++k) e[k] = (E)v[i + k];
+      if constexpr (STREAM && sizeof(e) == 16) {
+        typedef u32x4 any_u32x4 __attribute__((aligned(2)));
+        u32x4 w;
+        __builtin_memcpy(&w, e, 16);
+        __builtin_nontemporal_store(w, reinterpret_cast<any_u32x4*>(q + i));
+      } else {
+        __builtin_memcpy(q + i, e, sizeof(e));
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+      if (i < n) q[i] = (E)v[i];
+  }
+}
+
+// The same at element `at` of an array of C's type.
+template <typename T, int W>
+__device__ __forceinline__ void load_row(const void* p, int64_t at, int n, bool is_f32, float* out) {
+  if (is_f32)
+    load_as<float, W>(static_cast<const float*>(p) + at, n, out);
+  else
+    load_as<T, W>(static_cast<const T*>(p) + at, n, out);
+}
+
+template <typename T, int W, bool STREAM = false>
+__device__ __forceinline__ void store_row(void* p, int64_t at, int n, bool is_f32, const float* v) {
+  if (is_f32)
+    store_as<float, W, STREAM>(static_cast<float*>(p) + at, n, v);
+  else
+    store_as<T, W, STREAM>(static_cast<T*>(p) + at, n, v);
 }
 
 // A stream over weights with a few rows beside them: NT * 16 rows of B (at

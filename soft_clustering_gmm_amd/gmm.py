@@ -32,6 +32,8 @@ EXPORTS = (
     "gmm_plan_info", "gmm_estep_stats_static",
     "gmm_linear", "gmm_linear_backward", "gmm_linear_workspace_bytes",
     "gmm_expert_layer", "gmm_expert_rows", "gmm_expert_workspace_bytes",
+    "gmm_layer_norm", "gmm_layer_norm_backward", "gmm_layer_norm_workspace_bytes",
+    "gmm_adamw_step", "gmm_adamw_state_elements",
     "gmm_peak_mfma", "gmm_peak_mfma_flops", "gmm_peak_hbm_read", "gmm_peak_coissue",
 )
 PEAK_FP32, PEAK_FP64 = 0, 1
@@ -49,6 +51,7 @@ def _load() -> ctypes.CDLL:
                            "(or __graft_entry__.build()); there is no fallback path")
     L = ctypes.CDLL(LIB_PATH)
     P, I32, I64, SZ, F32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
+    F64 = ctypes.c_double
     L.gmm_version.restype = ctypes.c_int
     L.gmm_version.argtypes = []
     L.gmm_error_string.restype = ctypes.c_char_p
@@ -112,6 +115,16 @@ def _load() -> ctypes.CDLL:
     L.gmm_expert_rows.argtypes = [P, I32, I64, I32, P, P, I32, I32, P, P, P, P, I32, I32, I32, P, P, P, SZ, P]
     L.gmm_expert_workspace_bytes.restype = SZ
     L.gmm_expert_workspace_bytes.argtypes = [I64, I32, I32, I32, I32, I32, I32]
+    L.gmm_layer_norm.restype = ctypes.c_int
+    L.gmm_layer_norm.argtypes = [P, I32, I64, I32, P, P, I32, F32, P, I32, P, P]
+    L.gmm_layer_norm_backward.restype = ctypes.c_int
+    L.gmm_layer_norm_backward.argtypes = [P, I32, P, I32, I64, I32, P, P, I32, P, P, P, P, SZ, P]
+    L.gmm_layer_norm_workspace_bytes.restype = SZ
+    L.gmm_layer_norm_workspace_bytes.argtypes = [I64, I32, I32]
+    L.gmm_adamw_step.restype = ctypes.c_int
+    L.gmm_adamw_step.argtypes = [I32, P, P, I32, P, I32, P, P, P, I32, P, P, P, F64, F64, F64, F64, F64, P, P, P]
+    L.gmm_adamw_state_elements.restype = I64
+    L.gmm_adamw_state_elements.argtypes = [I32, P]
     return L
 
 
@@ -651,6 +664,213 @@ def expert_rows(X, idx, wts, W1, W2, *, b1=None, b2=None, act: int = ACT_SILU, g
         X.data_ptr(), xt, N, D, idx.data_ptr(), wts.data_ptr(), top, K, W1.data_ptr(), _at(b1), W2.data_ptr(),
         _at(b2), F, act, glu, _at(residual), Y.data_ptr(), *_space(ws, dev), _raw_stream(dev.index)))
     return Y
+
+
+class _LayerNorm(torch.autograd.Function):
+    """layer_norm in torch's graph: its backward pass is layer_norm_backward."""
+
+    @staticmethod
+    def forward(ctx, X, gamma, beta, eps, out_dtype, want_stats):
+        Y, stats = layer_norm(X, gamma, beta, eps=eps, out_dtype=out_dtype, want_stats=True)
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(X, gamma, stats)
+        ctx.weights = next((t.dtype for t in (gamma, beta) if t is not None), None)
+        if not want_stats:
+            return Y, None
+        ctx.mark_non_differentiable(stats)
+        return Y, stats
+
+    @staticmethod
+    def backward(ctx, dY, _):
+        if torch.is_grad_enabled():  # create_graph: the gradients would count as constants
+            raise NotImplementedError("gmm.layer_norm has no second derivatives")
+        grads = (None, None, None)
+        if dY is not None:
+            X, gamma, stats = ctx.saved_tensors
+            need = ctx.needs_input_grad
+            grads = layer_norm_backward(dY.contiguous(), X, stats, gamma, want_dx=need[0], want_dgamma=need[1],
+                                        want_dbeta=need[2], param_dtype=ctx.weights)
+        return (*grads, None, None, None)
+
+
+def layer_norm(X, gamma=None, beta=None, *, eps: float = 1e-5, out_dtype=None, want_stats: bool = False):
+    """Y = (x - mean) / sqrt(var + eps) gamma + beta over the rows of X; returns (Y, stats), stats N x 2 float32 (mean
+    and 1 / sqrt(var + eps)) or None.
+
+    X and Y are N x D, Y of out_dtype (X's type, the default, or any where X is float32); gamma and beta (1 and 0 where
+    None) share a type, Y's or float32. Y carries gradients to X, gamma and beta (first derivatives). A captured step
+    calls layer_norm_backward itself, under torch.no_grad()."""
+    if _tracked(X, gamma, beta):
+        return _LayerNorm.apply(X, gamma, beta, eps, out_dtype, want_stats)
+    N, D = _matrix(X, "X")
+    dev = X.device
+    if dev.index != _current_device():
+        with torch.cuda.device(dev):
+            return layer_norm(X, gamma, beta, eps=eps, out_dtype=out_dtype, want_stats=want_stats)
+    xt = _xtype(X)
+    if out_dtype is None:
+        out_dtype = X.dtype
+    elif out_dtype != X.dtype and (xt != GMM_F32 or out_dtype not in _DTYPES):
+        raise ValueError(f"out_dtype must be {X.dtype}{'' if xt else ', float16 or bfloat16'}, got {out_dtype}")
+    wt = _norm_weights(gamma, beta, out_dtype, D, dev)
+    Y = torch.empty(N, D, dtype=out_dtype, device=dev)
+    stats = torch.empty(N, 2, dtype=torch.float32, device=dev) if want_stats else None
+    _check("gmm_layer_norm", lib().gmm_layer_norm(
+        X.data_ptr(), xt, N, D, _at(gamma), _at(beta), wt, eps, Y.data_ptr(), _DTYPES[out_dtype], _at(stats),
+        _raw_stream(dev.index)))
+    return Y, stats
+
+
+def _norm_weights(gamma, beta, y_dtype, D, dev, dtype=None):
+    """The type of a layer norm's weights, which are checked."""
+    if dtype is None:
+        dtype = gamma.dtype if gamma is not None else beta.dtype if beta is not None else y_dtype
+    if dtype != y_dtype and dtype != torch.float32:
+        raise ValueError(f"gamma and beta must be {y_dtype} or float32, got {dtype}")
+    _optional(gamma, "gamma", dtype, (D,), dev)
+    _optional(beta, "beta", dtype, (D,), dev)
+    return _DTYPES[dtype]
+
+
+@functools.lru_cache(maxsize=4096)
+def _norm_bytes(N, D, x_dtype):
+    return int(lib().gmm_layer_norm_workspace_bytes(N, D, x_dtype))
+
+
+def layer_norm_workspace(N: int, D: int, dtype, device) -> torch.Tensor:
+    """A device workspace for layer_norm_backward with X of this torch dtype."""
+    return _scratch(_norm_bytes(N, D, _DTYPES[dtype]), device, f"N={N} D={D}")
+
+
+def layer_norm_backward(dY, X, stats, gamma=None, *, want_dx: bool = True, want_dgamma: bool = True,
+                        want_dbeta: bool = True, param_dtype=None, ws=None):
+    """Gradients of layer_norm: (dX, dgamma, dbeta), None for what is not wanted. stats is layer_norm's second result.
+    dX has X's type, dgamma and dbeta that of gamma (param_dtype, or dY's type, where gamma is None)."""
+    N, D = _matrix(X, "X")
+    dev = X.device
+    if dev.index != _current_device():
+        with torch.cuda.device(dev):
+            return layer_norm_backward(dY, X, stats, gamma, want_dx=want_dx, want_dgamma=want_dgamma,
+                                       want_dbeta=want_dbeta, param_dtype=param_dtype, ws=ws)
+    xt = _xtype(X)
+    if dY.dtype != X.dtype and (xt != GMM_F32 or dY.dtype not in _DTYPES):
+        raise ValueError(f"dY must be {X.dtype}{'' if xt else ', float16 or bfloat16'}, got {dY.dtype}")
+    _need(dY, "dY", dY.dtype, (N, D), dev)
+    _need(stats, "stats", torch.float32, (N, 2), dev)
+    if gamma is not None:
+        param_dtype = gamma.dtype
+    elif param_dtype is None:
+        param_dtype = dY.dtype
+    wt = _norm_weights(gamma, None, dY.dtype, D, dev, param_dtype)
+    dX = torch.empty_like(X) if want_dx else None
+    dgamma = torch.empty(D, dtype=param_dtype, device=dev) if want_dgamma else None
+    dbeta = torch.empty(D, dtype=param_dtype, device=dev) if want_dbeta else None
+    if ws is None and (want_dgamma or want_dbeta):
+        ws = layer_norm_workspace(N, D, X.dtype, dev)
+    _check("gmm_layer_norm_backward", lib().gmm_layer_norm_backward(
+        dY.data_ptr(), _DTYPES[dY.dtype], X.data_ptr(), xt, N, D, stats.data_ptr(), _at(gamma), wt, _at(dX),
+        _at(dgamma), _at(dbeta), *_space(ws, dev), _raw_stream(dev.index)))
+    return dX, dgamma, dbeta
+
+
+ADAMW_BLOCK = 256  # elements of adamw_step's state that share a scale; each tensor's part starts at a multiple
+
+
+def _state_elements(params):
+    return sum(-(-p.numel() // ADAMW_BLOCK) for p in params) * ADAMW_BLOCK
+
+
+def adamw_state(params, *, bits: int = 32, master: bool = False) -> dict:
+    """A fresh state of adamw_step for these parameters, as the keyword arguments that it takes: m, v, step, for 8 bits
+    m_scale and v_scale, and with `master` float32 copies of the parameters. A tensor's part of m, v and master starts
+    at the next multiple of 256 elements."""
+    params = list(params)
+    if bits not in (8, 32):
+        raise ValueError(f"bits must be 8 or 32, got {bits}")
+    if not params:
+        raise ValueError("no parameters")
+    dev, total = params[0].device, _state_elements(params)
+    state = {k: torch.zeros(total, dtype=torch.float32 if bits == 32 else torch.uint8, device=dev) for k in ("m", "v")}
+    state["step"] = torch.zeros(2, dtype=torch.int64, device=dev)
+    if bits == 8:
+        state = {k: t.view(torch.float8_e4m3fn) if t.dtype == torch.uint8 else t for k, t in state.items()}
+        for k in ("m_scale", "v_scale"):
+            state[k] = torch.zeros(total // ADAMW_BLOCK, dtype=torch.float32, device=dev)
+    if master:
+        state["master"] = torch.zeros(total, dtype=torch.float32, device=dev)
+        at = 0
+        for p in params:
+            state["master"][at:at + p.numel()] = p.detach().reshape(-1)
+            at += -(-p.numel() // ADAMW_BLOCK) * ADAMW_BLOCK
+    return state
+
+
+def _device_factor(t, name, device):
+    if t is not None and (t.dtype != torch.float32 or t.numel() != 1 or t.device != device):
+        raise ValueError(f"{name}: expected one float32 on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return _at(t)
+
+
+def adamw_step(params, grads, m, v, step, *, m_scale=None, v_scale=None, master=None, lr: float = 1e-3,
+               beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8, weight_decay: float = 0.01,
+               lr_factor=None, grad_factor=None) -> None:
+    """One AdamW step in place over many parameters of one type (contiguous, on one GPU), whose gradients (None: left as
+    it is) have their type or float32. m, v, step, m_scale, v_scale and master are those of adamw_state; m and v are
+    float32, or float8_e4m3fn with scales for each 256 elements. With master the float32 copies are updated and the
+    parameters receive their rounding. lr_factor and grad_factor (one float32 each, on the GPU) multiply lr and the
+    gradients and may change between the replays of a captured step, as step does."""
+    n = len(params)
+    if len(grads) != n:
+        raise ValueError(f"{n} parameters and {len(grads)} gradients")
+    dev = m.device
+    if dev.type != "cuda":
+        raise ValueError("the state must be on the GPU")
+    if dev.index != _current_device():
+        with torch.cuda.device(dev):
+            return adamw_step(params, grads, m, v, step, m_scale=m_scale, v_scale=v_scale, master=master, lr=lr,
+                              beta1=beta1, beta2=beta2, eps=eps, weight_decay=weight_decay, lr_factor=lr_factor,
+                              grad_factor=grad_factor)
+    pt = params[0].dtype if n else torch.float32
+    gt = next((g.dtype for g in grads if g is not None), pt)
+    if pt not in _DTYPES or gt != pt and gt != torch.float32:
+        raise ValueError(f"parameters must be float32, float16 or bfloat16 and gradients theirs or float32, got {pt}, {gt}")
+    sizes, at, spans = [], [], []
+    for p, g in zip(params, grads):
+        if p.dtype != pt or p.device != dev or not p.is_contiguous():
+            raise ValueError(f"parameter: expected contiguous {pt} on {dev}, got {p.dtype} {tuple(p.shape)} on {p.device}")
+        sizes.append(p.numel())
+        at.append(p.data_ptr())
+        if g is not None and (g.dtype != gt or g.shape != p.shape or g.device != dev or not g.is_contiguous()):
+            raise ValueError(f"gradient: expected contiguous {gt} {tuple(p.shape)} on {dev}, got {g.dtype} "
+                             f"{tuple(g.shape)} on {g.device}")
+    e = pt.itemsize
+    spans = sorted((a, k) for a, k in zip(at, sizes) if k)
+    for (a, k), (b, _) in zip(spans, spans[1:]):
+        if a + k * e > b:
+            raise ValueError("two parameters share memory")
+    total = _state_elements(params)
+    st = m.dtype
+    if st != torch.float32 and st != torch.float8_e4m3fn:
+        raise ValueError(f"m must be float32 or float8_e4m3fn, got {st}")
+    _need(m, "m", st, (total,), dev)
+    _need(v, "v", st, (total,), dev)
+    _need(step, "step", torch.int64, (2,), dev)
+    if st != torch.float32:
+        if m_scale is None or v_scale is None:
+            raise ValueError("states of 8 bits need m_scale and v_scale")
+        _need(m_scale, "m_scale", torch.float32, (total // ADAMW_BLOCK,), dev)
+        _need(v_scale, "v_scale", torch.float32, (total // ADAMW_BLOCK,), dev)
+    _optional(master, "master", torch.float32, (total,), dev)
+    if master is not None and pt == torch.float32:
+        raise ValueError("float32 parameters have no master copies")
+    _check("gmm_adamw_step", lib().gmm_adamw_step(
+        n, (ctypes.c_int64 * n)(*sizes), (ctypes.c_void_p * n)(*at), _DTYPES[pt],
+        (ctypes.c_void_p * n)(*[None if g is None else g.data_ptr() for g in grads]), _DTYPES[gt], _at(master),
+        m.data_ptr(), v.data_ptr(), 32 if st == torch.float32 else 8, _at(m_scale), _at(v_scale), step.data_ptr(), lr,
+        beta1, beta2, eps, weight_decay, _device_factor(lr_factor, "lr_factor", dev),
+        _device_factor(grad_factor, "grad_factor", dev), _raw_stream(dev.index)))
+    # a graph that has saved a parameter says so when it comes to it
+    torch.autograd.graph.increment_version([p for p, g in zip(params, grads) if g is not None])
 
 
 def peak_mfma(precision: int, trips: int, blocks: int, out: torch.Tensor) -> float:
