@@ -442,6 +442,48 @@ int gmm_layer_norm_backward(const void* dY, int32_t y_dtype, const void* X, int3
 /* Workspace bytes for gmm_layer_norm_backward; 0 for arguments outside the limits. */
 size_t gmm_layer_norm_workspace_bytes(int64_t N, int32_t D, int32_t x_dtype);
 
+/* Cross entropy of a linear head against the mixture's picks. V classes, of
+ * which row n picks `top` (1..8) as gmm_assign_top2 or gmm_kmeans_assign do:
+ *   z = X W^T + bias,  lse_n = log sum_v exp(z_nv),
+ *   loss_n = sum_j w_nj (lse_n - z_n,idx_nj)
+ * X is N x d_in, W V x d_in, bias (nullable) V, all of x_dtype; idx is N x top
+ * int32, wts N x top float (nullable: 1). A pick outside [0, V) or of weight 0
+ * counts for nothing; a row may pick a class more than once, and a row of no
+ * picks has a loss of 0. loss and lse (nullable) receive N floats. The logits
+ * are not written to memory (up to 16 rows, whose logits are, excepted): the
+ * tiles of the product leave the largest and the sum of each row's columns.
+ * Products and sums are float. A bias of -infinity takes a class out. A logit that is NaN or
+ * +infinity, or only -infinity, make the row's lse and loss NaN (lse -infinity in
+ * the last case).
+ * 1 <= V <= 2^20, N <= 2^30; alignment of X and W as in gmm_linear. The workspace
+ * must hold gmm_cross_entropy_workspace_bytes(N, d_in, V, x_dtype, 0) bytes. */
+int gmm_cross_entropy(const void* X, int32_t x_dtype, int64_t N, int32_t d_in, const void* W, int32_t V,
+                      const void* bias, const int32_t* idx, const float* wts, int32_t top, float* loss, float* lse,
+                      void* workspace, size_t ws_bytes, void* stream);
+
+/* The same with the gradients of sum_n dloss_n loss_n (dloss nullable: 1) in one
+ * call, each logit computed once. With p = exp(z - lse) and s_n = sum_j w_nj:
+ *   G_nv = dloss_n (s_n p_nv - sum_j w_nj [idx_nj = v]),
+ *   dX = G W,  dW = G^T X,  db = sum_n G_n
+ * dX (N x d_in), dW (V x d_in) and db (V) have type x_dtype; each is nullable, as
+ * lse is. A row of no picks, or whose dloss is 0, has no part in the gradients,
+ * whatever its X holds. The logits and G pass through the workspace in pieces of
+ * rows, of at most 2 GiB of logits (256 rows at least). The products take G rounded to
+ * x_dtype, as the matrix instructions do, and accumulate in float; 2-byte operands
+ * take it scaled so that the largest |dloss_n| sum_j |w_nj| becomes 2^14, which is
+ * taken back from the sums, so that half keeps its 11 bits down to 2^-28 of
+ * that whatever its size. db sums the rounded G. Sums run in a fixed order. N = 0
+ * gives dW = 0 and db = 0. The workspace must hold
+ * gmm_cross_entropy_workspace_bytes(N, d_in, V, x_dtype, 1) bytes. */
+int gmm_cross_entropy_gradients(const float* dloss, const void* X, int32_t x_dtype, int64_t N, int32_t d_in,
+                                const void* W, int32_t V, const void* bias, const int32_t* idx, const float* wts,
+                                int32_t top, float* loss, float* lse, void* dX, void* dW, void* db, void* workspace,
+                                size_t ws_bytes, void* stream);
+
+/* Workspace bytes for gmm_cross_entropy (gradients = 0) or
+ * gmm_cross_entropy_gradients (1); 0 for arguments outside the limits. */
+size_t gmm_cross_entropy_workspace_bytes(int64_t N, int32_t d_in, int32_t V, int32_t x_dtype, int32_t gradients);
+
 /* One AdamW step over `count` tensors, in place. With g = grad * *grad_factor
  * and the step's number n (from 1):
  *   m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2

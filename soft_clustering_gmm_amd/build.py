@@ -15,7 +15,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libgmm_mi355x.so")
 SOURCES = ["gmm_kernels.hip", "gmm_lists.hip", "gmm_api.cpp", "gmm_peaks.hip",
            "gmm_layers_api.cpp", "gmm_training_api.cpp", "gmm_adamw.hip",
-           *(f"gmm_{k}_{t}.hip" for k in ("linear", "experts", "norm") for t in ("f32", "f16", "bf16"))]
+           *(f"gmm_{k}_{t}.hip" for k in ("linear", "experts", "norm", "entropy") for t in ("f32", "f16", "bf16"))]
 ARCH = "gfx950"
 
 # Packed fp32 VALU ops are disabled for all device code; the kernels' fp32

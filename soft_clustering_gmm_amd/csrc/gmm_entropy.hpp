@@ -1,0 +1,70 @@
+// Internal declarations of the cross entropy of a linear head
+// (gmm_cross_entropy, gmm_cross_entropy_gradients).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace gmm {
+
+constexpr int kMaxPicksRow = 8;        // picks of a row
+constexpr int64_t kMaxClasses = 1 << 20;
+constexpr int kEntropyRange = 256;     // parts of the largest gradient of a row
+
+// What the gradient of a row's logits takes: G = up exp(z - base) - d (weights
+// of the picks), and 0 where d is.
+struct RowCoef {
+  float base, up, d, unused;
+};
+
+// Rows of a call, or of a piece of it.
+struct EntropyArgs {
+  const void* X;         // [rows][d_in]
+  const void* W;         // [V][d_in]
+  const void* bias;      // [V] or null
+  const int32_t* idx;    // [rows][top]
+  const float* wts;      // [rows][top] or null: 1
+  const float* dloss;    // [rows] or null: 1
+  int64_t rows;
+  int d_in, V, top;
+  float *loss, *lse;     // [rows], lse nullable
+  const float* stats;    // [rows][groups][2] of a kRowStats product, or null: from the logits
+  int groups;
+  const float* Z;        // [rows][ldz] logits, or null: the picks' are computed from X and W
+  void* G;               // [rows][ldz] their gradient in the operands' type
+  int64_t ldz;           // a multiple of 8
+  RowCoef* coef;         // [rows], or null: no gradient
+  float* range;          // [kEntropyRange] and G's scale's inverse behind; null: no scale
+  float* parts;          // [chunks][V] column sums of G, or null
+  int64_t chunk;         // rows of a chunk
+};
+
+// Work before the products, in one launch: copies of rows of whole pieces of
+// 16 bytes of X and of W (no rows: none), a copy of X with zeros for the rows
+// that have no gradient, and the parts of `range` over `all_rows` rows.
+struct EntropyPrep {
+  const void* X;
+  void *x, *clean;       // [rows][ld] each, or null
+  int64_t rows;
+  const void* W;
+  void* w;               // [V][ld], or null
+  int64_t ld;
+  int64_t all_rows;      // 0: no range
+  // the picks and losses of all rows, and the first row of X among them
+  const int32_t* idx;
+  const float *wts, *dloss;
+  int64_t first;
+  float* range;
+  int d_in, V, top;
+};
+
+template <typename T>
+hipError_t launch_entropy_prep(const EntropyPrep& p, hipStream_t s);
+// Loss, lse and coef of every row.
+template <typename T>
+hipError_t launch_entropy_loss(const EntropyArgs& p, hipStream_t s);
+// G and its column sums from Z and coef.
+template <typename T>
+hipError_t launch_entropy_gradient(const EntropyArgs& p, hipStream_t s);
+
+}  // namespace gmm

@@ -1,0 +1,288 @@
+// Kernels of the cross entropy of a linear head beside its products,
+// instantiated once per element type (gmm_entropy_f32.hip, gmm_entropy_f16.hip,
+// gmm_entropy_bf16.hip).
+#pragma once
+
+#include <cfloat>
+
+#include "gmm_entropy.hpp"
+#include "gmm_product.hpp"
+
+namespace gmm {
+
+// A row's pick: a class and its weight, -1 and 0 where there is none.
+struct Pick {
+  int v;
+  float w;
+};
+__device__ __forceinline__ Pick pick_of(const int32_t* idx, const float* wts, int64_t at, int V) {
+  const int v = idx[at];
+  const bool is = v >= 0 && v < V;
+  return {is ? v : -1, !is ? 0.f : wts ? wts[at] : 1.f};
+}
+
+// sum exp(z) as s exp(m), m the largest z: what two parts have together. m is
+// -infinity where all z are, or where they are not numbers and s is none.
+struct LogSum {
+  float m, s;
+};
+__device__ __forceinline__ LogSum join(LogSum a, LogSum b) {
+  constexpr float kInf = __builtin_inff();
+  const float m = fmaxf(a.m, b.m);
+  return {m, (a.m == -kInf ? a.s : a.s * exp_of(a.m - m)) + (b.m == -kInf ? b.s : b.s * exp_of(b.m - m))};
+}
+
+// ---------------------------------------------------------------------------
+// Work before the products. A row has no gradient where its picks weigh nothing
+// or its loss is not asked for; what is not finite in such a row of X would
+// reach dW as 0 times it, so dW's product takes a copy with zeros there.
+// One launch: of 1001 rows the copies, the clean rows and the range took 4 to 6
+// us each in launches of their own.
+// ---------------------------------------------------------------------------
+template <typename T>
+__device__ __forceinline__ void copy_row(const T* from, T* to, int n, int64_t ld, int lane) {
+  constexpr int V = Frag<T>::kPer;
+  for (int64_t c = lane * V; c < ld; c += 64 * V) *reinterpret_cast<u32x4*>(to + c) = load_frag<T>(from + c, (int)(n - c));
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) entropy_prep_kernel(const EntropyPrep p) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int block = blockIdx.x, blocks = gridDim.x;
+  if (p.all_rows) {  // the largest finite |dloss| sum |w|, in parts
+    if (block < kEntropyRange) {
+      __shared__ float red[4];
+      float most = 0.f;
+      for (int64_t row = block * 256ll + threadIdx.x; row < p.all_rows; row += kEntropyRange * 256ll) {
+        float sum = 0.f;
+        for (int j = 0; j < p.top; ++j) sum += fabsf(pick_of(p.idx, p.wts, row * p.top + j, p.V).w);
+        const float a = sum * fabsf(p.dloss ? p.dloss[row] : 1.f);
+        if (a <= FLT_MAX) most = fmaxf(most, a);
+      }
+#pragma unroll
+      for (int o = 32; o; o >>= 1) most = fmaxf(most, __shfl_xor(most, o));
+      if (lane == 0) red[wave] = most;
+      __syncthreads();
+      if (threadIdx.x == 0) p.range[block] = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+      return;
+    }
+    block -= kEntropyRange;
+    blocks -= kEntropyRange;
+  }
+  const int64_t jobs = p.rows + (p.w ? p.V : 0);
+  for (int64_t i = block * 4ll + wave; i < jobs; i += blocks * 4ll) {
+    if (i >= p.rows) {
+      const int64_t r = i - p.rows;
+      copy_row<T>(static_cast<const T*>(p.W) + r * p.d_in, static_cast<T*>(p.w) + r * p.ld, p.d_in, p.ld, lane);
+      continue;
+    }
+    const T* x = static_cast<const T*>(p.X) + i * p.d_in;
+    if (p.x) copy_row<T>(x, static_cast<T*>(p.x) + i * p.ld, p.d_in, p.ld, lane);
+    if (p.clean) {
+      const int64_t row = p.first + i;
+      bool on = false;
+      if (!p.dloss || p.dloss[row] != 0.f)
+        for (int j = 0; j < p.top; ++j) on |= pick_of(p.idx, p.wts, row * p.top + j, p.V).w != 0.f;
+      copy_row<T>(x, static_cast<T*>(p.clean) + i * p.ld, on ? p.d_in : 0, p.ld, lane);
+    }
+  }
+}
+
+// The scale of G: the largest |dloss| sum |w| becomes 2^14 (no entry passes
+// twice that), and the products take it back. So half's range is kept, and
+// where all rows weigh the same, as under a mean, the picks' entries
+// dloss (p - 1) lie next to 2^14, not next to a number whose rounding all rows
+// share: in bfloat16 the gradients of 8192 rows were off by 0.0029 without (1 /
+// 7373 is 0.0024 from its neighbour), and are by 0.0017, their own rounding. In
+// every thread of a wave.
+__device__ __forceinline__ float gradient_scale(const EntropyArgs& p) {
+  float most = 0.f;
+#pragma unroll
+  for (int i = 0; i < kEntropyRange / 64; ++i) most = fmaxf(most, p.range[i * 64 + (threadIdx.x & 63)]);
+#pragma unroll
+  for (int o = 32; o; o >>= 1) most = fmaxf(most, __shfl_xor(most, o));
+  most = most > 0.f ? fmaxf(most, 1e-30f) : 16384.f;  // the scale and its inverse are normal
+  if (blockIdx.x == 0 && threadIdx.x == 0) p.range[kEntropyRange] = most * (1.f / 16384.f);
+  return 16384.f / most;
+}
+
+// ---------------------------------------------------------------------------
+// A row's loss from its log-sum, in parts from the product's tiles (`stats`) or
+// from its logits, by THREADS threads:
+//   loss = sum_j w_j (log s + (m - z_j)),  lse = m + log s
+// m - z_j first, so that a loss near 0 keeps its digits. The picks' logits are
+// read, or where they are nowhere computed: they are few. Latency bounds it (a
+// wave a row of 2048 parts: 14 us for 4096 rows of 1024 features).
+// ---------------------------------------------------------------------------
+template <typename T, int THREADS>
+__global__ void __launch_bounds__((THREADS > 256 ? THREADS : 256)) entropy_loss_kernel(const EntropyArgs p) {
+  constexpr float kInf = __builtin_inff();
+  constexpr int kThreads = (THREADS > 256 ? THREADS : 256), kRows = kThreads / THREADS, kWaves = THREADS > 64 ? THREADS / 64 : 1;
+  __shared__ LogSum red[kWaves];
+  const int t = threadIdx.x % THREADS, lane = threadIdx.x & 63;
+  const float scale = p.coef && p.range ? gradient_scale(p) : 1.f;
+  const int64_t row = blockIdx.x * (int64_t)kRows + threadIdx.x / THREADS;
+  if (row >= p.rows) return;  // whole waves, and only where a row is one wave's
+  const float* z = p.Z ? p.Z + row * p.ldz : nullptr;
+  LogSum sum{-kInf, 0.f};
+  if (p.stats) {
+    const float* st = p.stats + row * p.groups * 2;
+#pragma unroll 4
+    for (int i = t; i < p.groups; i += THREADS) sum = join(sum, LogSum{st[2 * i], st[2 * i + 1]});
+  } else {
+#pragma unroll 4
+    for (int col = t * 4; col < p.V; col += THREADS * 4) {
+      float v[4], m = -kInf, s = 0.f;
+      load_as<float, 4>(z + col, 4, v);  // a row's memory is whole pieces
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (col + i >= p.V) v[i] = -kInf;
+        m = fmaxf(m, v[i]);
+      }
+      const float base = m == -kInf ? 0.f : m;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s += exp_of(v[i] - base);
+      sum = join(sum, LogSum{m, s});
+    }
+  }
+#pragma unroll
+  for (int o = 32; o; o >>= 1) sum = join(sum, LogSum{__shfl_xor(sum.m, o), __shfl_xor(sum.s, o)});
+  if constexpr (THREADS > 64) {
+    if (lane == 0) red[threadIdx.x / 64] = sum;
+    __syncthreads();
+    if (threadIdx.x >= 64) return;
+    sum = red[0];
+    for (int w = 1; w < kWaves; ++w) sum = join(sum, red[w]);
+  }
+  // one wave goes on
+  const float log_sum = logf(sum.s);
+  float loss = 0.f, share = 0.f;
+  bool any = false;
+  for (int j = 0; j < p.top; ++j) {
+    const Pick k = pick_of(p.idx, p.wts, row * p.top + j, p.V);
+    if (k.w == 0.f) continue;  // the same for the whole wave
+    float of;
+    if (z) {
+      of = z[k.v];
+    } else {
+      constexpr int V = Frag<T>::kPer;
+      const T *x = static_cast<const T*>(p.X) + row * p.d_in, *w = static_cast<const T*>(p.W) + (int64_t)k.v * p.d_in;
+      of = 0.f;
+      for (int c = lane * V; c < p.d_in; c += 64 * V) {
+        float a[V], b[V];
+        load_as<T, V>(x + c, p.d_in - c, a);
+        load_as<T, V>(w + c, p.d_in - c, b);
+#pragma unroll
+        for (int i = 0; i < V; ++i) of = fmaf(a[i], b[i], of);
+      }
+#pragma unroll
+      for (int o = 32; o; o >>= 1) of += __shfl_xor(of, o);
+      if (p.bias) of += (float)static_cast<const T*>(p.bias)[k.v];
+    }
+    any = true;
+    share += k.w;
+    loss = fmaf(k.w, log_sum + (sum.m - of), loss);
+  }
+  if (lane == 0) {
+    p.loss[row] = loss;
+    if (p.lse) p.lse[row] = sum.m == -kInf ? sum.s == 0.f ? -kInf : sum.s : sum.m + log_sum;
+    if (p.coef) {
+      const float d = any ? (p.dloss ? p.dloss[row] : 1.f) * scale : 0.f;
+      p.coef[row] = RowCoef{sum.m == -kInf ? 0.f : sum.m, d * share / sum.s, d, 0.f};
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The logits' gradient and its column sums (of the rounded values, in float,
+// without the scale). A wave takes a row's columns of its block, 16 bytes of G a
+// lane, so what belongs to the row is scalar; a block takes a chunk of rows.
+// HBM bounds it.
+// ---------------------------------------------------------------------------
+template <typename T>
+__global__ void __launch_bounds__(256) entropy_gradient_kernel(const EntropyArgs p, int across) {
+  constexpr int V = Frag<T>::kPer, kAhead = 4;  // rows of logits in flight
+  __shared__ float red[4][64 * V];
+  const int part = blockIdx.x / across, lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int first = (blockIdx.x % across) * 64 * V, col = first + lane * V;
+  const int64_t r0 = part * p.chunk + wave, r1 = min(p.rows, (part + 1) * p.chunk);
+  const bool mine = col < p.ldz;
+  float sum[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) sum[i] = 0.f;
+  for (int64_t r = r0; r < r1; r += 4 * kAhead) {
+    float z[kAhead][V];
+    RowCoef c[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (r + 4 * u < r1) {
+        c[u] = p.coef[r + 4 * u];
+        if (mine) load_as<float, V>(p.Z + (r + 4 * u) * p.ldz + col, V, z[u]);
+      }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int64_t row = r + 4 * u;
+      if (row >= r1) break;
+      const bool on = c[u].d != 0.f;
+      float g[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) g[i] = on && col + i < p.V ? c[u].up * exp_of(z[u][i] - c[u].base) : 0.f;
+      if (on)
+        for (int j = 0; j < p.top; ++j) {
+          const Pick k = pick_of(p.idx, p.wts, row * p.top + j, p.V);
+          const int at = k.v - col;
+          if (k.v >= first && k.v < first + 64 * V)  // the same for the whole wave
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+              if (at == i) g[i] = fmaf(-c[u].d, k.w, g[i]);
+        }
+      if (mine) {
+        store_as<T, V>(static_cast<T*>(p.G) + row * p.ldz + col, V, g);
+        if (p.parts)
+#pragma unroll
+          for (int i = 0; i < V; ++i) sum[i] += (float)(T)g[i];
+      }
+    }
+  }
+  if (!p.parts) return;
+#pragma unroll
+  for (int i = 0; i < V; ++i) red[wave][lane * V + i] = sum[i];
+  __syncthreads();
+  const float unscale = p.range ? p.range[kEntropyRange] : 1.f;
+  for (int i = threadIdx.x; i < 64 * V; i += 256)
+    if (first + i < p.V)
+      p.parts[part * (int64_t)p.V + first + i] = unscale * ((red[0][i] + red[1][i]) + (red[2][i] + red[3][i]));
+}
+
+template <typename T>
+hipError_t launch_entropy_prep(const EntropyPrep& p, hipStream_t s) {
+  const int64_t jobs = p.rows + (p.w ? p.V : 0), blocks = (jobs + 3) / 4;
+  const unsigned grid = (unsigned)(blocks < 8192 ? blocks : 8192) + (p.all_rows ? kEntropyRange : 0);
+  if (grid) entropy_prep_kernel<T><<<grid, 256, 0, s>>>(p);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch_entropy_loss(const EntropyArgs& p, hipStream_t s) {
+  if (p.stats || p.V <= 2048)
+    entropy_loss_kernel<T, 64><<<(unsigned)((p.rows + 3) / 4), 256, 0, s>>>(p);
+  else
+    entropy_loss_kernel<T, 1024><<<(unsigned)p.rows, 1024, 0, s>>>(p);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch_entropy_gradient(const EntropyArgs& p, hipStream_t s) {
+  const int across = (int)((p.ldz + 64 * Frag<T>::kPer - 1) / (64 * Frag<T>::kPer));
+  const int64_t chunks = (p.rows + p.chunk - 1) / p.chunk;
+  entropy_gradient_kernel<T><<<(unsigned)(across * chunks), 256, 0, s>>>(p, across);
+  return hipGetLastError();
+}
+
+#define GMM_ENTROPY_TYPE(T)                                                    \
+  template hipError_t launch_entropy_prep<T>(const EntropyPrep&, hipStream_t); \
+  template hipError_t launch_entropy_loss<T>(const EntropyArgs&, hipStream_t); \
+  template hipError_t launch_entropy_gradient<T>(const EntropyArgs&, hipStream_t);
+
+}  // namespace gmm

@@ -44,7 +44,7 @@ struct Cut {
   int64_t split_k;
 };
 
-inline Cut choose_cut(int64_t M, int64_t N, int64_t K, int e) {
+inline Cut choose_cut(int64_t M, int64_t N, int64_t K, int e, int64_t most_parts = 256) {
   struct Rate {
     int per_cu;         // blocks that a CU holds
     double one, full;   // us of a step with one block on a CU, and with all
@@ -59,7 +59,7 @@ inline Cut choose_cut(int64_t M, int64_t N, int64_t K, int e) {
   for (int v = 0; v < kTileVariants; ++v) {
     const Rate& r = kRates[e == 4][v];
     const int64_t tiles = ceil_div(M, kTileRows[v]) * ceil_div(N, kTileRows[v]);
-    for (int64_t want = 1; want <= std::min<int64_t>(steps, 256); want *= 2) {
+    for (int64_t want = 1; want <= std::min<int64_t>(steps, most_parts); want *= 2) {
       const int64_t per = ceil_div(steps, want), parts = ceil_div(steps, per);
       const double moved = parts > 1 ? 8. * parts * M * N : 0.;  // partial sums, written and read
       if (moved > 2e9) break;

@@ -106,7 +106,7 @@ static hipError_t linear_forward(const T* X, int64_t N, int d_in, const T* W, in
                                  const void* residual, void* Y, int y_f32, void* pre, char* ws, hipStream_t s) {
   const LinearPlan l = linear_plan(N, d_in, d_out, sizeof(T));
   if (l.few) {
-    const FewArgs f{X, W, (int)N, d_out, d_in, bias, residual, Y, pre, y_f32};
+    const FewArgs f{X, W, (int)N, d_out, d_in, bias, residual, Y, pre, y_f32, d_out};
     return launch_few<T>(act, f, s);
   }
   const int ey = y_f32 ? 4 : (int)sizeof(T);
@@ -114,6 +114,7 @@ static hipError_t linear_forward(const T* X, int64_t N, int d_in, const T* W, in
   p.B = W;
   p.lda = p.ldb = l.kp;
   p.N = d_out;
+  p.ldc = d_out;
   p.K = d_in;
   p.bias = bias;
   p.c_f32 = y_f32;
@@ -170,6 +171,7 @@ static hipError_t linear_gradients(const void* dY, int y_f32, const T* X, int64_
   p.partial = reinterpret_cast<float*>(ws + b.o_part);
   p.c_f32 = sizeof(T) == 4;
   p.N = d_in;
+  p.ldc = d_in;
   p.ldb = b.lx;
   p.unscale = unscale;
   if (db) {  // summed beside the first product

@@ -22,10 +22,12 @@ struct ProductArgs {
   int64_t split_k;       // k per part, a multiple of the k step
   // epilogue (splits == 1): C = act(z + bias) + residual; pre receives z + bias
   const void* bias;      // element type of the operands
-  const void* residual;  // type of C
+  const void* residual;  // type of C, or float (res_f32)
   void* C;
   void* pre;             // type of C
+  int64_t ldc;           // row length of C, residual and pre
   int c_f32;             // C, residual and pre are float (else the operands' type)
+  int res_f32;           // residual is float whatever C is
   int c_stream;          // C is written past the caches (kStreamBytes)
   float* partial;        // [splits][M][N]
   // column sums that ride along in blocks of their own (sum_blocks of them, 0:
@@ -34,7 +36,10 @@ struct ProductArgs {
   void* sums_out;        // type of the operands
   int64_t sums_rows;
   int sums_cols, sum_blocks;
-  const float* unscale;  // C = *unscale times the product, where not null (gradients of half operands)
+  // act kRowStats and kStatsToo: the largest z of each row and group of columns and
+  // the sum of exp(z - it): [M][groups][2], groups as stat_groups() says
+  float* stats;
+  const float* unscale;  // C = *unscale times the product, where not null (gradients of 2-byte operands)
 };
 constexpr int kSumCols = 16;  // columns of such a block
 
@@ -48,6 +53,15 @@ constexpr int64_t kStreamBytes = 64ll << 20;
 enum { kTile256 = 0, kTile128 = 1, kTile64 = 2, kTileVariants = 3 };
 constexpr int kTileRows[kTileVariants] = {256, 128, 64};
 constexpr int kStepBytes = 128;  // bytes of k per step and operand row
+// In the place of an activation: statistics of the rows instead of C, or beside it.
+constexpr int kRowStats = 6, kStatsToo = 7;
+
+// Groups of columns whose statistics such a product of N columns writes:
+// those of a wave, 4 in a tile, or 2 where its waves are 2 x 2.
+constexpr int stat_waves(int variant, int elem) { return variant == kTile256 || (variant == kTile128 && elem == 4) ? 4 : 2; }
+inline int stat_groups(int variant, int elem, int64_t N) {
+  return (int)((N + kTileRows[variant] - 1) / kTileRows[variant]) * stat_waves(variant, elem);
+}
 
 // Few rows: C[m][n] of at most kFewRows rows, operands of any alignment,
 // B (the weights) streamed once (bfloat16, 8192 x 16384 weights: 16 rows 49 us
@@ -64,6 +78,7 @@ struct FewArgs {
   void* C;
   void* pre;
   int c_f32;
+  int64_t ldc;
 };
 
 template <typename T>

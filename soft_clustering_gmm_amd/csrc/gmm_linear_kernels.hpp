@@ -195,14 +195,14 @@ struct Operand {
 // The residual of W consecutive n of one row, where there is one.
 template <typename T, int W>
 __device__ __forceinline__ void load_residual(const ProductArgs& p, int64_t m, int n, float* res) {
-  if (p.residual) load_row<T, W>(p.residual, m * p.N + n, p.N - n, p.c_f32, res);
+  if (p.residual) load_row<T, W>(p.residual, m * p.ldc + n, p.N - n, p.c_f32 | p.res_f32, res);
 }
 
 // z + bias -> pre, act(.) + residual -> C for W consecutive n of one row.
 template <typename T, int ACT, int W>
 __device__ __forceinline__ void finish_row(const ProductArgs& p, int64_t m, int n, float* z, const float* bias,
                                            const float* res) {
-  const int64_t at = m * p.N + n;
+  const int64_t at = m * p.ldc + n;
   const int left = p.N - n;
 #pragma unroll
   for (int i = 0; i < W; ++i) z[i] += bias[i];
@@ -270,9 +270,56 @@ __global__ void __launch_bounds__(256) column_sums_kernel(const ProductArgs p) {
   column_sums<T>(p, blockIdx.x, red);
 }
 
-// Products that may be unscaled: the gradients' of half operands (B k-strided).
+// The statistics of a wave's TI x NI tiles, straight from the registers: a lane
+// has 4 NI columns of a row, which 4 lanes share.
+template <typename T, int TI, int NI, typename F>
+__device__ __forceinline__ void row_stats(const ProductArgs& p, const f32x4 (*acc)[NI], F&& first_row, int n0, int group,
+                                          int groups, int lane) {
+  constexpr float kInf = __builtin_inff();
+  float bias[NI][4];
+#pragma unroll
+  for (int j = 0; j < NI; ++j) {
+    const int n = n0 + 16 * j + 4 * (lane >> 4);
+    if (p.bias)
+      load_as<T, 4>(static_cast<const T*>(p.bias) + n, p.N - n, bias[j]);
+    else
+#pragma unroll
+      for (int q = 0; q < 4; ++q) bias[j][q] = 0.f;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (n + q >= p.N) bias[j][q] = -kInf;  // the products there are 0
+  }
+#pragma unroll
+  for (int i = 0; i < TI; ++i) {
+    float most = -kInf, z[NI][4], sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < NI; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        z[j][q] = acc[i][j][q] + bias[j][q];
+        most = fmaxf(most, z[j][q]);
+      }
+    most = fmaxf(most, __shfl_xor(most, 16));
+    most = fmaxf(most, __shfl_xor(most, 32));
+    const float base = most == -kInf ? 0.f : most;
+#pragma unroll
+    for (int j = 0; j < NI; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) sum += exp_of(z[j][q] - base);
+    sum += __shfl_xor(sum, 16);
+    sum += __shfl_xor(sum, 32);
+    const int64_t m = first_row(i) + (lane & 15);
+    if (lane < 16 && m < p.M) {
+      float* out = p.stats + 2 * (m * groups + group);
+      out[0] = most;
+      out[1] = sum;
+    }
+  }
+}
+
+// Products that may be unscaled: the gradients' of 2-byte operands (B k-strided).
 template <typename T, bool BS>
-constexpr bool kScaled = BS && std::is_same<T, _Float16>::value;
+constexpr bool kScaled = BS && sizeof(T) == 2;
 
 template <typename T, int BM, int BN, int WM, int WN, bool AS, bool BS, int ACT>
 __global__ void __launch_bounds__(64 * WM * WN, 2)
@@ -364,6 +411,10 @@ product_kernel(const ProductArgs p) {
     multiply(1, 1, std::true_type{});
   }
   step_barrier<0>(lds);  // nobody reads the slots, and nothing arrives in them any more
+  if constexpr (ACT == kRowStats || ACT == kStatsToo)
+    row_stats<T, 2 * MI, NI>(p, acc[0], [&](int i) { return at.m0 + i / MI * HM + wm * TM + 16 * (i % MI); },
+                             at.n0 + wn * TN, at.n0 / BN * WN + wn, p.tiles_n * WN, lane);
+  if constexpr (ACT == kRowStats) return;
 
   // The results go through LDS, 16 rows of m at a time in memory of the wave's
   // own, so that neighbouring lanes access one row: whole lines for C, residual
@@ -501,6 +552,8 @@ __global__ void __launch_bounds__(64 * NW) few_kernel(const FewArgs p) {
     for (int w = 0; w < NW; ++w) z += red[w][m][n];
     ProductArgs e;
     e.N = p.N;
+    e.ldc = p.ldc;
+    e.res_f32 = 0;
     e.residual = p.residual;
     e.C = p.C;
     e.pre = p.pre;
@@ -692,6 +745,14 @@ static void launch_tile(int variant, const ProductArgs& p, hipStream_t s) {
 
 template <typename T>
 hipError_t launch_product(int variant, bool a_strided, bool b_strided, int act, const ProductArgs& p, hipStream_t s) {
+  if (act == kRowStats) {  // of k-contiguous operands
+    launch_tile<T, false, false, kRowStats>(variant, p, s);
+    return hipGetLastError();
+  }
+  if (act == kStatsToo) {
+    launch_tile<T, false, false, kStatsToo>(variant, p, s);
+    return hipGetLastError();
+  }
   if (!a_strided && !b_strided)
     return with_act<T, true>(act, p.c_f32, [&](auto a) {
       launch_tile<T, false, false, decltype(a)::value>(variant, p, s);

@@ -9,32 +9,6 @@
 
 namespace gmm {
 
-// Sums of K values over the G threads of a row, in every thread and in a fixed
-// order. Rows of several waves meet in LDS: `red` has two halves that calls
-// take in turn, so one barrier a call is enough (who writes a half again has
-// passed the barrier that all pass after reading it).
-template <int G, int K>
-__device__ __forceinline__ void row_sum(float* v, float (*red)[G > 64 ? G / 64 : 1][2], int& turn) {
-#pragma unroll
-  for (int o = (G < 64 ? G : 64) / 2; o; o >>= 1)
-#pragma unroll
-    for (int k = 0; k < K; ++k) v[k] += __shfl_xor(v[k], o);
-  if constexpr (G > 64) {
-    const int wave = threadIdx.x / 64;
-    if (threadIdx.x % 64 == 0)
-#pragma unroll
-      for (int k = 0; k < K; ++k) red[turn][wave][k] = v[k];
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      v[k] = 0.f;
-#pragma unroll
-      for (int w = 0; w < G / 64; ++w) v[k] += red[turn][w][k];
-    }
-    turn ^= 1;
-  }
-}
-
 // The W weights from column c on; `otherwise` where there are none.
 template <typename TY, int W>
 __device__ __forceinline__ void load_weights(const void* p, int c, int left, int w_f32, float otherwise, float* out) {

@@ -1,5 +1,5 @@
-// C-ABI of a training step around the mixture: the layer norm and the AdamW
-// step. Argument checks, workspace planning and dispatch; every check runs on
+// C-ABI of a training step around the mixture: the layer norm, the cross entropy
+// of a linear head and the AdamW step. Argument checks, workspace planning and dispatch; every check runs on
 // the host before anything is enqueued.
 #include "../../include/gmm.h"
 
@@ -10,6 +10,7 @@
 #include <type_traits>
 
 #include "gmm_adamw.hpp"
+#include "gmm_entropy.hpp"
 #include "gmm_layers.hpp"
 #include "gmm_norm.hpp"
 
@@ -39,6 +40,254 @@ static size_t norm_bytes(int64_t N, int D, int e) {
 }
 
 static bool factor_ok(double beta) { return beta >= 0. && beta < 1.; }
+
+// The rows of a piece: what the call keeps of a row (`bytes`) within `most`, in
+// whole tiles.
+static int64_t piece_rows(int64_t N, int64_t bytes, int64_t most) {
+  const int64_t rows = std::max<int64_t>(most / bytes / 256 * 256, 256);
+  return std::min(N, std::min<int64_t>(rows, 1 << 20));
+}
+constexpr int64_t kStatPiece = 256ll << 20;   // bytes of a piece's statistics
+constexpr int64_t kLogitPiece = 2048ll << 20; // bytes of a piece's logits
+
+// Workspace of the loss: [padded rows of X of a piece] [padded W] [statistics]
+// or, for few rows, [logits].
+struct EntropyPlan {
+  bool few, pad;
+  int64_t lx, ldz, piece;
+  Cut cut;
+  size_t o_x, o_w, o_z, bytes;
+};
+
+static EntropyPlan entropy_plan(int64_t N, int d_in, int V, int e) {
+  EntropyPlan l{};
+  l.few = N <= kFewRows;
+  l.lx = row_len(d_in, e);
+  l.pad = l.lx != d_in && !l.few;
+  l.ldz = ceil_div(V, 8) * 8;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off = align_up(off + bytes, 256);
+    return o;
+  };
+  l.piece = N;
+  if (!l.few) {
+    l.piece = piece_rows(N, ceil_div(V, 32) * 8, kStatPiece);
+    l.cut = choose_cut(l.piece, V, d_in, e, 1);
+    l.o_x = take(l.pad ? (size_t)l.piece * l.lx * e : 0);
+    l.o_w = take(l.pad ? (size_t)V * l.lx * e : 0);
+    l.o_z = take((size_t)l.piece * stat_groups(l.cut.variant, e, V) * 2 * sizeof(float));
+  } else {
+    l.o_z = take((size_t)N * l.ldz * sizeof(float));
+  }
+  l.bytes = off;
+  return l;
+}
+
+// Workspace of the gradients, for a piece of rows: [padded X] [X without the
+// rows that have no gradient] [padded W] [logits] [their gradient] [statistics]
+// [coefficients] [dW so far] [partial sums of the products] [column sums] [range
+// and scale].
+struct EntropyBackPlan {
+  bool few, pad;
+  int64_t lx, ldz, piece, chunk, chunks;  // chunks: of all rows
+  size_t o_x, o_clean, o_w, o_z, o_g, o_stats, o_coef, o_acc, o_part, o_db, o_range, bytes;
+};
+
+static EntropyBackPlan entropy_back_plan(int64_t N, int d_in, int V, int e) {
+  EntropyBackPlan l{};
+  l.few = N <= kFewRows;
+  l.lx = row_len(d_in, e);
+  l.pad = l.lx != d_in;
+  l.ldz = ceil_div(V, 8) * 8;
+  l.piece = piece_rows(N, l.ldz * (int64_t)sizeof(float), kLogitPiece);
+  // column sums: chunks of 64 rows at least, 1024 of them at most; a piece is whole chunks, or all there is
+  l.chunk = std::min(l.piece, std::max<int64_t>(64, ceil_div(ceil_div(N, 1024), 64) * 64));
+  l.chunks = ceil_div(l.piece, l.chunk) * (N / l.piece) + ceil_div(N % l.piece, l.chunk);
+  size_t off = 0, part = 0, stats = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off = align_up(off + bytes, 256);
+    return o;
+  };
+  for (int64_t rows : {l.piece, N % l.piece})
+    if (rows) {
+      if (!l.few) {
+        const Cut c = choose_cut(rows, V, d_in, e);
+        part = std::max(part, partial_bytes(c, rows, V));
+        stats = std::max(stats, (size_t)rows * stat_groups(c.variant, e, V) * 2 * sizeof(float));
+      }
+      part = std::max(part, partial_bytes(choose_cut(rows, d_in, V, e), rows, d_in));
+      part = std::max(part, partial_bytes(choose_cut(V, d_in, rows, e), V, d_in));
+    }
+  l.o_x = take(l.pad && !l.few ? (size_t)l.piece * l.lx * e : 0);
+  l.o_clean = take((size_t)l.piece * l.lx * e);
+  l.o_w = take(l.pad ? (size_t)V * l.lx * e : 0);
+  l.o_z = take((size_t)l.piece * l.ldz * sizeof(float));
+  l.o_g = take((size_t)l.piece * l.ldz * e);
+  l.o_stats = take(stats);
+  l.o_coef = take((size_t)l.piece * sizeof(RowCoef));
+  l.o_acc = take(l.piece < N && e == 2 ? (size_t)V * d_in * sizeof(float) : 0);
+  l.o_part = take(part);
+  l.o_db = take((size_t)l.chunks * V * sizeof(float));
+  l.o_range = take((kEntropyRange + 1) * sizeof(float));
+  l.bytes = off;
+  return l;
+}
+
+static int check_entropy(int64_t N, int32_t d_in, int32_t V, int32_t top, int32_t x_dtype) {
+  if (!dtype_ok(x_dtype) || N < 0 || d_in < 1 || V < 1 || top < 1) return GMM_EINVAL;
+  if (d_in > kMaxWidth || V > kMaxClasses || top > kMaxPicksRow || N > kMaxRows) return GMM_EUNSUPPORTED;
+  return GMM_OK;
+}
+
+// The first row of a piece in an array of `width` elements a row.
+template <typename E>
+static E* row_at(E* p, int64_t row, int64_t width) {
+  return p ? p + row * width : nullptr;
+}
+
+template <typename T>
+static hipError_t entropy_forward(EntropyArgs a, int64_t N, char* ws, hipStream_t s) {
+  const EntropyPlan l = entropy_plan(N, a.d_in, a.V, sizeof(T));
+  const EntropyArgs all = a;
+  hipError_t e = hipSuccess;
+  ProductArgs p{};
+  p.bias = a.bias;
+  p.lda = p.ldb = l.lx;
+  p.N = a.V;
+  p.K = a.d_in;
+  for (int64_t r = 0; r < N; r += l.piece) {
+    a.rows = std::min(N - r, l.piece);
+    a.X = row_at(static_cast<const T*>(all.X), r, a.d_in);
+    a.idx = row_at(all.idx, r, a.top);
+    a.wts = row_at(all.wts, r, a.top);
+    a.loss = row_at(all.loss, r, 1);
+    a.lse = row_at(all.lse, r, 1);
+    if (l.few) {
+      float* z = reinterpret_cast<float*>(ws + l.o_z);
+      const FewArgs f{a.X, a.W, (int)N, a.V, a.d_in, a.bias, nullptr, z, nullptr, 1, l.ldz};
+      if ((e = launch_few<T>(GMM_ACT_NONE, f, s)) != hipSuccess) return e;
+      a.Z = z;
+      a.ldz = l.ldz;
+      return launch_entropy_loss<T>(a, s);
+    }
+    p.A = a.X;
+    p.B = a.W;
+    if (l.pad) {
+      const PadJob px{a.X, ws + l.o_x, a.rows, l.lx, a.d_in}, pw{a.W, ws + l.o_w, r == 0 ? a.V : 0, l.lx, a.d_in};
+      if ((e = launch_pad<T>(px, pw, s)) != hipSuccess) return e;
+      p.A = ws + l.o_x;
+      p.B = ws + l.o_w;
+    }
+    p.M = a.rows;
+    p.stats = reinterpret_cast<float*>(ws + l.o_z);
+    if ((e = run_product<T>(l.cut, false, false, kRowStats, p, s)) != hipSuccess) return e;
+    a.stats = p.stats;
+    a.groups = stat_groups(l.cut.variant, sizeof(T), a.V);
+    if ((e = launch_entropy_loss<T>(a, s)) != hipSuccess) return e;
+  }
+  return e;
+}
+
+template <typename T>
+static hipError_t entropy_gradients(EntropyArgs a, int64_t N, T* dX, T* dW, T* db, char* ws, hipStream_t s) {
+  const EntropyBackPlan l = entropy_back_plan(N, a.d_in, a.V, sizeof(T));
+  const EntropyArgs all = a;
+  const bool scaled = sizeof(T) == 2;
+  hipError_t e = hipSuccess;
+  a.range = scaled ? reinterpret_cast<float*>(ws + l.o_range) : nullptr;
+  a.ldz = l.ldz;
+  a.Z = reinterpret_cast<float*>(ws + l.o_z);
+  a.G = ws + l.o_g;
+  a.coef = reinterpret_cast<RowCoef*>(ws + l.o_coef);
+  a.chunk = l.chunk;
+  float* sums = reinterpret_cast<float*>(ws + l.o_db);
+  a.parts = db ? sums : nullptr;
+  const bool pad_w = l.pad && (dX || !l.few), pad_x = l.pad && !l.few;
+  const void* W = pad_w ? ws + l.o_w : a.W;
+  for (int64_t r = 0; r < N; r += l.piece) {
+    const int64_t rows = a.rows = std::min(N - r, l.piece);
+    const bool last = r + rows == N;
+    a.X = row_at(static_cast<const T*>(all.X), r, a.d_in);
+    a.idx = row_at(all.idx, r, a.top);
+    a.wts = row_at(all.wts, r, a.top);
+    a.dloss = row_at(all.dloss, r, 1);
+    a.loss = row_at(all.loss, r, 1);
+    a.lse = row_at(all.lse, r, 1);
+    EntropyPrep b{};
+    b.X = a.X, b.ld = l.lx, b.d_in = a.d_in, b.V = a.V, b.top = a.top;
+    b.x = pad_x ? ws + l.o_x : nullptr;
+    b.clean = dW ? ws + l.o_clean : nullptr;
+    b.rows = b.x || b.clean ? rows : 0;
+    b.W = a.W, b.w = pad_w && r == 0 ? ws + l.o_w : nullptr;
+    b.all_rows = scaled && r == 0 ? N : 0;
+    b.idx = all.idx, b.wts = all.wts, b.dloss = all.dloss, b.first = r, b.range = a.range;
+    if ((e = launch_entropy_prep<T>(b, s)) != hipSuccess) return e;
+    ProductArgs p{};
+    p.partial = reinterpret_cast<float*>(ws + l.o_part);
+    // the logits
+    a.stats = nullptr;
+    if (l.few) {
+      const FewArgs f{a.X, a.W, (int)N, a.V, a.d_in, a.bias, nullptr, const_cast<float*>(a.Z), nullptr, 1, l.ldz};
+      e = launch_few<T>(GMM_ACT_NONE, f, s);
+    } else {
+      p.A = pad_x ? ws + l.o_x : a.X;
+      p.B = W, p.lda = p.ldb = l.lx;
+      p.M = rows, p.N = a.V, p.K = a.d_in;
+      p.bias = a.bias;
+      p.C = const_cast<float*>(a.Z), p.ldc = l.ldz, p.c_f32 = 1;
+      const Cut c = choose_cut(rows, a.V, a.d_in, sizeof(T));
+      if (c.splits == 1) {  // whole sums: the tiles' statistics with them
+        a.stats = p.stats = reinterpret_cast<float*>(ws + l.o_stats);
+        a.groups = stat_groups(c.variant, sizeof(T), a.V);
+      }
+      e = run_product<T>(c, false, false, a.stats ? kStatsToo : (int)GMM_ACT_NONE, p, s);
+    }
+    if (e != hipSuccess) return e;
+    if ((e = launch_entropy_loss<T>(a, s)) != hipSuccess) return e;
+    if (!dX && !dW && !db) continue;
+    if ((e = launch_entropy_gradient<T>(a, s)) != hipSuccess) return e;
+    if (db) a.parts += ceil_div(rows, l.chunk) * a.V;
+    p = ProductArgs{};
+    p.partial = reinterpret_cast<float*>(ws + l.o_part);
+    p.N = a.d_in;
+    p.ldc = a.d_in;
+    p.ldb = l.lx;
+    p.unscale = scaled ? a.range + kEntropyRange : nullptr;
+    if (db && last) {  // summed beside the next product
+      p.sums = sums;
+      p.sums_out = db;
+      p.sums_rows = l.chunks;
+      p.sums_cols = a.V;
+      p.sum_blocks = (int)ceil_div(a.V, kSumCols);
+      if (!dX && !dW) return launch_column_sums<T>(p, s);
+    }
+    if (dX) {  // dX = G W
+      p.A = a.G, p.lda = l.ldz;
+      p.B = W;
+      p.M = rows, p.K = a.V;
+      p.C = row_at(dX, r, a.d_in);
+      p.c_f32 = sizeof(T) == 4;
+      if ((e = run_product<T>(choose_cut(rows, a.d_in, a.V, sizeof(T)), false, true, GMM_ACT_NONE, p, s)) != hipSuccess)
+        return e;
+    }
+    if (dW) {  // dW = G^T X, over the pieces in float
+      float* acc = sizeof(T) == 4 ? reinterpret_cast<float*>(dW) : reinterpret_cast<float*>(ws + l.o_acc);
+      p.A = a.G, p.lda = l.ldz;
+      p.B = ws + l.o_clean;
+      p.M = a.V, p.K = rows;
+      p.residual = r ? acc : nullptr;
+      p.res_f32 = 1;
+      p.C = last ? static_cast<void*>(dW) : acc;
+      p.c_f32 = sizeof(T) == 4 || !last;
+      if ((e = run_product<T>(choose_cut(a.V, a.d_in, rows, sizeof(T)), true, true, GMM_ACT_NONE, p, s)) != hipSuccess)
+        return e;
+    }
+  }
+  return e;
+}
 
 }  // namespace gmm
 
@@ -94,6 +343,60 @@ int gmm_layer_norm_backward(const void* dY, int32_t y_dtype, const void* X, int3
   p.parts = norm_parts(N, D, elem_size(x_dtype));
   return with_norm_types(x_dtype, y_dtype, [&](auto* tx, auto* ty) {
     return launch_norm_backward<std::remove_pointer_t<decltype(tx)>, std::remove_pointer_t<decltype(ty)>>(p, s);
+  });
+}
+
+size_t gmm_cross_entropy_workspace_bytes(int64_t N, int32_t d_in, int32_t V, int32_t x_dtype, int32_t gradients) {
+  if (check_entropy(N, d_in, V, 1, x_dtype) != GMM_OK) return 0;
+  const int e = elem_size(x_dtype);
+  const size_t b = N == 0 ? 0 : gradients ? entropy_back_plan(N, d_in, V, e).bytes : entropy_plan(N, d_in, V, e).bytes;
+  return std::max<size_t>(b, 256);
+}
+
+int gmm_cross_entropy(const void* X, int32_t x_dtype, int64_t N, int32_t d_in, const void* W, int32_t V,
+                      const void* bias, const int32_t* idx, const float* wts, int32_t top, float* loss, float* lse,
+                      void* workspace, size_t ws_bytes, void* stream) {
+  int st = check_entropy(N, d_in, V, top, x_dtype);
+  if (st) return st;
+  if (!W || (N > 0 && (!X || !idx || !loss))) return GMM_EINVAL;
+  const int e = elem_size(x_dtype);
+  if (row_len(d_in, e) == d_in && (!aligned16(X) || !aligned16(W))) return GMM_EINVAL;
+  if (N == 0) return GMM_OK;
+  if ((st = check_ws(workspace, ws_bytes, entropy_plan(N, d_in, V, e).bytes))) return st;
+  EntropyArgs a{};
+  a.X = X, a.W = W, a.bias = bias, a.idx = idx, a.wts = wts, a.d_in = d_in, a.V = V, a.top = top;
+  a.loss = loss, a.lse = lse;
+  return with_type(x_dtype, [&](auto* t) {
+    using T = std::remove_pointer_t<decltype(t)>;
+    return hip_status(
+        entropy_forward<T>(a, N, static_cast<char*>(workspace), static_cast<hipStream_t>(stream)));
+  });
+}
+
+int gmm_cross_entropy_gradients(const float* dloss, const void* X, int32_t x_dtype, int64_t N, int32_t d_in,
+                                const void* W, int32_t V, const void* bias, const int32_t* idx, const float* wts,
+                                int32_t top, float* loss, float* lse, void* dX, void* dW, void* db, void* workspace,
+                                size_t ws_bytes, void* stream) {
+  int st = check_entropy(N, d_in, V, top, x_dtype);
+  if (st) return st;
+  if (!W || (N > 0 && (!X || !idx || !loss))) return GMM_EINVAL;
+  const int e = elem_size(x_dtype);
+  if (row_len(d_in, e) == d_in && (!aligned16(X) || !aligned16(W))) return GMM_EINVAL;
+  if (N > 0 && (st = check_ws(workspace, ws_bytes, entropy_back_plan(N, d_in, V, e).bytes))) return st;
+  EntropyArgs a{};
+  a.X = X, a.W = W, a.bias = bias, a.idx = idx, a.wts = wts, a.dloss = dloss, a.d_in = d_in, a.V = V, a.top = top;
+  a.loss = loss, a.lse = lse;
+  return with_type(x_dtype, [&](auto* t) {
+    using T = std::remove_pointer_t<decltype(t)>;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (N == 0) {  // sums over no rows
+      hipError_t r = hipSuccess;
+      if (dW) r = launch_zero<T>(static_cast<T*>(dW), (int64_t)V * d_in, s);
+      if (r == hipSuccess && db) r = launch_zero<T>(static_cast<T*>(db), V, s);
+      return hip_status(r);
+    }
+    return hip_status(entropy_gradients<T>(a, N, static_cast<T*>(dX), static_cast<T*>(dW), static_cast<T*>(db),
+                                           static_cast<char*>(workspace), s));
   });
 }
 

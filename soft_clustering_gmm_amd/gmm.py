@@ -33,6 +33,7 @@ EXPORTS = (
     "gmm_linear", "gmm_linear_backward", "gmm_linear_workspace_bytes",
     "gmm_expert_layer", "gmm_expert_rows", "gmm_expert_workspace_bytes",
     "gmm_layer_norm", "gmm_layer_norm_backward", "gmm_layer_norm_workspace_bytes",
+    "gmm_cross_entropy", "gmm_cross_entropy_gradients", "gmm_cross_entropy_workspace_bytes",
     "gmm_adamw_step", "gmm_adamw_state_elements",
     "gmm_peak_mfma", "gmm_peak_mfma_flops", "gmm_peak_hbm_read", "gmm_peak_coissue",
 )
@@ -121,6 +122,12 @@ def _load() -> ctypes.CDLL:
     L.gmm_layer_norm_backward.argtypes = [P, I32, P, I32, I64, I32, P, P, I32, P, P, P, P, SZ, P]
     L.gmm_layer_norm_workspace_bytes.restype = SZ
     L.gmm_layer_norm_workspace_bytes.argtypes = [I64, I32, I32]
+    L.gmm_cross_entropy.restype = ctypes.c_int
+    L.gmm_cross_entropy.argtypes = [P, I32, I64, I32, P, I32, P, P, P, I32, P, P, P, SZ, P]
+    L.gmm_cross_entropy_gradients.restype = ctypes.c_int
+    L.gmm_cross_entropy_gradients.argtypes = [P, P, I32, I64, I32, P, I32, P, P, P, I32, P, P, P, P, P, P, SZ, P]
+    L.gmm_cross_entropy_workspace_bytes.restype = SZ
+    L.gmm_cross_entropy_workspace_bytes.argtypes = [I64, I32, I32, I32, I32]
     L.gmm_adamw_step.restype = ctypes.c_int
     L.gmm_adamw_step.argtypes = [I32, P, P, I32, P, I32, P, P, P, I32, P, P, P, F64, F64, F64, F64, F64, P, P, P]
     L.gmm_adamw_state_elements.restype = I64
@@ -771,6 +778,106 @@ def layer_norm_backward(dY, X, stats, gamma=None, *, want_dx: bool = True, want_
         dY.data_ptr(), _DTYPES[dY.dtype], X.data_ptr(), xt, N, D, stats.data_ptr(), _at(gamma), wt, _at(dX),
         _at(dgamma), _at(dbeta), *_space(ws, dev), _raw_stream(dev.index)))
     return dX, dgamma, dbeta
+
+
+class _CrossEntropy(torch.autograd.Function):
+    """cross_entropy in torch's graph: its backward pass is cross_entropy_gradients."""
+
+    @staticmethod
+    def forward(ctx, X, W, bias, idx, wts):
+        loss, lse = cross_entropy(X, W, idx, wts=wts, bias=bias)
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(X, W, bias, idx, wts)
+        ctx.mark_non_differentiable(lse)
+        return loss, lse
+
+    @staticmethod
+    def backward(ctx, dloss, _):
+        if torch.is_grad_enabled():  # create_graph: the gradients would count as constants
+            raise NotImplementedError("gmm.cross_entropy has no second derivatives")
+        need = ctx.needs_input_grad
+        if need[4]:
+            raise NotImplementedError("gmm.cross_entropy has no gradient of wts")
+        if dloss is None:
+            return None, None, None, None, None
+        X, W, bias, idx, wts = ctx.saved_tensors
+        _, _, dX, dW, db = cross_entropy_gradients(X, W, idx, dloss=dloss.contiguous(), wts=wts, bias=bias,
+                                                   want_dx=need[0], want_dw=need[1], want_db=need[2])
+        return dX, dW, db, None, None
+
+
+@functools.lru_cache(maxsize=4096)
+def _entropy_bytes(N, d_in, V, x_dtype, gradients):
+    return int(lib().gmm_cross_entropy_workspace_bytes(N, d_in, V, x_dtype, gradients))
+
+
+def cross_entropy_workspace(N: int, d_in: int, V: int, dtype, device, *, gradients: bool = False) -> torch.Tensor:
+    """A device workspace for cross_entropy (or cross_entropy_gradients) with operands of this torch dtype."""
+    return _scratch(_entropy_bytes(N, d_in, V, _DTYPES[dtype], int(gradients)), device, f"N={N} d_in={d_in} V={V}")
+
+
+def _entropy_args(X, W, bias, idx, wts):
+    N, d_in = _matrix(X, "X")
+    dev, t = X.device, X.dtype
+    xt = _xtype(X)
+    V = W.shape[0]
+    _need(W, "W", t, (V, d_in), dev)
+    _optional(bias, "bias", t, (V,), dev)
+    if idx.dim() not in (1, 2):
+        raise ValueError("idx must be N or N x top")
+    top = 1 if idx.dim() == 1 else idx.shape[1]
+    _need(idx, "idx", torch.int32, (N,) if idx.dim() == 1 else (N, top), dev)
+    _optional(wts, "wts", torch.float32, tuple(idx.shape), dev)
+    return N, d_in, V, top, dev, xt
+
+
+def cross_entropy(X, W, idx, *, wts=None, bias=None, ws=None):
+    """Cross entropy of the head X W^T + bias against each row's picks; returns (loss[N], lse[N]) float32, with
+    loss = sum_j wts_j (lse - z[idx_j]) and lse the log-sum-exp of a row's logits.
+
+    X N x d_in, W V x d_in and bias V share one type. idx (N or N x top int32) and wts (the same shape, float32, 1 where
+    None) are those of assign_top2 or kmeans_assign, or any other labels; a pick outside [0, V) counts for nothing. loss
+    carries gradients to X, W and bias (first derivatives; lse carries none), for which the logits are computed again. A
+    training step that knows its loss's gradients beforehand (a mean over the rows) calls cross_entropy_gradients, under
+    torch.no_grad(), and computes them once; so does a captured step."""
+    if _tracked(X, W, bias, wts):
+        return _CrossEntropy.apply(X, W, bias, idx, wts)
+    N, d_in, V, top, dev, xt = _entropy_args(X, W, bias, idx, wts)
+    if dev.index != _current_device():
+        with torch.cuda.device(dev):
+            return cross_entropy(X, W, idx, wts=wts, bias=bias, ws=ws)
+    loss = torch.empty(N, dtype=torch.float32, device=dev)
+    lse = torch.empty(N, dtype=torch.float32, device=dev)
+    if ws is None:
+        ws = cross_entropy_workspace(N, d_in, V, X.dtype, dev)
+    _check("gmm_cross_entropy", lib().gmm_cross_entropy(
+        X.data_ptr(), xt, N, d_in, W.data_ptr(), V, _at(bias), idx.data_ptr(), _at(wts), top, loss.data_ptr(),
+        lse.data_ptr(), *_space(ws, dev), _raw_stream(dev.index)))
+    return loss, lse
+
+
+def cross_entropy_gradients(X, W, idx, *, dloss=None, wts=None, bias=None, want_dx: bool = True, want_dw: bool = True,
+                            want_db: bool = True, ws=None):
+    """cross_entropy with the gradients of sum_n dloss_n loss_n (dloss N float32, 1 where None) in one call: returns
+    (loss, lse, dX, dW, db), the gradients in X's type, None for what is not wanted. A row of no picks, or whose dloss is
+    0, has no part in them."""
+    N, d_in, V, top, dev, xt = _entropy_args(X, W, bias, idx, wts)
+    if dev.index != _current_device():
+        with torch.cuda.device(dev):
+            return cross_entropy_gradients(X, W, idx, dloss=dloss, wts=wts, bias=bias, want_dx=want_dx, want_dw=want_dw,
+                                           want_db=want_db, ws=ws)
+    _optional(dloss, "dloss", torch.float32, (N,), dev)
+    loss = torch.empty(N, dtype=torch.float32, device=dev)
+    lse = torch.empty(N, dtype=torch.float32, device=dev)
+    dX = torch.empty_like(X) if want_dx else None
+    dW = torch.empty_like(W) if want_dw else None
+    db = torch.empty(V, dtype=X.dtype, device=dev) if want_db else None
+    if ws is None:
+        ws = cross_entropy_workspace(N, d_in, V, X.dtype, dev, gradients=True)
+    _check("gmm_cross_entropy_gradients", lib().gmm_cross_entropy_gradients(
+        _at(dloss), X.data_ptr(), xt, N, d_in, W.data_ptr(), V, _at(bias), idx.data_ptr(), _at(wts), top,
+        loss.data_ptr(), lse.data_ptr(), _at(dX), _at(dW), _at(db), *_space(ws, dev), _raw_stream(dev.index)))
+    return loss, lse, dX, dW, db
 
 
 ADAMW_BLOCK = 256  # elements of adamw_step's state that share a scale; each tensor's part starts at a multiple
