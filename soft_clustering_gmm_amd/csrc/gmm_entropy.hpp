@@ -5,28 +5,23 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "gmm_linear.hpp"
+
 namespace gmm {
 
 constexpr int kMaxPicksRow = 8;        // picks of a row
 constexpr int64_t kMaxClasses = 1 << 20;
 constexpr int kEntropyRange = 256;     // parts of the largest gradient of a row
 
-// What the gradient of a row's logits takes: G = up exp(z - base) - d (weights
-// of the picks), and 0 where d is.
-struct RowCoef {
-  float base, up, d, unused;
-};
-
 // Rows of a call, or of a piece of it.
 struct EntropyArgs {
   const void* X;         // [rows][d_in]
   const void* W;         // [V][d_in]
   const void* bias;      // [V] or null
-  const int32_t* idx;    // [rows][top]
-  const float* wts;      // [rows][top] or null: 1
+  RowPicks picks;
   const float* dloss;    // [rows] or null: 1
   int64_t rows;
-  int d_in, V, top;
+  int d_in, V;
   float *loss, *lse;     // [rows], lse nullable
   const float* stats;    // [rows][groups][2] of a kRowStats product, or null: from the logits
   int groups;
@@ -51,11 +46,11 @@ struct EntropyPrep {
   int64_t ld;
   int64_t all_rows;      // 0: no range
   // the picks and losses of all rows, and the first row of X among them
-  const int32_t* idx;
-  const float *wts, *dloss;
+  RowPicks picks;
+  const float* dloss;
   int64_t first;
   float* range;
-  int d_in, V, top;
+  int d_in, V;
 };
 
 template <typename T>

@@ -10,17 +10,6 @@
 
 namespace gmm {
 
-// A row's pick: a class and its weight, -1 and 0 where there is none.
-struct Pick {
-  int v;
-  float w;
-};
-__device__ __forceinline__ Pick pick_of(const int32_t* idx, const float* wts, int64_t at, int V) {
-  const int v = idx[at];
-  const bool is = v >= 0 && v < V;
-  return {is ? v : -1, !is ? 0.f : wts ? wts[at] : 1.f};
-}
-
 // sum exp(z) as s exp(m), m the largest z: what two parts have together. m is
 // -infinity where all z are, or where they are not numbers and s is none.
 struct LogSum {
@@ -55,7 +44,7 @@ __global__ void __launch_bounds__(256) entropy_prep_kernel(const EntropyPrep p) 
       float most = 0.f;
       for (int64_t row = block * 256ll + threadIdx.x; row < p.all_rows; row += kEntropyRange * 256ll) {
         float sum = 0.f;
-        for (int j = 0; j < p.top; ++j) sum += fabsf(pick_of(p.idx, p.wts, row * p.top + j, p.V).w);
+        for (int j = 0; j < p.picks.top; ++j) sum += fabsf(pick_of(p.picks, row, j, p.V).w);
         const float a = sum * fabsf(p.dloss ? p.dloss[row] : 1.f);
         if (a <= FLT_MAX) most = fmaxf(most, a);
       }
@@ -82,7 +71,7 @@ __global__ void __launch_bounds__(256) entropy_prep_kernel(const EntropyPrep p) 
       const int64_t row = p.first + i;
       bool on = false;
       if (!p.dloss || p.dloss[row] != 0.f)
-        for (int j = 0; j < p.top; ++j) on |= pick_of(p.idx, p.wts, row * p.top + j, p.V).w != 0.f;
+        for (int j = 0; j < p.picks.top; ++j) on |= pick_of(p.picks, row, j, p.V).w != 0.f;
       copy_row<T>(x, static_cast<T*>(p.clean) + i * p.ld, on ? p.d_in : 0, p.ld, lane);
     }
   }
@@ -111,14 +100,15 @@ __device__ __forceinline__ float gradient_scale(const EntropyArgs& p) {
 // from its logits, by THREADS threads:
 //   loss = sum_j w_j (log s + (m - z_j)),  lse = m + log s
 // m - z_j first, so that a loss near 0 keeps its digits. The picks' logits are
-// read, or where they are nowhere computed: they are few. Latency bounds it (a
-// wave a row of 2048 parts: 14 us for 4096 rows of 1024 features).
+// read, or where they are nowhere computed, by the threads of the row: they are
+// few. Latency bounds it, so few rows take more threads each.
 // ---------------------------------------------------------------------------
 template <typename T, int THREADS>
-__global__ void __launch_bounds__((THREADS > 256 ? THREADS : 256)) entropy_loss_kernel(const EntropyArgs p) {
+__global__ void __launch_bounds__(THREADS > 256 ? THREADS : 256) entropy_loss_kernel(const EntropyArgs p) {
   constexpr float kInf = __builtin_inff();
-  constexpr int kThreads = (THREADS > 256 ? THREADS : 256), kRows = kThreads / THREADS, kWaves = THREADS > 64 ? THREADS / 64 : 1;
+  constexpr int kThreads = THREADS > 256 ? THREADS : 256, kRows = kThreads / THREADS, kWaves = (THREADS + 63) / 64;
   __shared__ LogSum red[kWaves];
+  __shared__ float dots[kWaves][kMaxPicksRow];
   const int t = threadIdx.x % THREADS, lane = threadIdx.x & 63;
   const float scale = p.coef && p.range ? gradient_scale(p) : 1.f;
   const int64_t row = blockIdx.x * (int64_t)kRows + threadIdx.x / THREADS;
@@ -147,8 +137,31 @@ __global__ void __launch_bounds__((THREADS > 256 ? THREADS : 256)) entropy_loss_
   }
 #pragma unroll
   for (int o = 32; o; o >>= 1) sum = join(sum, LogSum{__shfl_xor(sum.m, o), __shfl_xor(sum.s, o)});
+  // this wave's part of x W_j
+  auto dot = [&](int v) {
+    constexpr int V = Frag<T>::kPer;
+    const T *x = static_cast<const T*>(p.X) + row * p.d_in, *w = static_cast<const T*>(p.W) + (int64_t)v * p.d_in;
+    float of = 0.f;
+#pragma unroll 2
+    for (int c = t * V; c < p.d_in; c += THREADS * V) {
+      float a[V], b[V];
+      load_as<T, V>(x + c, p.d_in - c, a);
+      load_as<T, V>(w + c, p.d_in - c, b);
+#pragma unroll
+      for (int i = 0; i < V; ++i) of = fmaf(a[i], b[i], of);
+    }
+#pragma unroll
+    for (int o = 32; o; o >>= 1) of += __shfl_xor(of, o);
+    return of;
+  };
   if constexpr (THREADS > 64) {
     if (lane == 0) red[threadIdx.x / 64] = sum;
+    if (!z)
+      for (int j = 0; j < p.picks.top; ++j) {
+        const Pick k = pick_of(p.picks, row, j, p.V);
+        const float of = k.w == 0.f ? 0.f : dot(k.v);
+        if (lane == 0) dots[threadIdx.x / 64][j] = of;
+      }
     __syncthreads();
     if (threadIdx.x >= 64) return;
     sum = red[0];
@@ -157,38 +170,42 @@ __global__ void __launch_bounds__((THREADS > 256 ? THREADS : 256)) entropy_loss_
   // one wave goes on
   const float log_sum = logf(sum.s);
   float loss = 0.f, share = 0.f;
-  bool any = false;
-  for (int j = 0; j < p.top; ++j) {
-    const Pick k = pick_of(p.idx, p.wts, row * p.top + j, p.V);
+  RowCoef c{};
+  c.v0 = c.v1 = -1;
+  for (int j = 0; j < p.picks.top; ++j) {
+    const Pick k = pick_of(p.picks, row, j, p.V);
     if (k.w == 0.f) continue;  // the same for the whole wave
-    float of;
+    float of = 0.f;
     if (z) {
       of = z[k.v];
     } else {
-      constexpr int V = Frag<T>::kPer;
-      const T *x = static_cast<const T*>(p.X) + row * p.d_in, *w = static_cast<const T*>(p.W) + (int64_t)k.v * p.d_in;
-      of = 0.f;
-      for (int c = lane * V; c < p.d_in; c += 64 * V) {
-        float a[V], b[V];
-        load_as<T, V>(x + c, p.d_in - c, a);
-        load_as<T, V>(w + c, p.d_in - c, b);
+      if constexpr (THREADS > 64) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) of = fmaf(a[i], b[i], of);
+        for (int w = 0; w < kWaves; ++w) of += dots[w][j];
+      } else {
+        of = dot(k.v);
       }
-#pragma unroll
-      for (int o = 32; o; o >>= 1) of += __shfl_xor(of, o);
       if (p.bias) of += (float)static_cast<const T*>(p.bias)[k.v];
     }
-    any = true;
     share += k.w;
+    if (c.v0 < 0 || c.v0 == k.v)
+      c.v0 = k.v, c.c0 += k.w;
+    else if (c.v1 < 0 || c.v1 == k.v)
+      c.v1 = k.v, c.c1 += k.w;
+    else
+      c.all = 1;
     loss = fmaf(k.w, log_sum + (sum.m - of), loss);
   }
   if (lane == 0) {
     p.loss[row] = loss;
     if (p.lse) p.lse[row] = sum.m == -kInf ? sum.s == 0.f ? -kInf : sum.s : sum.m + log_sum;
     if (p.coef) {
-      const float d = any ? (p.dloss ? p.dloss[row] : 1.f) * scale : 0.f;
-      p.coef[row] = RowCoef{sum.m == -kInf ? 0.f : sum.m, d * share / sum.s, d, 0.f};
+      c.d = c.v0 >= 0 ? (p.dloss ? p.dloss[row] : 1.f) * scale : 0.f;
+      c.base = sum.m == -kInf ? 0.f : sum.m;
+      c.up = c.d * share / sum.s;
+      c.c0 *= c.d;
+      c.c1 *= c.d;
+      p.coef[row] = c;
     }
   }
 }
@@ -224,19 +241,8 @@ __global__ void __launch_bounds__(256) entropy_gradient_kernel(const EntropyArgs
     for (int u = 0; u < kAhead; ++u) {
       const int64_t row = r + 4 * u;
       if (row >= r1) break;
-      const bool on = c[u].d != 0.f;
       float g[V];
-#pragma unroll
-      for (int i = 0; i < V; ++i) g[i] = on && col + i < p.V ? c[u].up * exp_of(z[u][i] - c[u].base) : 0.f;
-      if (on)
-        for (int j = 0; j < p.top; ++j) {
-          const Pick k = pick_of(p.idx, p.wts, row * p.top + j, p.V);
-          const int at = k.v - col;
-          if (k.v >= first && k.v < first + 64 * V)  // the same for the whole wave
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-              if (at == i) g[i] = fmaf(-c[u].d, k.w, g[i]);
-        }
+      logit_gradient<V>(c[u], p.picks, row, col, p.V, z[u], g);
       if (mine) {
         store_as<T, V>(static_cast<T*>(p.G) + row * p.ldz + col, V, g);
         if (p.parts)
@@ -265,8 +271,13 @@ hipError_t launch_entropy_prep(const EntropyPrep& p, hipStream_t s) {
 
 template <typename T>
 hipError_t launch_entropy_loss(const EntropyArgs& p, hipStream_t s) {
-  if (p.stats || p.V <= 2048)
+  const int parts = p.stats ? p.groups : p.V / 4;
+  // a wave a row where the rows fill the device (8 rows of 4096 features, 1024 parts: 9.8 us, by 256 threads 5.8)
+  const int threads = p.rows >= 1024 ? (parts <= 2048 ? 64 : 1024) : parts <= 128 ? 64 : parts <= 4096 ? 256 : 1024;
+  if (threads == 64)
     entropy_loss_kernel<T, 64><<<(unsigned)((p.rows + 3) / 4), 256, 0, s>>>(p);
+  else if (threads == 256)
+    entropy_loss_kernel<T, 256><<<(unsigned)p.rows, 256, 0, s>>>(p);
   else
     entropy_loss_kernel<T, 1024><<<(unsigned)p.rows, 1024, 0, s>>>(p);
   return hipGetLastError();

@@ -92,9 +92,9 @@ inline void set_cut(ProductArgs& p, const Cut& c) {
 }
 
 template <typename T>
-hipError_t run_product(const Cut& c, bool as, bool bs, int act, ProductArgs& p, hipStream_t s) {
+hipError_t run_product(const Cut& c, bool as, bool bs, int act, ProductArgs& p, hipStream_t s, bool stream = true) {
   set_cut(p, c);
-  p.c_stream = p.M * p.N * (p.c_f32 ? 4 : (int64_t)sizeof(T)) >= kStreamBytes;
+  p.c_stream = stream && p.M * p.N * (p.c_f32 ? 4 : (int64_t)sizeof(T)) >= kStreamBytes;
   hipError_t e = launch_product<T>(c.variant, as, bs, act, p, s);
   p.sum_blocks = 0;  // once
   if (e == hipSuccess && c.splits > 1) e = launch_reduce<T>(act, p, s);

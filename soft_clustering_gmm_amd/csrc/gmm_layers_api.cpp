@@ -106,7 +106,7 @@ static hipError_t linear_forward(const T* X, int64_t N, int d_in, const T* W, in
                                  const void* residual, void* Y, int y_f32, void* pre, char* ws, hipStream_t s) {
   const LinearPlan l = linear_plan(N, d_in, d_out, sizeof(T));
   if (l.few) {
-    const FewArgs f{X, W, (int)N, d_out, d_in, bias, residual, Y, pre, y_f32, d_out};
+    const FewArgs f{X, W, (int)N, d_out, d_in, bias, residual, Y, pre, y_f32, d_out, nullptr};
     return launch_few<T>(act, f, s);
   }
   const int ey = y_f32 ? 4 : (int)sizeof(T);

@@ -6,6 +6,22 @@
 
 namespace gmm {
 
+// What the gradient of a row's logits takes:
+//   G_v = up exp(z_v - base) - c0 [v = v0] - c1 [v = v1],
+// 0 where d is; where `all`, the picks are the row's own, times d.
+struct RowCoef {
+  float base, up;
+  int v0, v1;
+  float c0, c1, d;
+  int all;
+};
+static_assert(sizeof(RowCoef) == 32, "two loads of 16 bytes");
+struct RowPicks {
+  const int32_t* idx;  // [rows][top]
+  const float* wts;    // [rows][top] or null: 1
+  int top;
+};
+
 // One product C[m][n] = sum_k A(m, k) B(n, k) on 16-byte aligned operands.
 // An operand is "k-contiguous" (element (r, k) at p[r * ld + k]) or
 // "k-strided" (element (r, k) at p[k * ld + r]); ld * element size is a
@@ -39,6 +55,13 @@ struct ProductArgs {
   // act kRowStats and kStatsToo: the largest z of each row and group of columns and
   // the sum of exp(z - it): [M][groups][2], groups as stat_groups() says
   float* stats;
+  // act kLogitGradient: of the rows of C, which has the operands' type and zeros
+  // from N to the end of its last 16 bytes; column sums of the rounded C times
+  // *parts_unscale (null: 1), two for each tile's rows: [2 tiles_m][N], or null
+  const RowCoef* coef;
+  RowPicks picks;
+  float* parts;
+  const float* parts_unscale;
   const float* unscale;  // C = *unscale times the product, where not null (gradients of 2-byte operands)
 };
 constexpr int kSumCols = 16;  // columns of such a block
@@ -53,8 +76,10 @@ constexpr int64_t kStreamBytes = 64ll << 20;
 enum { kTile256 = 0, kTile128 = 1, kTile64 = 2, kTileVariants = 3 };
 constexpr int kTileRows[kTileVariants] = {256, 128, 64};
 constexpr int kStepBytes = 128;  // bytes of k per step and operand row
-// In the place of an activation: statistics of the rows instead of C, or beside it.
-constexpr int kRowStats = 6, kStatsToo = 7;
+// In the place of an activation: statistics of the rows instead of C, or beside
+// it; the gradient of a cross entropy whose logits z are.
+constexpr int kRowStats = 6, kStatsToo = 7, kLogitGradient = 8;
+
 
 // Groups of columns whose statistics such a product of N columns writes:
 // those of a wave, 4 in a tile, or 2 where its waves are 2 x 2.
@@ -79,7 +104,11 @@ struct FewArgs {
   void* pre;
   int c_f32;
   int64_t ldc;
+  float* stats;  // act kRowStats, as in ProductArgs: groups of 16 few_tiles() columns
 };
+// Tiles of 16 rows of B a block. More than two blocks a CU: two, which halves
+// what is read of A; a single row is one address for all lanes and costs little.
+inline int few_tiles(int M, int N) { return N >= 16 * 512 && M > 1 ? 2 : 1; }
 
 template <typename T>
 hipError_t launch_product(int variant, bool a_strided, bool b_strided, int act, const ProductArgs& p, hipStream_t s);

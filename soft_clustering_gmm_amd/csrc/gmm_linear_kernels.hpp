@@ -206,6 +206,19 @@ __device__ __forceinline__ void finish_row(const ProductArgs& p, int64_t m, int 
   const int left = p.N - n;
 #pragma unroll
   for (int i = 0; i < W; ++i) z[i] += bias[i];
+  if constexpr (ACT == kLogitGradient) {
+    RowCoef c;
+    __builtin_memcpy(&c, res, sizeof(c));
+    float g[W];
+    logit_gradient<W>(c, p.picks, m, n, p.N, z, g);
+    if (p.c_stream)
+      store_as<T, W, true>(static_cast<T*>(p.C) + at, W, g);
+    else
+      store_as<T, W>(static_cast<T*>(p.C) + at, W, g);
+#pragma unroll
+    for (int i = 0; i < W; ++i) z[i] = (float)(T)g[i];  // for the column sums
+    return;
+  }
   if (p.pre) store_row<T, W>(p.pre, at, left, p.c_f32, z);
 #pragma unroll
   for (int i = 0; i < W; ++i) z[i] = act_value<ACT>(z[i]);
@@ -435,16 +448,25 @@ product_kernel(const ProductArgs p) {
   if (whole && p.bias && n < p.N) load_as<T, W>(static_cast<const T*>(p.bias) + n, p.N - n, bias);
   // The next 16 rows' residual is on its way while these are finished: C may be
   // the residual, so the compiler keeps a load behind the stores before it.
-  float res[2][Q][W];
+  constexpr int R = ACT == kLogitGradient ? sizeof(RowCoef) / 4 : W;  // or the row's coefficients in its place
+  float res[2][Q][R];
   auto row_of = [&](int i, int q) {
     return at.m0 + i / MI * HM + wm * TM + 16 * (i % MI) + q * kRows + lane / kChunks;
   };
   auto fetch = [&](int i) {
 #pragma unroll
     for (int q = 0; q < Q; ++q)
-      if (whole && row_of(i, q) < p.M && n < p.N) load_residual<T, W>(p, row_of(i, q), n, res[i & 1][q]);
+      if (whole && row_of(i, q) < p.M && n < p.N) {
+        if constexpr (ACT == kLogitGradient)
+          load_as<float, R>(reinterpret_cast<const float*>(p.coef + row_of(i, q)), R, res[i & 1][q]);
+        else
+          load_residual<T, W>(p, row_of(i, q), n, res[i & 1][q]);
+      }
   };
   fetch(0);
+  float cols[W];
+#pragma unroll
+  for (int i = 0; i < W; ++i) cols[i] = 0.f;
 #pragma unroll
   for (int i = 0; i < 2 * MI; ++i) {
     if (i + 1 < 2 * MI) fetch(i + 1);
@@ -467,13 +489,28 @@ product_kernel(const ProductArgs p) {
         for (int k = 0; k < W; ++k) z[k] *= unscale;
       const int64_t m = row_of(i, q);
       if (m < p.M && n < p.N) {
-        if (whole)
+        if (whole) {
           finish_row<T, ACT, W>(p, m, n, z, bias, res[i & 1][q]);
-        else
+          if (ACT == kLogitGradient)
+#pragma unroll
+            for (int k = 0; k < W; ++k) cols[k] += z[k];
+        } else
           store_as<float, W>(p.partial + ((int64_t)at.part * p.M + m) * p.N + n, p.N - n, z);
       }
     }
     wave_lds_order();
+  }
+  if constexpr (ACT == kLogitGradient) {
+    if (!p.parts) return;
+    const float unscaled = p.parts_unscale ? *p.parts_unscale : 1.f;
+#pragma unroll
+    for (int o = kChunks; o < 64; o *= 2)
+#pragma unroll
+      for (int k = 0; k < W; ++k) cols[k] += __shfl_xor(cols[k], o);
+#pragma unroll
+    for (int k = 0; k < W; ++k) cols[k] *= unscaled;
+    static_assert(WM == 2, "two sums for a tile's rows");
+    if (lane < kChunks && n < p.N) store_as<float, W>(p.parts + (at.m0 / BM * WM + wm) * (int64_t)p.N + n, p.N - n, cols);
   }
 }
 
@@ -544,6 +581,31 @@ __global__ void __launch_bounds__(64 * NW) few_kernel(const FewArgs p) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) red[wave][r][16 * j + 4 * g + q] = acc[0][j][q];
   __syncthreads();
+  if constexpr (ACT == kRowStats) {
+    constexpr float kInf = __builtin_inff();
+    for (int i = threadIdx.x; i < 16 * NB; i += 64 * NW) {
+      const int n = i % NB, m = i / NB;
+      float z = -kInf;
+      if (n0 + n < p.N) {
+        z = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) z += red[w][m][n];
+        if (p.bias) z += (float)static_cast<const T*>(p.bias)[n0 + n];
+      }
+      float most = z;
+#pragma unroll
+      for (int o = NB / 2; o; o >>= 1) most = fmaxf(most, __shfl_xor(most, o));
+      float sum = exp_of(z - (most == -kInf ? 0.f : most));
+#pragma unroll
+      for (int o = NB / 2; o; o >>= 1) sum += __shfl_xor(sum, o);
+      if (n == 0 && m < p.M) {
+        float* out = p.stats + 2 * ((int64_t)m * gridDim.x + blockIdx.x);
+        out[0] = most;
+        out[1] = sum;
+      }
+    }
+    return;
+  }
   for (int i = threadIdx.x; i < 16 * NB; i += 64 * NW) {
     const int n = i % NB, m = i / NB;
     if (m >= p.M || n0 + n >= p.N) continue;
@@ -753,6 +815,10 @@ hipError_t launch_product(int variant, bool a_strided, bool b_strided, int act, 
     launch_tile<T, false, false, kStatsToo>(variant, p, s);
     return hipGetLastError();
   }
+  if (act == kLogitGradient) {
+    launch_tile<T, false, false, kLogitGradient>(variant, p, s);
+    return hipGetLastError();
+  }
   if (!a_strided && !b_strided)
     return with_act<T, true>(act, p.c_f32, [&](auto a) {
       launch_tile<T, false, false, decltype(a)::value>(variant, p, s);
@@ -768,16 +834,16 @@ hipError_t launch_product(int variant, bool a_strided, bool b_strided, int act, 
 
 template <typename T>
 hipError_t launch_few(int act, const FewArgs& p, hipStream_t s) {
-  return with_act<T, true>(act, p.c_f32, [&](auto a) {
+  auto go = [&](auto a) {
     constexpr int ACT = decltype(a)::value;
-    // more than two blocks a CU: two tiles a block, which halves what is read
-    // of A; a single row is one address for all lanes and costs little
-    if (p.N >= 16 * 512 && p.M > 1)
+    if (few_tiles(p.M, p.N) == 2)
       few_kernel<T, 8, 2, ACT><<<(p.N + 31) / 32, 512, 0, s>>>(p);
     else
       few_kernel<T, 8, 1, ACT><<<(p.N + 15) / 16, 512, 0, s>>>(p);
     return hipGetLastError();
-  });
+  };
+  if (act == kRowStats) return go(std::integral_constant<int, kRowStats>{});
+  return with_act<T, true>(act, p.c_f32, go);
 }
 
 static unsigned blocks_for(int64_t items) {

@@ -40,7 +40,8 @@ inline NormShape norm_shape(int64_t D, int e) {
     if (pieces <= 64 * c) return {64, c};
   for (int c = 1; c * v <= kNormKeep; c *= 2)
     if (pieces <= 256 * c) return {256, c};
-  int c = 1;
+  int c = kNormKeep / v;
+  if (pieces <= 512 * c) return {512, c};
   while (pieces > 1024 * c) c *= 2;
   return {1024, c};
 }
@@ -51,7 +52,7 @@ inline int norm_parts(int64_t N, int64_t D, int e) {
   const NormShape s = norm_shape(D, e);
   if (!norm_keeps(s, e)) return (int)(N < 128 ? N : 128);
   const int64_t at_once = s.group < 256 ? 256 / s.group : 1, blocks = (N + at_once - 1) / at_once;
-  const int64_t most = s.group == 1024 ? 256 : 1024;
+  const int64_t most = s.group == 1024 ? 256 : s.group == 512 ? 512 : 1024;
   return (int)(blocks < most ? blocks : most);
 }
 

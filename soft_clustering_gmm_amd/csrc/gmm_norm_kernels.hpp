@@ -9,63 +9,128 @@
 
 namespace gmm {
 
-// The W weights from column c on; `otherwise` where there are none.
-template <typename TY, int W>
-__device__ __forceinline__ void load_weights(const void* p, int c, int left, int w_f32, float otherwise, float* out) {
-  if (p && left > 0) {
-    load_row<TY, W>(p, c, left, w_f32, out);
-  } else {
-#pragma unroll
-    for (int i = 0; i < W; ++i) out[i] = otherwise;
+// How the pieces of a row's threads lie: whole ones; the last one moved back to
+// end with the row, so that it begins with elements that the piece before has,
+// too; or the row is shorter than a piece. A part of a piece would be loaded
+// element by element behind a branch, and waited for there.
+enum { kWhole = 0, kMoved = 1, kTiny = 2 };
+
+template <int W, int LIE>
+struct Span {
+  int at;    // first column
+  int skip;  // elements that are not this thread's, from the first on
+  int left;  // kTiny: elements of the row from `at` on
+  __device__ __forceinline__ Span(int col, int D) {
+    at = LIE == kTiny ? col : min(col, D - W);
+    skip = LIE == kTiny ? 0 : col - at;
+    left = D - at;
   }
-}
+  __device__ __forceinline__ bool mine(int i) const {
+    return LIE == kTiny ? i < left : LIE == kWhole ? skip == 0 : i >= skip;
+  }
+  // The elements as they lie in memory; what loads several and then uses the
+  // first waits for the first alone. kMoved: all are inside the row, mine or not;
+  // else what is not mine is 0.
+  template <typename E>
+  __device__ __forceinline__ void load(const E* row, E* e) const {
+    if constexpr (LIE == kTiny) {
+#pragma unroll
+      for (int i = 0; i < W; ++i) e[i] = i < left ? row[at + i] : (E)0.f;
+    } else if (LIE == kMoved || skip == 0) {
+      __builtin_memcpy(e, row + at, sizeof(E) * W);
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i) e[i] = (E)0.f;
+    }
+  }
+  // Elements that two threads have get the same value from both.
+  template <typename E>
+  __device__ __forceinline__ void store(E* row, const float* v) const {
+    if (LIE == kTiny)
+      store_as<E, W>(row + at, left, v);
+    else if (skip < W)
+      store_as<E, W>(row + at, W, v);
+  }
+  // Weights of the row's columns, `otherwise` where there are none.
+  template <typename TY>
+  __device__ __forceinline__ void weights(const void* p, int w_f32, float otherwise, float* out) const {
+    if (p) {
+      load_row<TY, W>(p, at, LIE == kTiny ? left : W, w_f32, out);
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i) out[i] = otherwise;
+    }
+  }
+};
 
 constexpr int norm_threads(int group) { return group > 256 ? group : 256; }
 
 // ---------------------------------------------------------------------------
-// Forward. A row stays in the registers of its G threads: its mean, then the
-// sums of the deviations d and of d^2, whose mean the first one's rounding has
-// left: var = (sum d^2 - (sum d)^2 / D) / D. So a row with a mean far from 0
-// loses no more than the rounding of its x. HBM bounds it: X is read once and
-// Y written once.
+// Forward. A row stays in the registers of its G threads, as it lies in memory:
+// its mean, then the sums of the deviations d and of d^2, whose mean the first
+// one's rounding has left: var = (sum d^2 - (sum d)^2 / D) / D. So a row with a
+// mean far from 0 loses no more than the rounding of its x. HBM bounds it: X is
+// read once and Y written once (32768 x 4096 in bfloat16: NORMFWD). Rows of more
+// than 16384 elements are read three times, the others from the caches: held,
+// they would spill.
 // ---------------------------------------------------------------------------
-template <typename TX, typename TY, int G, int C>
+template <typename TX, typename TY, int G, int C, int LIE>
 __global__ void __launch_bounds__(norm_threads(G)) norm_kernel(const NormArgs p) {
   constexpr int V = 16 / (int)sizeof(TX), kRows = norm_threads(G) / G;
-  constexpr bool kKeep = C * V <= kNormKeep;  // the weights stay in registers
+  constexpr bool kKeep = C * V <= kNormKeep;  // row and weights stay in registers
+  constexpr bool kAhead = kKeep && G <= 512;  // the next row is on its way while one is finished
+  constexpr int kHeld = kKeep ? C : 1, kUnroll = kKeep ? C : 1;
   __shared__ float red[2][G > 64 ? G / 64 : 1][2];
   int turn = 0;
   const int t = threadIdx.x % G, D = p.D;
   const float inv = 1.f / (float)D;
-  float gamma[kKeep ? C : 1][V], beta[kKeep ? C : 1][V];
+  const int64_t step = (int64_t)gridDim.x * kRows;
+  int64_t row = blockIdx.x * (int64_t)kRows + threadIdx.x / G;
+  auto span = [&](int c) { return Span<V, LIE>((c * G + t) * V, D); };
+  struct Piece {
+    TX e[V];
+  } x[kHeld], next[kAhead ? C : 1];
+  auto piece = [&](int64_t r, int c, Piece& to) { span(c).load(static_cast<const TX*>(p.X) + r * D, to.e); };
+  auto fetch = [&](int64_t r, Piece* to) {
+    if (kKeep && r < p.N)
+#pragma unroll
+      for (int c = 0; c < kHeld; ++c) piece(r, c, to[c]);
+  };
+  fetch(row, x);
+  float gamma[kHeld][V], beta[kHeld][V];
+  auto weights = [&](int c, float* ga, float* be) {
+    span(c).template weights<TY>(p.gamma, p.w_f32, 1.f, ga);
+    span(c).template weights<TY>(p.beta, p.w_f32, 0.f, be);
+  };
   if (kKeep)
 #pragma unroll
+    for (int c = 0; c < kHeld; ++c) weights(c, gamma[c], beta[c]);
+  for (; row < p.N; row += step) {
+    if constexpr (kAhead) fetch(row + step, next);
+    float sum[2] = {0.f, 0.f};
+#pragma unroll kUnroll
     for (int c = 0; c < C; ++c) {
-      const int col = (c * G + t) * V;
-      load_weights<TY, V>(p.gamma, col, D - col, p.w_f32, 1.f, gamma[c]);
-      load_weights<TY, V>(p.beta, col, D - col, p.w_f32, 0.f, beta[c]);
-    }
-  for (int64_t row = blockIdx.x * (int64_t)kRows + threadIdx.x / G; row < p.N; row += (int64_t)gridDim.x * kRows) {
-    const TX* x = static_cast<const TX*>(p.X) + row * D;
-    float d[C][V], sum[2] = {0.f, 0.f};
+      const int w = kKeep ? c : 0;
+      const auto own = span(c);
+      if (!kKeep) piece(row, c, x[0]);
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int col = (c * G + t) * V;
-      load_as<TX, V>(x + col, D - col, d[c]);
-#pragma unroll
-      for (int i = 0; i < V; ++i) sum[0] += d[c][i];
+      for (int i = 0; i < V; ++i) sum[0] += LIE != kMoved || own.mine(i) ? (float)x[w].e[i] : 0.f;
     }
     row_sum<G, 1>(sum, red, turn);
-    float mean = sum[0] * inv;
+    const float mean = sum[0] * inv;
     sum[0] = 0.f;
-#pragma unroll
-    for (int c = 0; c < C; ++c)
+#pragma unroll kUnroll
+    for (int c = 0; c < C; ++c) {
+      const int w = kKeep ? c : 0;
+      const auto own = span(c);
+      if (!kKeep) piece(row, c, x[0]);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        d[c][i] = (c * G + t) * V + i < D ? d[c][i] - mean : 0.f;
-        sum[0] += d[c][i];
-        sum[1] = fmaf(d[c][i], d[c][i], sum[1]);
+        const float d = own.mine(i) ? (float)x[w].e[i] - mean : 0.f;
+        sum[0] += d;
+        sum[1] = fmaf(d, d, sum[1]);
       }
+    }
     row_sum<G, 2>(sum, red, turn);
     const float shift = sum[0] * inv;
     const float rstd = 1.f / sqrtf(fmaxf(fmaf(-shift, shift, sum[1] * inv), 0.f) + p.eps);
@@ -73,18 +138,23 @@ __global__ void __launch_bounds__(norm_threads(G)) norm_kernel(const NormArgs p)
       p.stats[2 * row] = mean + shift;
       p.stats[2 * row + 1] = rstd;
     }
-    TY* y = static_cast<TY*>(p.Y) + row * D;
-#pragma unroll
+#pragma unroll kUnroll
     for (int c = 0; c < C; ++c) {
-      const int col = (c * G + t) * V;
+      const int w = kKeep ? c : 0;
       if (!kKeep) {
-        load_weights<TY, V>(p.gamma, col, D - col, p.w_f32, 1.f, gamma[0]);
-        load_weights<TY, V>(p.beta, col, D - col, p.w_f32, 0.f, beta[0]);
+        piece(row, c, x[0]);
+        weights(c, gamma[0], beta[0]);
       }
+      float out[V];
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        d[c][i] = fmaf((d[c][i] - shift) * rstd, gamma[kKeep ? c : 0][i], beta[kKeep ? c : 0][i]);
-      store_as<TY, V>(y + col, D - col, d[c]);
+      for (int i = 0; i < V; ++i) out[i] = fmaf(((float)x[w].e[i] - mean - shift) * rstd, gamma[w][i], beta[w][i]);
+      span(c).store(static_cast<TY*>(p.Y) + row * D, out);
+    }
+    if constexpr (kAhead) {
+#pragma unroll
+      for (int c = 0; c < C; ++c) x[c] = next[c];
+    } else {
+      fetch(row + step, x);
     }
   }
 }
@@ -92,66 +162,101 @@ __global__ void __launch_bounds__(norm_threads(G)) norm_kernel(const NormArgs p)
 // ---------------------------------------------------------------------------
 // Backward. With h = (x - mean) rstd and k = dY gamma,
 //   dX = rstd (k - mean(k) - h mean(k h)),  dgamma = sum dY h,  dbeta = sum dY.
-// One read of X and dY: a thread keeps its columns' sums over the rows that its
-// block takes; they go to `partial` and are added in a fixed order.
+// One read of X and dY (two of rows of more than 16384 elements, the second from
+// the caches): a thread keeps its columns' sums over the rows that its
+// block takes; they go to `partial` and are added in a fixed order. HBM bounds
+// it (16384 x 2048, float X and bfloat16 dY: NORMBWD).
 // ---------------------------------------------------------------------------
-template <typename TX, typename TY, int G, int C>
+template <typename TX, typename TY, int G, int C, int LIE>
 __global__ void __launch_bounds__(norm_threads(G)) norm_backward_kernel(const NormArgs p) {
   constexpr int V = 16 / (int)sizeof(TX), kThreads = norm_threads(G), kRows = kThreads / G;
   constexpr bool kKeep = C * V <= kNormKeep;
+  constexpr bool kAhead = kKeep && G <= 512;  // the next row is on its way while one is finished
+  constexpr int kHeld = kKeep ? C : 1, kUnroll = kKeep ? C : 1;
+  constexpr bool kGamma = kKeep && G <= 512;  // gamma, too (of 1024 threads it would spill)
   __shared__ float red[2][G > 64 ? G / 64 : 1][2];
   __shared__ float sums[kKeep && kRows > 1 ? kRows : 1][kKeep && kRows > 1 ? G * C * V : 1];
   int turn = 0;
   const int t = threadIdx.x % G, group = threadIdx.x / G, D = p.D;
   const float inv = 1.f / (float)D;
-  float gamma[kKeep ? C : 1][V], dg[kKeep ? C : 1][V], db[kKeep ? C : 1][V];
+  const int64_t step = (int64_t)gridDim.x * kRows;
+  int64_t row = blockIdx.x * (int64_t)kRows + group;
+  auto span = [&](int c) { return Span<V, LIE>((c * G + t) * V, D); };
+  struct Piece {
+    TX x[V];
+    TY y[V];
+  };
+  struct Row {
+    Piece e[kHeld];
+    float mean, rstd;
+  };
+  auto piece = [&](int64_t r, int c, Piece& to) {
+    span(c).load(static_cast<const TX*>(p.X) + r * D, to.x);
+    span(c).load(static_cast<const TY*>(p.dY) + r * D, to.y);
+  };
+  auto fetch = [&](int64_t r, Row& to) {
+    if (r >= p.N) return;
+    if (kKeep)
+#pragma unroll
+      for (int c = 0; c < kHeld; ++c) piece(r, c, to.e[c]);
+    to.mean = p.stats[2 * r];
+    to.rstd = p.stats[2 * r + 1];
+  };
+  Row now, next;
+  fetch(row, now);
+  float gamma[kGamma ? C : 1][V], dg[kHeld][V], db[kHeld][V];
   if (kKeep)
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int col = (c * G + t) * V;
-      load_weights<TY, V>(p.gamma, col, D - col, p.w_f32, 1.f, gamma[c]);
+    for (int c = 0; c < kHeld; ++c) {
+      if (kGamma) span(c).template weights<TY>(p.gamma, p.w_f32, 1.f, gamma[kGamma ? c : 0]);
 #pragma unroll
       for (int i = 0; i < V; ++i) dg[c][i] = db[c][i] = 0.f;
     }
-  for (int64_t row = blockIdx.x * (int64_t)kRows + group; row < p.N; row += (int64_t)gridDim.x * kRows) {
-    const TX* x = static_cast<const TX*>(p.X) + row * D;
-    const TY* dy = static_cast<const TY*>(p.dY) + row * D;
-    const float mean = p.stats[2 * row], rstd = p.stats[2 * row + 1];
-    float h[C][V], k[C][V], sum[2] = {0.f, 0.f};
-#pragma unroll
+  for (; row < p.N; row += step) {
+    if constexpr (kAhead) fetch(row + step, next);
+    float sum[2] = {0.f, 0.f};
+#pragma unroll kUnroll
     for (int c = 0; c < C; ++c) {
-      const int col = (c * G + t) * V;
-      load_as<TX, V>(x + col, D - col, h[c]);
-      load_as<TY, V>(dy + col, D - col, k[c]);
-    }
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int col = (c * G + t) * V;
-      if (!kKeep) load_weights<TY, V>(p.gamma, col, D - col, p.w_f32, 1.f, gamma[0]);
+      const int w = kKeep ? c : 0;
+      const auto own = span(c);
+      if (!kKeep) piece(row, c, now.e[0]);
+      if (!kGamma) own.template weights<TY>(p.gamma, p.w_f32, 1.f, gamma[0]);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        h[c][i] = (h[c][i] - mean) * rstd;
-        if (kKeep && col + i < D) {  // beyond the row dY is 0, h need not be finite
-          dg[c][i] = fmaf(k[c][i], h[c][i], dg[c][i]);
-          db[c][i] += k[c][i];
+        // what is another's counts as 0; beyond the row dY is
+        const float dy = LIE != kMoved || own.mine(i) ? (float)now.e[w].y[i] : 0.f;
+        const float h = ((float)now.e[w].x[i] - now.mean) * now.rstd;
+        if (kKeep) {
+          dg[w][i] = fmaf(dy, h, dg[w][i]);
+          db[w][i] += dy;
         }
-        if (col + i >= D) h[c][i] = 0.f;
-        k[c][i] *= gamma[kKeep ? c : 0][i];
-        sum[0] += k[c][i];
-        sum[1] = fmaf(k[c][i], h[c][i], sum[1]);
+        const float k = dy * gamma[kGamma ? c : 0][i];
+        sum[0] += k;
+        sum[1] = fmaf(k, h, sum[1]);
       }
     }
-    if (!p.dX) continue;  // the same for all threads
-    row_sum<G, 2>(sum, red, turn);
-    const float a = sum[0] * inv, b = sum[1] * inv;
-    TX* dx = static_cast<TX*>(p.dX) + row * D;
+    if (p.dX) {  // the same for all threads
+      row_sum<G, 2>(sum, red, turn);
+      const float a = sum[0] * inv, b = sum[1] * inv;
+#pragma unroll kUnroll
+      for (int c = 0; c < C; ++c) {
+        const int w = kKeep ? c : 0;
+        const auto own = span(c);
+        if (!kKeep) piece(row, c, now.e[0]);
+        if (!kGamma) own.template weights<TY>(p.gamma, p.w_f32, 1.f, gamma[0]);
+        float out[V];
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int col = (c * G + t) * V;
-#pragma unroll
-      for (int i = 0; i < V; ++i) k[c][i] = rstd * (k[c][i] - fmaf(h[c][i], b, a));
-      store_as<TX, V>(dx + col, D - col, k[c]);
+        for (int i = 0; i < V; ++i) {
+          const float h = ((float)now.e[w].x[i] - now.mean) * now.rstd;
+          out[i] = now.rstd * ((float)now.e[w].y[i] * gamma[kGamma ? c : 0][i] - fmaf(h, b, a));
+        }
+        own.store(static_cast<TX*>(p.dX) + row * D, out);
+      }
     }
+    if constexpr (kAhead)
+      now = next;
+    else
+      fetch(row + step, now);
   }
   if constexpr (kKeep) {
     if (!p.partial) return;
@@ -159,18 +264,25 @@ __global__ void __launch_bounds__(norm_threads(G)) norm_backward_kernel(const No
     if constexpr (kRows == 1) {
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        const int col = (c * G + t) * V;
-        store_as<float, V>(out + col, D - col, dg[c]);
-        store_as<float, V>(out + D + col, D - col, db[c]);
+        const auto own = span(c);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (own.mine(i)) {
+            out[own.at + i] = dg[c][i];
+            out[D + own.at + i] = db[c][i];
+          }
       }
     } else {
 #pragma unroll
       for (int both = 0; both < 2; ++both) {
         __syncthreads();
 #pragma unroll
-        for (int c = 0; c < C; ++c)
+        for (int c = 0; c < C; ++c) {
+          const auto own = span(c);
 #pragma unroll
-          for (int i = 0; i < V; ++i) sums[group][(c * G + t) * V + i] = both ? db[c][i] : dg[c][i];
+          for (int i = 0; i < V; ++i)
+            if (own.mine(i)) sums[group][own.at + i] = both ? db[c][i] : dg[c][i];
+        }
         __syncthreads();
         for (int col = threadIdx.x; col < D; col += kThreads) {
           float s = 0.f;
@@ -245,35 +357,40 @@ __global__ void __launch_bounds__(64 * kNormSlices) norm_finish_kernel(const Nor
 
 // f with the row shape's group and pieces as constants.
 template <int V, typename F>
-void with_norm_shape(NormShape s, F&& f) {
+void with_norm_shape(NormShape s, int D, F&& f3) {
   using std::integral_constant;
+  auto f = [&](auto g, auto c) {
+    if (D % V == 0) return f3(g, c, integral_constant<int, kWhole>{});
+    if constexpr (decltype(g)::value == 8)
+      if (D < V) return f3(g, c, integral_constant<int, kTiny>{});
+    f3(g, c, integral_constant<int, kMoved>{});
+  };
   auto pieces = [&](auto g, auto most) {
     constexpr int kMost = decltype(most)::value;
     if (s.pieces == 1) return f(g, integral_constant<int, 1>{});
     if constexpr (kMost >= 2)
       if (s.pieces == 2) return f(g, integral_constant<int, 2>{});
-    if constexpr (kMost >= 4)
-      if (s.pieces == 4) return f(g, integral_constant<int, 4>{});
-    if constexpr (kMost >= 8)
-      if (s.pieces == 8) return f(g, integral_constant<int, 8>{});
-    if constexpr (kMost >= 16) return f(g, integral_constant<int, 16>{});
+    if constexpr (kMost >= 4) f(g, integral_constant<int, 4>{});
   };
   constexpr integral_constant<int, kNormKeep / V> few{};
   if (s.group == 8) return f(integral_constant<int, 8>{}, integral_constant<int, 1>{});
   if (s.group == 16) return f(integral_constant<int, 16>{}, integral_constant<int, 1>{});
   if (s.group == 64) return pieces(integral_constant<int, 64>{}, few);
   if (s.group == 256) return pieces(integral_constant<int, 256>{}, few);
-  pieces(integral_constant<int, 1024>{}, integral_constant<int, 64 / V>{});
+  if (s.group == 512) return f(integral_constant<int, 512>{}, few);
+  if (s.pieces == few) return f(integral_constant<int, 1024>{}, few);
+  if (s.pieces == 2 * few) return f(integral_constant<int, 1024>{}, integral_constant<int, 2 * few>{});
+  f(integral_constant<int, 1024>{}, integral_constant<int, 4 * few>{});
 }
 
 template <typename TX, typename TY>
 hipError_t launch_norm(const NormArgs& p, hipStream_t s) {
   constexpr int V = 16 / (int)sizeof(TX);
   const NormShape shape = norm_shape(p.D, sizeof(TX));
-  with_norm_shape<V>(shape, [&](auto g, auto c) {
+  with_norm_shape<V>(shape, p.D, [&](auto g, auto c, auto lie) {
     constexpr int G = decltype(g)::value, kThreads = norm_threads(G), kRows = kThreads / G;
-    const int64_t blocks = (p.N + kRows - 1) / kRows, most = G == 1024 ? 512 : 2048;
-    norm_kernel<TX, TY, G, decltype(c)::value><<<(unsigned)(blocks < most ? blocks : most), kThreads, 0, s>>>(p);
+    const int64_t blocks = (p.N + kRows - 1) / kRows, most = G == 1024 ? 512 : G == 512 ? 1024 : 2048;
+    norm_kernel<TX, TY, G, decltype(c)::value, decltype(lie)::value><<<(unsigned)(blocks < most ? blocks : most), kThreads, 0, s>>>(p);
   });
   return hipGetLastError();
 }
@@ -288,9 +405,9 @@ hipError_t launch_norm_backward(const NormArgs& p, hipStream_t s) {
     norm_columns_kernel<TX, TY><<<across * p.parts, 256, 0, s>>>(p, across, (p.N + p.parts - 1) / p.parts);
   }
   if (p.dX || (p.partial && keeps))
-    with_norm_shape<V>(shape, [&](auto g, auto c) {
+    with_norm_shape<V>(shape, p.D, [&](auto g, auto c, auto lie) {
       constexpr int G = decltype(g)::value;
-      norm_backward_kernel<TX, TY, G, decltype(c)::value>
+      norm_backward_kernel<TX, TY, G, decltype(c)::value, decltype(lie)::value>
           <<<norm_parts(p.N, keeps ? p.D : 1 << 14, sizeof(TX)), norm_threads(G), 0, s>>>(p);
     });
   if (p.partial) norm_finish_kernel<TY><<<(2 * p.D + 63) / 64, 64 * kNormSlices, 0, s>>>(p);

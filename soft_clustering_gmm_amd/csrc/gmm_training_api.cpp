@@ -48,15 +48,17 @@ static int64_t piece_rows(int64_t N, int64_t bytes, int64_t most) {
   return std::min(N, std::min<int64_t>(rows, 1 << 20));
 }
 constexpr int64_t kStatPiece = 256ll << 20;   // bytes of a piece's statistics
-constexpr int64_t kLogitPiece = 2048ll << 20; // bytes of a piece's logits
+// Bytes of a piece's logits: dW is read and written once for each (8192 x 2048
+// to 65536 classes: 6062 us in one piece, 6884 in four, 8009 in eight).
+constexpr int64_t kLogitPiece = 2048ll << 20;
 
-// Workspace of the loss: [padded rows of X of a piece] [padded W] [statistics]
-// or, for few rows, [logits].
+// Workspace of the loss: [padded rows of X of a piece] [padded W] [statistics].
 struct EntropyPlan {
   bool few, pad;
-  int64_t lx, ldz, piece;
+  int64_t lx, piece;
+  int groups;
   Cut cut;
-  size_t o_x, o_w, o_z, bytes;
+  size_t o_x, o_w, o_stats, bytes;
 };
 
 static EntropyPlan entropy_plan(int64_t N, int d_in, int V, int e) {
@@ -64,26 +66,36 @@ static EntropyPlan entropy_plan(int64_t N, int d_in, int V, int e) {
   l.few = N <= kFewRows;
   l.lx = row_len(d_in, e);
   l.pad = l.lx != d_in && !l.few;
-  l.ldz = ceil_div(V, 8) * 8;
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t o = off;
     off = align_up(off + bytes, 256);
     return o;
   };
-  l.piece = N;
-  if (!l.few) {
+  if (l.few) {
+    l.piece = N;
+    l.groups = (int)ceil_div(V, 16 * few_tiles((int)N, V));
+  } else {
     l.piece = piece_rows(N, ceil_div(V, 32) * 8, kStatPiece);
     l.cut = choose_cut(l.piece, V, d_in, e, 1);
-    l.o_x = take(l.pad ? (size_t)l.piece * l.lx * e : 0);
-    l.o_w = take(l.pad ? (size_t)V * l.lx * e : 0);
-    l.o_z = take((size_t)l.piece * stat_groups(l.cut.variant, e, V) * 2 * sizeof(float));
-  } else {
-    l.o_z = take((size_t)N * l.ldz * sizeof(float));
+    l.groups = stat_groups(l.cut.variant, e, V);
   }
+  l.o_x = take(l.pad ? (size_t)l.piece * l.lx * e : 0);
+  l.o_w = take(l.pad ? (size_t)V * l.lx * e : 0);
+  l.o_stats = take((size_t)l.piece * l.groups * 2 * sizeof(float));
   l.bytes = off;
   return l;
 }
+
+// Up to so many features, and where the logits are more than the caches keep at
+// hand, they are computed twice, once for the loss and once for their gradient,
+// and not written to memory (8192 rows to 32768 classes in bfloat16, against
+// once: 64 features 674 us and 1159, 512 1231 and 1425, 1024 2043 and 2007; to
+// 8192 in float: 64 features 416 and 469, 128 646 and 637; 4096 rows to 4096
+// classes in bfloat16, 64 MiB: 64 features 72 and 82, 512 147 and 146; 1000 rows
+// to 8000, 32 MiB: 512 features 92 and 89; 8192 to 1024 in float: 91 and 84).
+constexpr int kTwice = 896, kTwiceF32 = 96;
+constexpr int64_t kTwiceBytes = 32ll << 20;
 
 // Workspace of the gradients, for a piece of rows: [padded X] [X without the
 // rows that have no gradient] [padded W] [logits] [their gradient] [statistics]
@@ -91,8 +103,16 @@ static EntropyPlan entropy_plan(int64_t N, int d_in, int V, int e) {
 // and scale].
 struct EntropyBackPlan {
   bool few, pad;
+  bool twice;  // the logits are computed twice and not written
   int64_t lx, ldz, piece, chunk, chunks;  // chunks: of all rows
   size_t o_x, o_clean, o_w, o_z, o_g, o_stats, o_coef, o_acc, o_part, o_db, o_range, bytes;
+
+  // Tiles of the logits' product: whole sums where it is not written.
+  Cut logits(int64_t rows, int V, int d_in, int e) const { return choose_cut(rows, V, d_in, e, twice ? 1 : 256); }
+  // Column sums of a column that a piece's gradient leaves.
+  int64_t sums(int64_t rows, int V, int d_in, int e) const {
+    return twice ? 2 * ceil_div(rows, kTileRows[logits(rows, V, d_in, e).variant]) : ceil_div(rows, chunk);
+  }
 };
 
 static EntropyBackPlan entropy_back_plan(int64_t N, int d_in, int V, int e) {
@@ -102,9 +122,13 @@ static EntropyBackPlan entropy_back_plan(int64_t N, int d_in, int V, int e) {
   l.pad = l.lx != d_in;
   l.ldz = ceil_div(V, 8) * 8;
   l.piece = piece_rows(N, l.ldz * (int64_t)sizeof(float), kLogitPiece);
-  // column sums: chunks of 64 rows at least, 1024 of them at most; a piece is whole chunks, or all there is
-  l.chunk = std::min(l.piece, std::max<int64_t>(64, ceil_div(ceil_div(N, 1024), 64) * 64));
-  l.chunks = ceil_div(l.piece, l.chunk) * (N / l.piece) + ceil_div(N % l.piece, l.chunk);
+  l.twice = !l.few && d_in <= (e == 2 ? kTwice : kTwiceF32) && l.piece * l.ldz * (int64_t)sizeof(float) > kTwiceBytes;
+  // Rows of a block that has columns of G: 16 at least (of 1001 rows and 7777 classes in half 64 make a block a CU, 17.9
+  // us, and 16 CHUNK16), more while 2048 blocks are left, and no more than 1024 column sums of a column.
+  const int64_t across = ceil_div(l.ldz, 64 * (16 / e));
+  l.chunk = std::max<int64_t>(16, std::min<int64_t>(64, l.piece * across / 2048 / 16 * 16));
+  l.chunk = std::min(l.piece, std::max(l.chunk, ceil_div(ceil_div(N, 1024), 16) * 16));
+  l.chunks = l.sums(l.piece, V, d_in, e) * (N / l.piece) + (N % l.piece ? l.sums(N % l.piece, V, d_in, e) : 0);
   size_t off = 0, part = 0, stats = 0;
   auto take = [&](size_t bytes) {
     const size_t o = off;
@@ -114,7 +138,7 @@ static EntropyBackPlan entropy_back_plan(int64_t N, int d_in, int V, int e) {
   for (int64_t rows : {l.piece, N % l.piece})
     if (rows) {
       if (!l.few) {
-        const Cut c = choose_cut(rows, V, d_in, e);
+        const Cut c = l.logits(rows, V, d_in, e);
         part = std::max(part, partial_bytes(c, rows, V));
         stats = std::max(stats, (size_t)rows * stat_groups(c.variant, e, V) * 2 * sizeof(float));
       }
@@ -124,7 +148,7 @@ static EntropyBackPlan entropy_back_plan(int64_t N, int d_in, int V, int e) {
   l.o_x = take(l.pad && !l.few ? (size_t)l.piece * l.lx * e : 0);
   l.o_clean = take((size_t)l.piece * l.lx * e);
   l.o_w = take(l.pad ? (size_t)V * l.lx * e : 0);
-  l.o_z = take((size_t)l.piece * l.ldz * sizeof(float));
+  l.o_z = take(l.twice ? 0 : (size_t)l.piece * l.ldz * sizeof(float));
   l.o_g = take((size_t)l.piece * l.ldz * e);
   l.o_stats = take(stats);
   l.o_coef = take((size_t)l.piece * sizeof(RowCoef));
@@ -161,16 +185,15 @@ static hipError_t entropy_forward(EntropyArgs a, int64_t N, char* ws, hipStream_
   for (int64_t r = 0; r < N; r += l.piece) {
     a.rows = std::min(N - r, l.piece);
     a.X = row_at(static_cast<const T*>(all.X), r, a.d_in);
-    a.idx = row_at(all.idx, r, a.top);
-    a.wts = row_at(all.wts, r, a.top);
+    a.picks.idx = row_at(all.picks.idx, r, a.picks.top);
+    a.picks.wts = row_at(all.picks.wts, r, a.picks.top);
     a.loss = row_at(all.loss, r, 1);
     a.lse = row_at(all.lse, r, 1);
+    a.stats = p.stats = reinterpret_cast<float*>(ws + l.o_stats);
     if (l.few) {
-      float* z = reinterpret_cast<float*>(ws + l.o_z);
-      const FewArgs f{a.X, a.W, (int)N, a.V, a.d_in, a.bias, nullptr, z, nullptr, 1, l.ldz};
-      if ((e = launch_few<T>(GMM_ACT_NONE, f, s)) != hipSuccess) return e;
-      a.Z = z;
-      a.ldz = l.ldz;
+      const FewArgs f{a.X, a.W, (int)N, a.V, a.d_in, a.bias, nullptr, nullptr, nullptr, 1, 0, p.stats};
+      a.groups = l.groups;
+      if ((e = launch_few<T>(kRowStats, f, s)) != hipSuccess) return e;
       return launch_entropy_loss<T>(a, s);
     }
     p.A = a.X;
@@ -182,10 +205,8 @@ static hipError_t entropy_forward(EntropyArgs a, int64_t N, char* ws, hipStream_
       p.B = ws + l.o_w;
     }
     p.M = a.rows;
-    p.stats = reinterpret_cast<float*>(ws + l.o_z);
     if ((e = run_product<T>(l.cut, false, false, kRowStats, p, s)) != hipSuccess) return e;
-    a.stats = p.stats;
-    a.groups = stat_groups(l.cut.variant, sizeof(T), a.V);
+    a.groups = l.groups;
     if ((e = launch_entropy_loss<T>(a, s)) != hipSuccess) return e;
   }
   return e;
@@ -211,26 +232,27 @@ static hipError_t entropy_gradients(EntropyArgs a, int64_t N, T* dX, T* dW, T* d
     const int64_t rows = a.rows = std::min(N - r, l.piece);
     const bool last = r + rows == N;
     a.X = row_at(static_cast<const T*>(all.X), r, a.d_in);
-    a.idx = row_at(all.idx, r, a.top);
-    a.wts = row_at(all.wts, r, a.top);
+    a.picks.idx = row_at(all.picks.idx, r, a.picks.top);
+    a.picks.wts = row_at(all.picks.wts, r, a.picks.top);
     a.dloss = row_at(all.dloss, r, 1);
     a.loss = row_at(all.loss, r, 1);
     a.lse = row_at(all.lse, r, 1);
     EntropyPrep b{};
-    b.X = a.X, b.ld = l.lx, b.d_in = a.d_in, b.V = a.V, b.top = a.top;
+    b.X = a.X, b.ld = l.lx, b.d_in = a.d_in, b.V = a.V;
     b.x = pad_x ? ws + l.o_x : nullptr;
     b.clean = dW ? ws + l.o_clean : nullptr;
     b.rows = b.x || b.clean ? rows : 0;
     b.W = a.W, b.w = pad_w && r == 0 ? ws + l.o_w : nullptr;
     b.all_rows = scaled && r == 0 ? N : 0;
-    b.idx = all.idx, b.wts = all.wts, b.dloss = all.dloss, b.first = r, b.range = a.range;
+    b.picks = all.picks, b.dloss = all.dloss, b.first = r, b.range = a.range;
     if ((e = launch_entropy_prep<T>(b, s)) != hipSuccess) return e;
     ProductArgs p{};
     p.partial = reinterpret_cast<float*>(ws + l.o_part);
-    // the logits
+    // the logits, through the caches, which the next kernel finds them in (2048 x 1024 to 32768 classes: 580 us against
+    // 598 past them)
     a.stats = nullptr;
     if (l.few) {
-      const FewArgs f{a.X, a.W, (int)N, a.V, a.d_in, a.bias, nullptr, const_cast<float*>(a.Z), nullptr, 1, l.ldz};
+      const FewArgs f{a.X, a.W, (int)N, a.V, a.d_in, a.bias, nullptr, const_cast<float*>(a.Z), nullptr, 1, l.ldz, nullptr};
       e = launch_few<T>(GMM_ACT_NONE, f, s);
     } else {
       p.A = pad_x ? ws + l.o_x : a.X;
@@ -238,18 +260,29 @@ static hipError_t entropy_gradients(EntropyArgs a, int64_t N, T* dX, T* dW, T* d
       p.M = rows, p.N = a.V, p.K = a.d_in;
       p.bias = a.bias;
       p.C = const_cast<float*>(a.Z), p.ldc = l.ldz, p.c_f32 = 1;
-      const Cut c = choose_cut(rows, a.V, a.d_in, sizeof(T));
+      const Cut c = l.logits(rows, a.V, a.d_in, sizeof(T));
       if (c.splits == 1) {  // whole sums: the tiles' statistics with them
         a.stats = p.stats = reinterpret_cast<float*>(ws + l.o_stats);
         a.groups = stat_groups(c.variant, sizeof(T), a.V);
       }
-      e = run_product<T>(c, false, false, a.stats ? kStatsToo : (int)GMM_ACT_NONE, p, s);
+      a.Z = l.twice ? nullptr : reinterpret_cast<float*>(ws + l.o_z);
+      e = run_product<T>(c, false, false, l.twice ? kRowStats : a.stats ? kStatsToo : (int)GMM_ACT_NONE, p, s, false);
+      if (e == hipSuccess && l.twice) e = launch_entropy_loss<T>(a, s);
+      if (e == hipSuccess && l.twice && (dX || dW || db)) {  // again, for their gradient
+        p.coef = a.coef;
+        p.picks = a.picks;
+        p.parts = a.parts;
+        p.parts_unscale = scaled ? a.range + kEntropyRange : nullptr;
+        p.C = a.G;
+        p.c_f32 = sizeof(T) == 4;
+        e = run_product<T>(c, false, false, kLogitGradient, p, s, false);
+      }
     }
     if (e != hipSuccess) return e;
-    if ((e = launch_entropy_loss<T>(a, s)) != hipSuccess) return e;
+    if (!l.twice && (e = launch_entropy_loss<T>(a, s)) != hipSuccess) return e;
     if (!dX && !dW && !db) continue;
-    if ((e = launch_entropy_gradient<T>(a, s)) != hipSuccess) return e;
-    if (db) a.parts += ceil_div(rows, l.chunk) * a.V;
+    if (!l.twice && (e = launch_entropy_gradient<T>(a, s)) != hipSuccess) return e;
+    if (db) a.parts += l.sums(rows, a.V, a.d_in, sizeof(T)) * a.V;
     p = ProductArgs{};
     p.partial = reinterpret_cast<float*>(ws + l.o_part);
     p.N = a.d_in;
@@ -364,7 +397,7 @@ int gmm_cross_entropy(const void* X, int32_t x_dtype, int64_t N, int32_t d_in, c
   if (N == 0) return GMM_OK;
   if ((st = check_ws(workspace, ws_bytes, entropy_plan(N, d_in, V, e).bytes))) return st;
   EntropyArgs a{};
-  a.X = X, a.W = W, a.bias = bias, a.idx = idx, a.wts = wts, a.d_in = d_in, a.V = V, a.top = top;
+  a.X = X, a.W = W, a.bias = bias, a.picks = RowPicks{idx, wts, top}, a.d_in = d_in, a.V = V;
   a.loss = loss, a.lse = lse;
   return with_type(x_dtype, [&](auto* t) {
     using T = std::remove_pointer_t<decltype(t)>;
@@ -384,7 +417,7 @@ int gmm_cross_entropy_gradients(const float* dloss, const void* X, int32_t x_dty
   if (row_len(d_in, e) == d_in && (!aligned16(X) || !aligned16(W))) return GMM_EINVAL;
   if (N > 0 && (st = check_ws(workspace, ws_bytes, entropy_back_plan(N, d_in, V, e).bytes))) return st;
   EntropyArgs a{};
-  a.X = X, a.W = W, a.bias = bias, a.idx = idx, a.wts = wts, a.dloss = dloss, a.d_in = d_in, a.V = V, a.top = top;
+  a.X = X, a.W = W, a.bias = bias, a.picks = RowPicks{idx, wts, top}, a.dloss = dloss, a.d_in = d_in, a.V = V;
   a.loss = loss, a.lse = lse;
   return with_type(x_dtype, [&](auto* t) {
     using T = std::remove_pointer_t<decltype(t)>;

@@ -128,7 +128,7 @@ def test_against_64_bits(G, monkeypatch, i, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("N,d,V", [(4090, 520, 8190), (8200, 1000, 2050), (2040, 136, 33001)])
+@pytest.mark.parametrize("N,d,V", [(4090, 520, 8190), (8200, 1000, 2050), (2040, 136, 33001), (4090, 72, 4101)])
 def test_large_tiles(G, monkeypatch, N, d, V, dtype):
     monkeypatch.setattr(oracle, "ON", "cuda")
     t = TYPES[dtype]
@@ -146,10 +146,10 @@ def test_large_tiles(G, monkeypatch, N, d, V, dtype):
     compare(lse, want[1], bounds[1], "lse")
 
 
-@pytest.mark.parametrize("dtype", sorted(TYPES))
-def test_pieces_of_rows(G, dtype):
-    """A million classes: 512 rows of logits at a time, with dW and db summed over three pieces."""
-    N, d, V = 1100, 16, 1 << 20
+@pytest.mark.parametrize("dtype,N,d", [("f32", 1100, 16), ("f16", 1100, 16), ("bf16", 1100, 16), ("bf16", 600, 904)])
+def test_pieces_of_rows(G, dtype, N, d):
+    """A million classes: 512 rows of logits at a time, with dW and db summed over the pieces."""
+    V = 1 << 20
     t = TYPES[dtype]
     X, W, b, idx, wts, dloss = inputs(N, d, V, 2, t, True, True, seed=3, on="cuda")
     got = G.cross_entropy_gradients(X, W, idx, dloss=dloss, wts=wts, bias=b)
@@ -179,7 +179,7 @@ def test_pieces_of_rows(G, dtype):
     for a, w, what in ((got[3], dw, "dw"), (got[4], db, "db")):
         assert (a.double() - w).norm() <= (2e-4 + 2 * oracle.EPS[t] / 2) * w.norm(), what
     # pieces of another size, the same rows: the last piece alone
-    tail = slice(1024, N)
+    tail = slice(N // 512 * 512, N)
     alone = G.cross_entropy_gradients(X[tail], W, idx[tail], dloss=dloss[tail], wts=wts[tail], bias=b)
     assert (alone[1] - got[1][tail]).abs().max() < 1e-4
 
