@@ -23,7 +23,7 @@ struct NormArgs {
   int parts;                 // blocks (or chunks of rows) that write partial sums
 };
 
-// A row is shared by G threads with C pieces of 16 bytes of X each.
+// A row is shared by `group` threads with `pieces` pieces of 16 bytes of X each.
 struct NormShape {
   int group, pieces;
 };
@@ -47,12 +47,16 @@ inline NormShape norm_shape(int64_t D, int e) {
 }
 inline bool norm_keeps(NormShape s, int e) { return s.pieces * 16 / e <= kNormKeep; }
 
-// Blocks of the backward kernel, or chunks of rows of the kernel by columns.
+// Blocks of the backward kernel, or chunks of rows of the kernel by columns. Each
+// leaves sums, so no more of them than keep HBM busy: fewer where a thread has
+// two pieces or more in flight (bfloat16, 16384 x 4096: 86 us with 512 blocks, 107
+// with 1024; 8192 x 8192, 512 threads a row: 97 with 256, 107 with 512), not where
+// it has one (32768 x 2048: 106 with 512, 88 with 1024).
 inline int norm_parts(int64_t N, int64_t D, int e) {
   const NormShape s = norm_shape(D, e);
   if (!norm_keeps(s, e)) return (int)(N < 128 ? N : 128);
   const int64_t at_once = s.group < 256 ? 256 / s.group : 1, blocks = (N + at_once - 1) / at_once;
-  const int64_t most = s.group == 1024 ? 256 : s.group == 512 ? 512 : 1024;
+  const int64_t most = s.group >= 512 ? 256 : s.pieces > 1 ? 512 : 1024;
   return (int)(blocks < most ? blocks : most);
 }
 

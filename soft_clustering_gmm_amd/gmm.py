@@ -8,8 +8,10 @@ this module on a machine without it raises immediately.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import functools
+import operator
 import os
 
 import torch
@@ -883,8 +885,21 @@ def cross_entropy_gradients(X, W, idx, *, dloss=None, wts=None, bias=None, want_
 ADAMW_BLOCK = 256  # elements of adamw_step's state that share a scale; each tensor's part starts at a multiple
 
 
-def _state_elements(params):
-    return sum(-(-p.numel() // ADAMW_BLOCK) for p in params) * ADAMW_BLOCK
+# Over hundreds of tensors a step is as long as its host time: what is asked of each goes through these.
+_ptr_of, _numel_of, _size_of = torch.Tensor.data_ptr, torch.Tensor.numel, torch.Tensor.size
+_contiguous, _index_of, _dtype_of = torch.Tensor.is_contiguous, torch.Tensor.get_device, torch.Tensor.dtype.__get__
+
+
+def _state_elements(sizes):
+    return sum([-(-n // ADAMW_BLOCK) for n in sizes]) * ADAMW_BLOCK
+
+
+def _need_all(tensors, dtype, index, what):
+    """Every one contiguous, of this type and on this GPU."""
+    if not (set(map(_dtype_of, tensors)) <= {dtype} and set(map(_index_of, tensors)) <= {index}
+            and all(map(_contiguous, tensors))):
+        raise ValueError(f"{what}: expected contiguous {dtype} on cuda:{index}, got "
+                         f"{[(t.dtype, tuple(t.shape), tuple(t.stride()), str(t.device)) for t in tensors][:8]}")
 
 
 def adamw_state(params, *, bits: int = 32, master: bool = False) -> dict:
@@ -896,7 +911,7 @@ def adamw_state(params, *, bits: int = 32, master: bool = False) -> dict:
         raise ValueError(f"bits must be 8 or 32, got {bits}")
     if not params:
         raise ValueError("no parameters")
-    dev, total = params[0].device, _state_elements(params)
+    dev, total = params[0].device, _state_elements([p.numel() for p in params])
     state = {k: torch.zeros(total, dtype=torch.float32 if bits == 32 else torch.uint8, device=dev) for k in ("m", "v")}
     state["step"] = torch.zeros(2, dtype=torch.int64, device=dev)
     if bits == 8:
@@ -937,25 +952,24 @@ def adamw_step(params, grads, m, v, step, *, m_scale=None, v_scale=None, master=
             return adamw_step(params, grads, m, v, step, m_scale=m_scale, v_scale=v_scale, master=master, lr=lr,
                               beta1=beta1, beta2=beta2, eps=eps, weight_decay=weight_decay, lr_factor=lr_factor,
                               grad_factor=grad_factor)
+    given, stepped = grads, params
+    if any([g is None for g in grads]):
+        given = [g for g in grads if g is not None]
+        stepped = [p for p, g in zip(params, grads) if g is not None]
     pt = params[0].dtype if n else torch.float32
-    gt = next((g.dtype for g in grads if g is not None), pt)
+    gt = given[0].dtype if given else pt
     if pt not in _DTYPES or gt != pt and gt != torch.float32:
         raise ValueError(f"parameters must be float32, float16 or bfloat16 and gradients theirs or float32, got {pt}, {gt}")
-    sizes, at, spans = [], [], []
-    for p, g in zip(params, grads):
-        if p.dtype != pt or p.device != dev or not p.is_contiguous():
-            raise ValueError(f"parameter: expected contiguous {pt} on {dev}, got {p.dtype} {tuple(p.shape)} on {p.device}")
-        sizes.append(p.numel())
-        at.append(p.data_ptr())
-        if g is not None and (g.dtype != gt or g.shape != p.shape or g.device != dev or not g.is_contiguous()):
-            raise ValueError(f"gradient: expected contiguous {gt} {tuple(p.shape)} on {dev}, got {g.dtype} "
-                             f"{tuple(g.shape)} on {g.device}")
-    e = pt.itemsize
-    spans = sorted((a, k) for a, k in zip(at, sizes) if k)
-    for (a, k), (b, _) in zip(spans, spans[1:]):
-        if a + k * e > b:
-            raise ValueError("two parameters share memory")
-    total = _state_elements(params)
+    _need_all(params, pt, dev.index, "parameters")
+    _need_all(given, gt, dev.index, "gradients")
+    if list(map(_size_of, stepped)) != list(map(_size_of, given)):
+        raise ValueError("a gradient has another shape than its parameter")
+    sizes, at = list(map(_numel_of, params)), list(map(_ptr_of, params))
+    # none overlap: in order, none starts before the last one's end
+    ends = sorted([a + k * pt.itemsize for a, k in zip(at, sizes) if k])
+    if not all(map(operator.le, ends, sorted([a for a, k in zip(at, sizes) if k])[1:])):
+        raise ValueError("two parameters share memory")
+    total = _state_elements(sizes)
     st = m.dtype
     if st != torch.float32 and st != torch.float8_e4m3fn:
         raise ValueError(f"m must be float32 or float8_e4m3fn, got {st}")
@@ -970,14 +984,15 @@ def adamw_step(params, grads, m, v, step, *, m_scale=None, v_scale=None, master=
     _optional(master, "master", torch.float32, (total,), dev)
     if master is not None and pt == torch.float32:
         raise ValueError("float32 parameters have no master copies")
+    of = list(map(_ptr_of, grads)) if given is grads else [0 if g is None else g.data_ptr() for g in grads]
+    sizes, at, of = array.array("q", sizes), array.array("Q", at), array.array("Q", of)
     _check("gmm_adamw_step", lib().gmm_adamw_step(
-        n, (ctypes.c_int64 * n)(*sizes), (ctypes.c_void_p * n)(*at), _DTYPES[pt],
-        (ctypes.c_void_p * n)(*[None if g is None else g.data_ptr() for g in grads]), _DTYPES[gt], _at(master),
+        n, sizes.buffer_info()[0], at.buffer_info()[0], _DTYPES[pt], of.buffer_info()[0], _DTYPES[gt], _at(master),
         m.data_ptr(), v.data_ptr(), 32 if st == torch.float32 else 8, _at(m_scale), _at(v_scale), step.data_ptr(), lr,
         beta1, beta2, eps, weight_decay, _device_factor(lr_factor, "lr_factor", dev),
         _device_factor(grad_factor, "grad_factor", dev), _raw_stream(dev.index)))
     # a graph that has saved a parameter says so when it comes to it
-    torch.autograd.graph.increment_version([p for p, g in zip(params, grads) if g is not None])
+    torch.autograd.graph.increment_version(stepped)
 
 
 def peak_mfma(precision: int, trips: int, blocks: int, out: torch.Tensor) -> float:
