@@ -136,8 +136,7 @@ struct AdamLane {
       const float x = (float)g[k] * s.scale_g;
       m[k] = s.beta1 * m[k] + s.rest1 * x;
       v[k] = s.beta2 * v[k] + s.rest2 * x * x;
-      // held in 8 bits, sqrt(v) is the nearest float; a last place is no matter to a step
-      const float r = F8 ? sqrtf(v[k]) : __builtin_amdgcn_sqrtf(v[k]);
+      const float r = sqrtf(v[k]);  // the instruction alone would take a denormal v for 0
       const float old = MASTER ? master[k] : (float)p[k];
       master[k] = fmaf(s.keep, old, -(s.rate * m[k] * __builtin_amdgcn_rcpf(fmaf(r, s.root, s.eps))));
       p[k] = (TP)master[k];

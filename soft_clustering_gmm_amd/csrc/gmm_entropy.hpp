@@ -62,4 +62,10 @@ hipError_t launch_entropy_loss(const EntropyArgs& p, hipStream_t s);
 template <typename T>
 hipError_t launch_entropy_gradient(const EntropyArgs& p, hipStream_t s);
 
+// `count` rows of V column sums to kFoldedSums or fewer: those of each group of
+// fold_rows(count) added up.
+constexpr int kFoldedSums = 256;
+inline int64_t fold_rows(int64_t count) { return (count + kFoldedSums - 1) / kFoldedSums; }
+hipError_t launch_entropy_fold(const float* parts, int64_t count, int V, float* out, hipStream_t s);
+
 }  // namespace gmm

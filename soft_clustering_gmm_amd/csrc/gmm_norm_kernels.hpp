@@ -43,12 +43,18 @@ struct Span {
       for (int i = 0; i < W; ++i) e[i] = (E)0.f;
     }
   }
-  // Elements that two threads have get the same value from both.
-  template <typename E>
+  // Elements that two threads have get the same value from both. ALONE: each
+  // stores its own alone, where the other may read the row once more before it
+  // does (the output may lie over the input).
+  template <bool ALONE, typename E>
   __device__ __forceinline__ void store(E* row, const float* v) const {
     if (LIE == kTiny)
       store_as<E, W>(row + at, left, v);
-    else if (skip < W)
+    else if (ALONE && LIE == kMoved && skip > 0) {
+#pragma unroll
+      for (int i = 0; i < W; ++i)
+        if (mine(i)) row[at + i] = (E)v[i];
+    } else if (skip < W)
       store_as<E, W>(row + at, W, v);
   }
   // Weights of the row's columns, `otherwise` where there are none.
@@ -148,7 +154,7 @@ __global__ void __launch_bounds__(norm_threads(G)) norm_kernel(const NormArgs p)
       float out[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) out[i] = fmaf(((float)x[w].e[i] - mean - shift) * rstd, gamma[w][i], beta[w][i]);
-      span(c).store(static_cast<TY*>(p.Y) + row * D, out);
+      span(c).template store<!kKeep>(static_cast<TY*>(p.Y) + row * D, out);
     }
     if constexpr (kAhead) {
 #pragma unroll
@@ -250,7 +256,7 @@ __global__ void __launch_bounds__(norm_threads(G)) norm_backward_kernel(const No
           const float h = ((float)now.e[w].x[i] - now.mean) * now.rstd;
           out[i] = now.rstd * ((float)now.e[w].y[i] * gamma[kGamma ? c : 0][i] - fmaf(h, b, a));
         }
-        own.store(static_cast<TX*>(p.dX) + row * D, out);
+        own.template store<!kKeep>(static_cast<TX*>(p.dX) + row * D, out);
       }
     }
     if constexpr (kAhead)

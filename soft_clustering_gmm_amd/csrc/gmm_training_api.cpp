@@ -99,19 +99,24 @@ constexpr int64_t kTwiceBytes = 32ll << 20;
 
 // Workspace of the gradients, for a piece of rows: [padded X] [X without the
 // rows that have no gradient] [padded W] [logits] [their gradient] [statistics]
-// [coefficients] [dW so far] [partial sums of the products] [column sums] [range
-// and scale].
+// [coefficients] [dW so far] [partial sums of the products] [column sums of the
+// tiles] [column sums] [range and scale].
 struct EntropyBackPlan {
   bool few, pad;
   bool twice;  // the logits are computed twice and not written
   int64_t lx, ldz, piece, chunk, chunks;  // chunks: of all rows
-  size_t o_x, o_clean, o_w, o_z, o_g, o_stats, o_coef, o_acc, o_part, o_db, o_range, bytes;
+  size_t o_x, o_clean, o_w, o_z, o_g, o_stats, o_coef, o_acc, o_part, o_fold, o_db, o_range, bytes;
 
   // Tiles of the logits' product: whole sums where it is not written.
   Cut logits(int64_t rows, int V, int d_in, int e) const { return choose_cut(rows, V, d_in, e, twice ? 1 : 256); }
-  // Column sums of a column that a piece's gradient leaves.
-  int64_t sums(int64_t rows, int V, int d_in, int e) const {
+  // Sums of a column that a piece's gradient leaves, and what is kept of them: those of many tiles are added up first.
+  int64_t tile_sums(int64_t rows, int V, int d_in, int e) const {
     return twice ? 2 * ceil_div(rows, kTileRows[logits(rows, V, d_in, e).variant]) : ceil_div(rows, chunk);
+  }
+  bool folds(int64_t rows, int V, int d_in, int e) const { return twice && tile_sums(rows, V, d_in, e) > kFoldedSums; }
+  int64_t sums(int64_t rows, int V, int d_in, int e) const {
+    const int64_t n = tile_sums(rows, V, d_in, e);
+    return folds(rows, V, d_in, e) ? ceil_div(n, fold_rows(n)) : n;
   }
 };
 
@@ -129,7 +134,7 @@ static EntropyBackPlan entropy_back_plan(int64_t N, int d_in, int V, int e) {
   l.chunk = std::max<int64_t>(16, std::min<int64_t>(64, l.piece * across / 2048 / 16 * 16));
   l.chunk = std::min(l.piece, std::max(l.chunk, ceil_div(ceil_div(N, 1024), 16) * 16));
   l.chunks = l.sums(l.piece, V, d_in, e) * (N / l.piece) + (N % l.piece ? l.sums(N % l.piece, V, d_in, e) : 0);
-  size_t off = 0, part = 0, stats = 0;
+  size_t off = 0, part = 0, stats = 0, fold = 0;
   auto take = [&](size_t bytes) {
     const size_t o = off;
     off = align_up(off + bytes, 256);
@@ -144,6 +149,7 @@ static EntropyBackPlan entropy_back_plan(int64_t N, int d_in, int V, int e) {
       }
       part = std::max(part, partial_bytes(choose_cut(rows, d_in, V, e), rows, d_in));
       part = std::max(part, partial_bytes(choose_cut(V, d_in, rows, e), V, d_in));
+      if (l.folds(rows, V, d_in, e)) fold = std::max(fold, (size_t)l.tile_sums(rows, V, d_in, e) * V * sizeof(float));
     }
   l.o_x = take(l.pad && !l.few ? (size_t)l.piece * l.lx * e : 0);
   l.o_clean = take((size_t)l.piece * l.lx * e);
@@ -154,6 +160,7 @@ static EntropyBackPlan entropy_back_plan(int64_t N, int d_in, int V, int e) {
   l.o_coef = take((size_t)l.piece * sizeof(RowCoef));
   l.o_acc = take(l.piece < N && e == 2 ? (size_t)V * d_in * sizeof(float) : 0);
   l.o_part = take(part);
+  l.o_fold = take(fold);
   l.o_db = take((size_t)l.chunks * V * sizeof(float));
   l.o_range = take((kEntropyRange + 1) * sizeof(float));
   l.bytes = off;
@@ -271,11 +278,14 @@ static hipError_t entropy_gradients(EntropyArgs a, int64_t N, T* dX, T* dW, T* d
       if (e == hipSuccess && l.twice && (dX || dW || db)) {  // again, for their gradient
         p.coef = a.coef;
         p.picks = a.picks;
-        p.parts = a.parts;
+        const bool folds = db && l.folds(rows, a.V, a.d_in, sizeof(T));
+        p.parts = folds ? reinterpret_cast<float*>(ws + l.o_fold) : a.parts;
         p.parts_unscale = scaled ? a.range + kEntropyRange : nullptr;
         p.C = a.G;
         p.c_f32 = sizeof(T) == 4;
         e = run_product<T>(c, false, false, kLogitGradient, p, s, false);
+        if (e == hipSuccess && folds)
+          e = launch_entropy_fold(p.parts, l.tile_sums(rows, a.V, a.d_in, sizeof(T)), a.V, a.parts, s);
       }
     }
     if (e != hipSuccess) return e;

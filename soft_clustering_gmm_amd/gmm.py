@@ -786,8 +786,8 @@ class _CrossEntropy(torch.autograd.Function):
     """cross_entropy in torch's graph: its backward pass is cross_entropy_gradients."""
 
     @staticmethod
-    def forward(ctx, X, W, bias, idx, wts):
-        loss, lse = cross_entropy(X, W, idx, wts=wts, bias=bias)
+    def forward(ctx, X, W, bias, idx, wts, ws):
+        loss, lse = cross_entropy(X, W, idx, wts=wts, bias=bias, ws=ws)
         ctx.set_materialize_grads(False)
         ctx.save_for_backward(X, W, bias, idx, wts)
         ctx.mark_non_differentiable(lse)
@@ -801,11 +801,11 @@ class _CrossEntropy(torch.autograd.Function):
         if need[4]:
             raise NotImplementedError("gmm.cross_entropy has no gradient of wts")
         if dloss is None:
-            return None, None, None, None, None
+            return None, None, None, None, None, None
         X, W, bias, idx, wts = ctx.saved_tensors
         _, _, dX, dW, db = cross_entropy_gradients(X, W, idx, dloss=dloss.contiguous(), wts=wts, bias=bias,
                                                    want_dx=need[0], want_dw=need[1], want_db=need[2])
-        return dX, dW, db, None, None
+        return dX, dW, db, None, None, None
 
 
 @functools.lru_cache(maxsize=4096)
@@ -843,7 +843,7 @@ def cross_entropy(X, W, idx, *, wts=None, bias=None, ws=None):
     training step that knows its loss's gradients beforehand (a mean over the rows) calls cross_entropy_gradients, under
     torch.no_grad(), and computes them once; so does a captured step."""
     if _tracked(X, W, bias, wts):
-        return _CrossEntropy.apply(X, W, bias, idx, wts)
+        return _CrossEntropy.apply(X, W, bias, idx, wts, ws)
     N, d_in, V, top, dev, xt = _entropy_args(X, W, bias, idx, wts)
     if dev.index != _current_device():
         with torch.cuda.device(dev):

@@ -184,6 +184,21 @@ def test_pieces_of_rows(G, dtype, N, d):
     assert (alone[1] - got[1][tail]).abs().max() < 1e-4
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_many_rows_of_few_classes(G, monkeypatch, dtype):
+    """Thousands of tiles, each with sums of the bias's gradient."""
+    monkeypatch.setattr(oracle, "ON", "cuda")
+    N, d, V, t = 70001, 16, 130, TYPES[dtype]
+    X, W, b, idx, wts, _ = inputs(N, d, V, 2, t, True, True, seed=1)
+    dloss = torch.full((N,), 1 / N, device="cuda")
+    want, bounds = reference(X, W, b, idx, wts, dloss)
+    got = G.cross_entropy_gradients(X, W, idx, dloss=dloss, wts=wts, bias=b)
+    for a, w, bd, what in zip(got, want, bounds, NAMES):
+        compare(a, w, bd, what)
+        # errors of either sign add up as their root: of a sum of 70001 terms, and two roundings
+        assert (a.double() - w).norm() <= (1e-5 if t == torch.float32 else 2 * oracle.EPS[t] / 2) * w.norm(), what
+
+
 def test_gradients_against_differences(G):
     X, W, b, idx, wts, dloss = inputs(9, 12, 31, 2, torch.float32, True, True, seed=11)
     _, _, *grads = G.cross_entropy_gradients(X, W, idx, dloss=dloss, wts=wts, bias=b)
@@ -328,6 +343,8 @@ def test_graph(G, dtype):
     for t in (X, W, b):
         t.requires_grad_()
     loss, lse = G.cross_entropy(X, W, idx, wts=wts, bias=b)
+    ws = G.cross_entropy_workspace(70, 45, 333, TYPES[dtype], "cuda")
+    assert torch.equal(G.cross_entropy(X, W, idx, wts=wts, bias=b, ws=ws)[0], loss)
     assert loss.requires_grad and not lse.requires_grad
     for a, w in zip(torch.autograd.grad(loss, (X, W, b), dloss), want[2:]):
         assert torch.equal(a, w)

@@ -169,7 +169,7 @@ def test_what_is_not_finite_stays_in_its_row(G):
         assert Y[1].isnan().all() and Y[4].isnan().any() and dbeta.isfinite().all()
 
 
-@pytest.mark.parametrize("D", [5, 77, 1023, 4099])
+@pytest.mark.parametrize("D", [5, 77, 1023, 4099, 16383, 20001, 65535])
 def test_rows_from_any_element_and_in_place(G, D):
     """Views that start off every 16-byte border, outputs over their inputs, and nothing written beside them."""
     t = torch.float16
