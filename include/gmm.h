@@ -1,7 +1,9 @@
 /*
  * gmm.h — C-ABI of libgmm_mi355x.so: the fused Gaussian-mixture EM E-step for
- * MI355X (gfx950), with its M-step, EM loop and top-2 assignment, and the
- * learned products around it: a linear layer and a layer of experts.
+ * MI355X (gfx950), with its M-step, EM loop and top-2 assignment, the learned
+ * products around it (a linear layer and a layer of experts), and what a
+ * training step around it takes (a layer norm, the cross entropy of a linear
+ * head, and AdamW).
  *
  * The operation (pages: "Turbo-GMM: FlashAttention-Inspired GPU-Accelerated
  * Gaussian Mixture Model", abstract; "Flash-GMM: a memory-efficient kernel for
@@ -467,8 +469,11 @@ int gmm_cross_entropy(const void* X, int32_t x_dtype, int64_t N, int32_t d_in, c
  *   dX = G W,  dW = G^T X,  db = sum_n G_n
  * dX (N x d_in), dW (V x d_in) and db (V) have type x_dtype; each is nullable, as
  * lse is. A row of no picks, or whose dloss is 0, has no part in the gradients,
- * whatever its X holds. The logits and G pass through the workspace in pieces of
- * rows, of at most 2 GiB of logits (256 rows at least). The products take G rounded to
+ * whatever its X holds. G and, where the features are many, the logits pass through
+ * the workspace in pieces of rows, of at most 2^29 logits (256 rows at least). lse
+ * and loss come from the float logits; for G of 2-byte operands a logit may have been
+ * kept in half, as its difference from the largest z of its row and of the 32 or 64
+ * columns around it, so that a p is off by 2^-11 of that difference. The products take G rounded to
  * x_dtype, as the matrix instructions do, and accumulate in float; 2-byte operands
  * take it scaled so that the largest |dloss_n| sum_j |w_nj| becomes 2^14, which is
  * taken back from the sums, so that half keeps its 11 bits down to 2^-28 of

@@ -23,10 +23,11 @@ struct EntropyArgs {
   int64_t rows;
   int d_in, V;
   float *loss, *lse;     // [rows], lse nullable
-  const float* stats;    // [rows][groups][2] of a kRowStats product, or null: from the logits
-  int groups;
+  const float* stats;    // [rows][groups][2] of the logits' product, or null: from the logits
+  int groups, columns;   // of a group
   const float* Z;        // [rows][ldz] logits, or null: the picks' are computed from X and W
-  void* G;               // [rows][ldz] their gradient in the operands' type
+  void* G;               // [rows][ldz] their gradient in the operands' type; in its place
+                         // before, where Z is null, the logits' differences from their group's largest in half
   int64_t ldz;           // a multiple of 8
   RowCoef* coef;         // [rows], or null: no gradient
   float* range;          // [kEntropyRange] and G's scale's inverse behind; null: no scale
@@ -58,7 +59,7 @@ hipError_t launch_entropy_prep(const EntropyPrep& p, hipStream_t s);
 // Loss, lse and coef of every row.
 template <typename T>
 hipError_t launch_entropy_loss(const EntropyArgs& p, hipStream_t s);
-// G and its column sums from Z and coef.
+// G and its column sums from Z, or the differences, and coef.
 template <typename T>
 hipError_t launch_entropy_gradient(const EntropyArgs& p, hipStream_t s);
 

@@ -4,6 +4,7 @@
 #pragma once
 
 #include <cfloat>
+#include <type_traits>
 
 #include "gmm_entropy.hpp"
 #include "gmm_product.hpp"
@@ -214,9 +215,12 @@ __global__ void __launch_bounds__(THREADS > 256 ? THREADS : 256) entropy_loss_ke
 // The logits' gradient and its column sums (of the rounded values, in float,
 // without the scale). A wave takes a row's columns of its block, 16 bytes of G a
 // lane, so what belongs to the row is scalar; a block takes a chunk of rows.
-// HBM bounds it.
+// HBM bounds it. GROUPED: 2-byte operands' logits lie in G's place as differences
+// from the largest z of their row and group of columns, in half: a probability is
+// off by 2^-11 of its distance to that, so the large ones least (8192 x 65536:
+// 401 us, against 600 from floats, which the product took 240 us more to write).
 // ---------------------------------------------------------------------------
-template <typename T>
+template <typename T, bool GROUPED>
 __global__ void __launch_bounds__(256) entropy_gradient_kernel(const EntropyArgs p, int across) {
   constexpr int V = Frag<T>::kPer, kAhead = 4;  // rows of logits in flight
   __shared__ float red[4][64 * V];
@@ -229,20 +233,35 @@ __global__ void __launch_bounds__(256) entropy_gradient_kernel(const EntropyArgs
 #pragma unroll
   for (int i = 0; i < V; ++i) sum[i] = 0.f;
   for (int64_t r = r0; r < r1; r += 4 * kAhead) {
-    float z[kAhead][V];
+    using E = std::conditional_t<GROUPED, _Float16, float>;
+    struct {
+      E e[V];
+    } raw[kAhead];
+    float most[kAhead], z[V];
     RowCoef c[kAhead];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u)
       if (r + 4 * u < r1) {
-        c[u] = p.coef[r + 4 * u];
-        if (mine) load_as<float, V>(p.Z + (r + 4 * u) * p.ldz + col, V, z[u]);
+        const int64_t row = r + 4 * u;
+        c[u] = p.coef[row];
+        if (mine) {
+          const E* from = GROUPED ? static_cast<const E*>(p.G) : reinterpret_cast<const E*>(p.Z);
+          __builtin_memcpy(raw[u].e, from + row * p.ldz + col, sizeof(raw[u].e));
+          if (GROUPED) most[u] = p.stats[2 * (row * p.groups + min(col, p.V - 1) / p.columns)];
+        }
       }
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const int64_t row = r + 4 * u;
       if (row >= r1) break;
       float g[V];
-      logit_gradient<V>(c[u], p.picks, row, col, p.V, z[u], g);
+#pragma unroll
+      for (int i = 0; i < V; ++i) z[i] = (float)raw[u].e[i];
+      if (GROUPED) {  // exp(z + most - base), most -infinity where all of the group are
+        c[u].up = most[u] == -__builtin_inff() ? 0.f : c[u].up * exp_of(most[u] - c[u].base);
+        c[u].base = 0.f;
+      }
+      logit_gradient<V>(c[u], p.picks, row, col, p.V, z, g);
       if (mine) {
         store_as<T, V>(static_cast<T*>(p.G) + row * p.ldz + col, V, g);
         if (p.parts)
@@ -287,7 +306,14 @@ template <typename T>
 hipError_t launch_entropy_gradient(const EntropyArgs& p, hipStream_t s) {
   const int across = (int)((p.ldz + 64 * Frag<T>::kPer - 1) / (64 * Frag<T>::kPer));
   const int64_t chunks = (p.rows + p.chunk - 1) / p.chunk;
-  entropy_gradient_kernel<T><<<(unsigned)(across * chunks), 256, 0, s>>>(p, across);
+  const unsigned grid = (unsigned)(across * chunks);
+  if constexpr (sizeof(T) == 2) {
+    if (!p.Z) {
+      entropy_gradient_kernel<T, true><<<grid, 256, 0, s>>>(p, across);
+      return hipGetLastError();
+    }
+  }
+  entropy_gradient_kernel<T, false><<<grid, 256, 0, s>>>(p, across);
   return hipGetLastError();
 }
 

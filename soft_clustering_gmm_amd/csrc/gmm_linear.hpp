@@ -77,13 +77,15 @@ enum { kTile256 = 0, kTile128 = 1, kTile64 = 2, kTileVariants = 3 };
 constexpr int kTileRows[kTileVariants] = {256, 128, 64};
 constexpr int kStepBytes = 128;  // bytes of k per step and operand row
 // In the place of an activation: statistics of the rows instead of C, or beside
-// it; the gradient of a cross entropy whose logits z are.
+// it (of 2-byte operands C is then z - the largest z of its row and group, in
+// half); the gradient of a cross entropy whose logits z are.
 constexpr int kRowStats = 6, kStatsToo = 7, kLogitGradient = 8;
 
 
 // Groups of columns whose statistics such a product of N columns writes:
 // those of a wave, 4 in a tile, or 2 where its waves are 2 x 2.
 constexpr int stat_waves(int variant, int elem) { return variant == kTile256 || (variant == kTile128 && elem == 4) ? 4 : 2; }
+constexpr int stat_columns(int variant, int elem) { return kTileRows[variant] / stat_waves(variant, elem); }
 inline int stat_groups(int variant, int elem, int64_t N) {
   return (int)((N + kTileRows[variant] - 1) / kTileRows[variant]) * stat_waves(variant, elem);
 }

@@ -48,8 +48,9 @@ static int64_t piece_rows(int64_t N, int64_t bytes, int64_t most) {
   return std::min(N, std::min<int64_t>(rows, 1 << 20));
 }
 constexpr int64_t kStatPiece = 256ll << 20;   // bytes of a piece's statistics
-// Bytes of a piece's logits: dW is read and written once for each (8192 x 2048
-// to 65536 classes: 6062 us in one piece, 6884 in four, 8009 in eight).
+// Bytes of a piece's logits, were they float: dW is read and written once for
+// each (8192 x 2048 to 65536 classes: 6062 us in one piece, 6884 in four, 8009 in
+// eight).
 constexpr int64_t kLogitPiece = 2048ll << 20;
 
 // Workspace of the loss: [padded rows of X of a piece] [padded W] [statistics].
@@ -90,11 +91,11 @@ static EntropyPlan entropy_plan(int64_t N, int d_in, int V, int e) {
 // Up to so many features, and where the logits are more than the caches keep at
 // hand, they are computed twice, once for the loss and once for their gradient,
 // and not written to memory (8192 rows to 32768 classes in bfloat16, against
-// once: 64 features 674 us and 1159, 512 1231 and 1425, 1024 2043 and 2007; to
-// 8192 in float: 64 features 416 and 469, 128 646 and 637; 4096 rows to 4096
-// classes in bfloat16, 64 MiB: 64 features 72 and 82, 512 147 and 146; 1000 rows
-// to 8000, 32 MiB: 512 features 92 and 89; 8192 to 1024 in float: 91 and 84).
-constexpr int kTwice = 896, kTwiceF32 = 96;
+// once: 64 features 731 us and 815, 256 922 and 931, 512 1206 and 1142; to 8192 in
+// float: 64 features 416 and 469, 128 646 and 637; 4096 rows to 4096 classes in
+// bfloat16, 64 MiB of float: 64 features 72 and 80; 1000 rows to 8000, 32 MiB: 512
+// features 90 and 88; 8192 to 1024 in float: 91 and 84).
+constexpr int kTwice = 256, kTwiceF32 = 96;
 constexpr int64_t kTwiceBytes = 32ll << 20;
 
 // Workspace of the gradients, for a piece of rows: [padded X] [X without the
@@ -109,6 +110,10 @@ struct EntropyBackPlan {
 
   // Tiles of the logits' product: whole sums where it is not written.
   Cut logits(int64_t rows, int V, int d_in, int e) const { return choose_cut(rows, V, d_in, e, twice ? 1 : 256); }
+  // Whether they are kept as half differences from their group's largest, in the place of their gradient.
+  bool shifted(int64_t rows, int V, int d_in, int e) const {
+    return !few && !twice && e == 2 && logits(rows, V, d_in, e).splits == 1;
+  }
   // Sums of a column that a piece's gradient leaves, and what is kept of them: those of many tiles are added up first.
   int64_t tile_sums(int64_t rows, int V, int d_in, int e) const {
     return twice ? 2 * ceil_div(rows, kTileRows[logits(rows, V, d_in, e).variant]) : ceil_div(rows, chunk);
@@ -129,7 +134,7 @@ static EntropyBackPlan entropy_back_plan(int64_t N, int d_in, int V, int e) {
   l.piece = piece_rows(N, l.ldz * (int64_t)sizeof(float), kLogitPiece);
   l.twice = !l.few && d_in <= (e == 2 ? kTwice : kTwiceF32) && l.piece * l.ldz * (int64_t)sizeof(float) > kTwiceBytes;
   // Rows of a block that has columns of G: 16 at least (of 1001 rows and 7777 classes in half 64 make a block a CU, 17.9
-  // us, and 16 CHUNK16), more while 2048 blocks are left, and no more than 1024 column sums of a column.
+  // us, and 16 take 10.4), more while 2048 blocks are left, and no more than 1024 column sums of a column.
   const int64_t across = ceil_div(l.ldz, 64 * (16 / e));
   l.chunk = std::max<int64_t>(16, std::min<int64_t>(64, l.piece * across / 2048 / 16 * 16));
   l.chunk = std::min(l.piece, std::max(l.chunk, ceil_div(ceil_div(N, 1024), 16) * 16));
@@ -140,8 +145,12 @@ static EntropyBackPlan entropy_back_plan(int64_t N, int d_in, int V, int e) {
     off = align_up(off + bytes, 256);
     return o;
   };
+  size_t z = 0, g = 0;
   for (int64_t rows : {l.piece, N % l.piece})
     if (rows) {
+      const bool shifted = l.shifted(rows, V, d_in, e);
+      if (!l.twice && !shifted) z = std::max(z, (size_t)rows * l.ldz * sizeof(float));
+      g = std::max(g, (size_t)rows * l.ldz * e);
       if (!l.few) {
         const Cut c = l.logits(rows, V, d_in, e);
         part = std::max(part, partial_bytes(c, rows, V));
@@ -154,8 +163,8 @@ static EntropyBackPlan entropy_back_plan(int64_t N, int d_in, int V, int e) {
   l.o_x = take(l.pad && !l.few ? (size_t)l.piece * l.lx * e : 0);
   l.o_clean = take((size_t)l.piece * l.lx * e);
   l.o_w = take(l.pad ? (size_t)V * l.lx * e : 0);
-  l.o_z = take(l.twice ? 0 : (size_t)l.piece * l.ldz * sizeof(float));
-  l.o_g = take((size_t)l.piece * l.ldz * e);
+  l.o_z = take(z);
+  l.o_g = take(g);
   l.o_stats = take(stats);
   l.o_coef = take((size_t)l.piece * sizeof(RowCoef));
   l.o_acc = take(l.piece < N && e == 2 ? (size_t)V * d_in * sizeof(float) : 0);
@@ -266,13 +275,17 @@ static hipError_t entropy_gradients(EntropyArgs a, int64_t N, T* dX, T* dW, T* d
       p.B = W, p.lda = p.ldb = l.lx;
       p.M = rows, p.N = a.V, p.K = a.d_in;
       p.bias = a.bias;
-      p.C = const_cast<float*>(a.Z), p.ldc = l.ldz, p.c_f32 = 1;
       const Cut c = l.logits(rows, a.V, a.d_in, sizeof(T));
       if (c.splits == 1) {  // whole sums: the tiles' statistics with them
         a.stats = p.stats = reinterpret_cast<float*>(ws + l.o_stats);
         a.groups = stat_groups(c.variant, sizeof(T), a.V);
+        a.columns = stat_columns(c.variant, sizeof(T));
       }
-      a.Z = l.twice ? nullptr : reinterpret_cast<float*>(ws + l.o_z);
+      const bool shifted = l.shifted(rows, a.V, a.d_in, sizeof(T));
+      a.Z = l.twice || shifted ? nullptr : reinterpret_cast<float*>(ws + l.o_z);
+      p.C = shifted ? a.G : const_cast<float*>(a.Z);
+      p.ldc = l.ldz;
+      p.c_f32 = !shifted;
       e = run_product<T>(c, false, false, l.twice ? kRowStats : a.stats ? kStatsToo : (int)GMM_ACT_NONE, p, s, false);
       if (e == hipSuccess && l.twice) e = launch_entropy_loss<T>(a, s);
       if (e == hipSuccess && l.twice && (dX || dW || db)) {  // again, for their gradient

@@ -72,6 +72,8 @@ def reference(X, W, bias, idx, wts, dloss):
     grad = d[:, None] * s[:, None] * p
     # p is off by its logit's error and the sum's, and the roundings of the exponential and of three products
     gb = grad.abs() * (zb + lb[:, None] + 2 * U * far + 16 * U)
+    if X.dtype != torch.float32:  # a difference from a largest logit around it in half: half a step, 2^-11 of it
+        gb += grad.abs() * (2.0 ** -11 * far + 2.0 ** -25)
     gb += (d * c.abs().sum(1))[:, None].abs() * p * 10 * U  # s may cancel
     grad.scatter_add_(1, i, -d[:, None] * c)
     pick = torch.zeros_like(grad).scatter_add_(1, i, (d[:, None] * c).abs())
@@ -128,7 +130,7 @@ def test_against_64_bits(G, monkeypatch, i, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("N,d,V", [(4090, 520, 8190), (8200, 1000, 2050), (2040, 136, 33001), (4090, 72, 4101)])
+@pytest.mark.parametrize("N,d,V", [(4090, 520, 8190), (4090, 200, 8190), (8200, 1000, 2050), (2040, 136, 33001), (4090, 72, 4101)])
 def test_large_tiles(G, monkeypatch, N, d, V, dtype):
     monkeypatch.setattr(oracle, "ON", "cuda")
     t = TYPES[dtype]
