@@ -457,8 +457,9 @@ size_t gmm_layer_norm_workspace_bytes(int64_t N, int32_t D, int32_t x_dtype);
  * Products and sums are float. A bias of -infinity takes a class out. A logit that is NaN or
  * +infinity, or only -infinity, make the row's lse and loss NaN (lse -infinity in
  * the last case).
- * 1 <= V <= 2^20, N <= 2^30; alignment of X and W as in gmm_linear. The workspace
- * must hold gmm_cross_entropy_workspace_bytes(N, d_in, V, x_dtype, 0) bytes. */
+ * 1 <= V <= 2^20, N <= 2^30; alignment of X and W as in gmm_linear. No output may
+ * overlap an input. The workspace must hold
+ * gmm_cross_entropy_workspace_bytes(N, d_in, V, x_dtype, 0) bytes. */
 int gmm_cross_entropy(const void* X, int32_t x_dtype, int64_t N, int32_t d_in, const void* W, int32_t V,
                       const void* bias, const int32_t* idx, const float* wts, int32_t top, float* loss, float* lse,
                       void* workspace, size_t ws_bytes, void* stream);

@@ -134,10 +134,11 @@ static EntropyBackPlan entropy_back_plan(int64_t N, int d_in, int V, int e) {
   l.piece = piece_rows(N, l.ldz * (int64_t)sizeof(float), kLogitPiece);
   l.twice = !l.few && d_in <= (e == 2 ? kTwice : kTwiceF32) && l.piece * l.ldz * (int64_t)sizeof(float) > kTwiceBytes;
   // Rows of a block that has columns of G: 16 at least (of 1001 rows and 7777 classes in half 64 make a block a CU, 17.9
-  // us, and 16 take 10.4), more while 2048 blocks are left, and no more than 1024 column sums of a column.
+  // us, and 16 take 10.4), more while 2048 blocks are left, then as many as leave 1024 sums of a column, 8192 at most.
   const int64_t across = ceil_div(l.ldz, 64 * (16 / e));
   l.chunk = std::max<int64_t>(16, std::min<int64_t>(64, l.piece * across / 2048 / 16 * 16));
-  l.chunk = std::min(l.piece, std::max(l.chunk, ceil_div(ceil_div(N, 1024), 16) * 16));
+  l.chunk = std::max(l.chunk, std::min<int64_t>(8192, ceil_div(ceil_div(N, 1024), 16) * 16));
+  l.chunk = std::min(l.piece, l.chunk);
   l.chunks = l.sums(l.piece, V, d_in, e) * (N / l.piece) + (N % l.piece ? l.sums(N % l.piece, V, d_in, e) : 0);
   size_t off = 0, part = 0, stats = 0, fold = 0;
   auto take = [&](size_t bytes) {
