@@ -22,17 +22,32 @@ __device__ __forceinline__ LogSum join(LogSum a, LogSum b) {
   return {m, (a.m == -kInf ? a.s : a.s * exp_of(a.m - m)) + (b.m == -kInf ? b.s : b.s * exp_of(b.m - m))};
 }
 
+// |dloss| sum |w| of a row, which bounds its gradient; 0 where it has none, and
+// what is not finite counts as none for the scale.
+__device__ __forceinline__ float row_weight(const RowPicks& picks, const float* dloss, int64_t row, int V) {
+  float sum = 0.f;
+  for (int j = 0; j < picks.top; ++j) sum += fabsf(pick_of(picks, row, j, V).w);
+  return sum * fabsf(dloss ? dloss[row] : 1.f);
+}
+__device__ __forceinline__ bool has_gradient(const RowPicks& picks, const float* dloss, int64_t row, int V) {
+  bool on = false;
+  if (!dloss || dloss[row] != 0.f)
+    for (int j = 0; j < picks.top; ++j) on |= pick_of(picks, row, j, V).w != 0.f;
+  return on;
+}
+
 // ---------------------------------------------------------------------------
 // Work before the products. A row has no gradient where its picks weigh nothing
 // or its loss is not asked for; what is not finite in such a row of X would
 // reach dW as 0 times it, so dW's product takes a copy with zeros there.
 // One launch: of 1001 rows the copies, the clean rows and the range took 4 to 6
-// us each in launches of their own.
+// us each in launches of their own. Of up to kOwnPrepRows rows that need no
+// padded copies the loss kernel does the same beside its work.
 // ---------------------------------------------------------------------------
-template <typename T>
-__device__ __forceinline__ void copy_row(const T* from, T* to, int n, int64_t ld, int lane) {
+template <typename T, int THREADS = 64>
+__device__ __forceinline__ void copy_row(const T* from, T* to, int n, int64_t ld, int t) {
   constexpr int V = Frag<T>::kPer;
-  for (int64_t c = lane * V; c < ld; c += 64 * V) *reinterpret_cast<u32x4*>(to + c) = load_frag<T>(from + c, (int)(n - c));
+  for (int64_t c = t * V; c < ld; c += THREADS * V) *reinterpret_cast<u32x4*>(to + c) = load_frag<T>(from + c, (int)(n - c));
 }
 
 template <typename T>
@@ -44,9 +59,7 @@ __global__ void __launch_bounds__(256) entropy_prep_kernel(const EntropyPrep p) 
       __shared__ float red[4];
       float most = 0.f;
       for (int64_t row = block * 256ll + threadIdx.x; row < p.all_rows; row += kEntropyRange * 256ll) {
-        float sum = 0.f;
-        for (int j = 0; j < p.picks.top; ++j) sum += fabsf(pick_of(p.picks, row, j, p.V).w);
-        const float a = sum * fabsf(p.dloss ? p.dloss[row] : 1.f);
+        const float a = row_weight(p.picks, p.dloss, row, p.V);
         if (a <= FLT_MAX) most = fmaxf(most, a);
       }
 #pragma unroll
@@ -69,10 +82,7 @@ __global__ void __launch_bounds__(256) entropy_prep_kernel(const EntropyPrep p) 
     const T* x = static_cast<const T*>(p.X) + i * p.d_in;
     if (p.x) copy_row<T>(x, static_cast<T*>(p.x) + i * p.ld, p.d_in, p.ld, lane);
     if (p.clean) {
-      const int64_t row = p.first + i;
-      bool on = false;
-      if (!p.dloss || p.dloss[row] != 0.f)
-        for (int j = 0; j < p.picks.top; ++j) on |= pick_of(p.picks, row, j, p.V).w != 0.f;
+      const bool on = has_gradient(p.picks, p.dloss, p.first + i, p.V);
       copy_row<T>(x, static_cast<T*>(p.clean) + i * p.ld, on ? p.d_in : 0, p.ld, lane);
     }
   }
@@ -87,8 +97,15 @@ __global__ void __launch_bounds__(256) entropy_prep_kernel(const EntropyPrep p) 
 // every thread of a wave.
 __device__ __forceinline__ float gradient_scale(const EntropyArgs& p) {
   float most = 0.f;
+  if (p.own_range) {
+    for (int64_t row = threadIdx.x & 63; row < p.rows; row += 64) {
+      const float a = row_weight(p.picks, p.dloss, row, p.V);
+      if (a <= FLT_MAX) most = fmaxf(most, a);
+    }
+  } else {
 #pragma unroll
-  for (int i = 0; i < kEntropyRange / 64; ++i) most = fmaxf(most, p.range[i * 64 + (threadIdx.x & 63)]);
+    for (int i = 0; i < kEntropyRange / 64; ++i) most = fmaxf(most, p.range[i * 64 + (threadIdx.x & 63)]);
+  }
 #pragma unroll
   for (int o = 32; o; o >>= 1) most = fmaxf(most, __shfl_xor(most, o));
   most = most > 0.f ? fmaxf(most, 1e-30f) : 16384.f;  // the scale and its inverse are normal
@@ -114,6 +131,9 @@ __global__ void __launch_bounds__(THREADS > 256 ? THREADS : 256) entropy_loss_ke
   const float scale = p.coef && p.range ? gradient_scale(p) : 1.f;
   const int64_t row = blockIdx.x * (int64_t)kRows + threadIdx.x / THREADS;
   if (row >= p.rows) return;  // whole waves, and only where a row is one wave's
+  if (p.clean)
+    copy_row<T, THREADS>(static_cast<const T*>(p.X) + row * p.d_in, static_cast<T*>(p.clean) + row * p.ldx,
+                         has_gradient(p.picks, p.dloss, row, p.V) ? p.d_in : 0, p.ldx, t);
   const float* z = p.Z ? p.Z + row * p.ldz : nullptr;
   LogSum sum{-kInf, 0.f};
   if (p.stats) {

@@ -254,6 +254,11 @@ static hipError_t entropy_gradients(EntropyArgs a, int64_t N, T* dX, T* dW, T* d
     a.dloss = row_at(all.dloss, r, 1);
     a.loss = row_at(all.loss, r, 1);
     a.lse = row_at(all.lse, r, 1);
+    // few rows in their place: the loss kernel does the rest
+    const bool alone = N <= kOwnPrepRows && !pad_x && !pad_w;
+    a.own_range = alone;
+    a.clean = alone && dW ? ws + l.o_clean : nullptr;
+    a.ldx = l.lx;
     EntropyPrep b{};
     b.X = a.X, b.ld = l.lx, b.d_in = a.d_in, b.V = a.V;
     b.x = pad_x ? ws + l.o_x : nullptr;
@@ -262,7 +267,7 @@ static hipError_t entropy_gradients(EntropyArgs a, int64_t N, T* dX, T* dW, T* d
     b.W = a.W, b.w = pad_w && r == 0 ? ws + l.o_w : nullptr;
     b.all_rows = scaled && r == 0 ? N : 0;
     b.picks = all.picks, b.dloss = all.dloss, b.first = r, b.range = a.range;
-    if ((e = launch_entropy_prep<T>(b, s)) != hipSuccess) return e;
+    if (!alone && (e = launch_entropy_prep<T>(b, s)) != hipSuccess) return e;
     ProductArgs p{};
     p.partial = reinterpret_cast<float*>(ws + l.o_part);
     // the logits, through the caches, which the next kernel finds them in (2048 x 1024 to 32768 classes: 580 us against
