@@ -476,8 +476,8 @@ int gmm_cross_entropy(const void* X, int32_t x_dtype, int64_t N, int32_t d_in, c
  * kept in half, as its difference from the largest z of its row and of the 32 or 64
  * columns around it, so that a p is off by 2^-11 of that difference. The products take G rounded to
  * x_dtype, as the matrix instructions do, and accumulate in float; 2-byte operands
- * take it scaled so that the largest |dloss_n| sum_j |w_nj| becomes 2^14, which is
- * taken back from the sums, so that half keeps its 11 bits down to 2^-28 of
+ * take it scaled so that the largest |dloss_n w_nj| becomes 2^11, which is
+ * taken back from the sums, so that half keeps its 11 bits down to 2^-25 of
  * that whatever its size. db sums the rounded G. Sums run in a fixed order. N = 0
  * gives dW = 0 and db = 0. The workspace must hold
  * gmm_cross_entropy_workspace_bytes(N, d_in, V, x_dtype, 1) bytes. */

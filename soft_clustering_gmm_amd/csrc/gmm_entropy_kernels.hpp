@@ -22,12 +22,11 @@ __device__ __forceinline__ LogSum join(LogSum a, LogSum b) {
   return {m, (a.m == -kInf ? a.s : a.s * exp_of(a.m - m)) + (b.m == -kInf ? b.s : b.s * exp_of(b.m - m))};
 }
 
-// |dloss| sum |w| of a row, which bounds its gradient; 0 where it has none, and
-// what is not finite counts as none for the scale.
+// The largest |dloss w| of a row's picks.
 __device__ __forceinline__ float row_weight(const RowPicks& picks, const float* dloss, int64_t row, int V) {
-  float sum = 0.f;
-  for (int j = 0; j < picks.top; ++j) sum += fabsf(pick_of(picks, row, j, V).w);
-  return sum * fabsf(dloss ? dloss[row] : 1.f);
+  float most = 0.f;
+  for (int j = 0; j < picks.top; ++j) most = fmaxf(most, fabsf(pick_of(picks, row, j, V).w));
+  return most * fabsf(dloss ? dloss[row] : 1.f);
 }
 __device__ __forceinline__ bool has_gradient(const RowPicks& picks, const float* dloss, int64_t row, int V) {
   bool on = false;
@@ -54,7 +53,7 @@ template <typename T>
 __global__ void __launch_bounds__(256) entropy_prep_kernel(const EntropyPrep p) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int block = blockIdx.x, blocks = gridDim.x;
-  if (p.all_rows) {  // the largest finite |dloss| sum |w|, in parts
+  if (p.all_rows) {  // the largest finite |dloss w|, in parts
     if (block < kEntropyRange) {
       __shared__ float red[4];
       float most = 0.f;
@@ -88,13 +87,13 @@ __global__ void __launch_bounds__(256) entropy_prep_kernel(const EntropyPrep p) 
   }
 }
 
-// The scale of G: the largest |dloss| sum |w| becomes 2^14 (no entry passes
-// twice that), and the products take it back. So half's range is kept, and
-// where all rows weigh the same, as under a mean, the picks' entries
-// dloss (p - 1) lie next to 2^14, not next to a number whose rounding all rows
-// share: in bfloat16 the gradients of 8192 rows were off by 0.0029 without (1 /
-// 7373 is 0.0024 from its neighbour), and are by 0.0017, their own rounding. In
-// every thread of a wave.
+// The scale of G: the largest |dloss w| becomes 2^11 (no entry passes 16 times
+// that, 8 picks and the probability's share of as many), and the products take it
+// back. So half's range is kept, and where all picks weigh the same, as under a
+// mean over labelled rows, their entries dloss (p - 1) lie next to 2^11, not next
+// to a number whose rounding all rows share: in bfloat16 the gradients of 8192
+// rows were off by 0.0029 without (1 / 7373 is 0.0024 from its neighbour), and are
+// by 0.0017, their own rounding. In every thread of a wave.
 __device__ __forceinline__ float gradient_scale(const EntropyArgs& p) {
   float most = 0.f;
   if (p.own_range) {
@@ -108,9 +107,9 @@ __device__ __forceinline__ float gradient_scale(const EntropyArgs& p) {
   }
 #pragma unroll
   for (int o = 32; o; o >>= 1) most = fmaxf(most, __shfl_xor(most, o));
-  most = most > 0.f ? fmaxf(most, 1e-30f) : 16384.f;  // the scale and its inverse are normal
-  if (blockIdx.x == 0 && threadIdx.x == 0) p.range[kEntropyRange] = most * (1.f / 16384.f);
-  return 16384.f / most;
+  most = most > 0.f ? fmaxf(most, 1e-30f) : 2048.f;  // the scale and its inverse are normal
+  if (blockIdx.x == 0 && threadIdx.x == 0) p.range[kEntropyRange] = most * (1.f / 2048.f);
+  return 2048.f / most;
 }
 
 // ---------------------------------------------------------------------------

@@ -209,6 +209,26 @@ def test_large_states(G):
             assert torch.equal(one[name][:k], state[name][o:o + k])
 
 
+def test_elements_past_32_bits(G):
+    """A tensor of more than 2^31 elements, behind another one: its ends are those of calls of their own."""
+    n = (1 << 31) + 777
+    p = [torch.ones(300, dtype=torch.bfloat16, device="cuda"), torch.empty(n, dtype=torch.bfloat16, device="cuda")]
+    ramp = torch.arange(1 << 20, device="cuda", dtype=torch.float32).sub_(1 << 19).div_(1 << 19).bfloat16()
+    for o in range(0, n, 1 << 20):
+        p[1][o:o + (1 << 20)] = ramp[:n - o]
+    g = [t.clone() for t in p]
+    ends = [(0, 5000), ((1 << 30) + 256, 4096), ((1 << 31) - 512, 1289)]
+    start = [p[1][o:o + k].clone() for o, k in ends]
+    state = G.adamw_state(p)
+    G.adamw_step(p, g, **state, **HYPER)
+    for (o, k), q in zip(ends, start):
+        one = G.adamw_state([q])
+        G.adamw_step([q], [g[1][o:o + k]], **one, **HYPER)
+        assert torch.equal(q, p[1][o:o + k])
+        for name in ("m", "v"):
+            assert torch.equal(one[name][:k], state[name][512 + o:512 + o + k])
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 @pytest.mark.parametrize("count", [96, 97, 250])
 def test_many_tensors(G, count, bits):

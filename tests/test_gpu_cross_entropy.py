@@ -78,9 +78,9 @@ def reference(X, W, bias, idx, wts, dloss):
     grad.scatter_add_(1, i, -d[:, None] * c)
     pick = torch.zeros_like(grad).scatter_add_(1, i, (d[:, None] * c).abs())
     gb += 10 * U * pick
-    if X.dtype != torch.float32:  # rounded to the operands' type, of which the scale makes the largest weight 2^14
-        largest = float((d.abs() * c.abs().sum(1)).max()) if N else 0.0
-        gb += (grad.abs() + gb) * (oracle.EPS[X.dtype] / 2 + 4 * U) + oracle.TINY[X.dtype] * max(largest, 1e-30) / 16384
+    if X.dtype != torch.float32:  # rounded to the operands' type, of which the scale makes the largest pick 2^11
+        largest = float((d.abs() * c.abs().amax(1)).max()) if N else 0.0
+        gb += (grad.abs() + gb) * (oracle.EPS[X.dtype] / 2 + 4 * U) + oracle.TINY[X.dtype] * max(largest, 1e-30) / 2048
     dx, dw, db = grad @ w, grad.T @ x, grad.sum(0)
     size = grad.abs() + gb
     dxb = gb @ w.abs() + oracle.sum_bound(size, w.T, V) + 2 * U * dx.abs()
@@ -290,6 +290,28 @@ def test_extreme_logits(G):
     assert ((loss - 200 - torch.tensor(299.0).log()).abs() < 1e-4).all()
     off, _ = G.cross_entropy(X * 1e30, W, (idx + 1) % 20)
     assert (off > 1e31).all() and off.isfinite().all()
+
+
+@pytest.mark.parametrize("N", [5, 700])
+@pytest.mark.parametrize("top", [1, 3, 7])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_weights_that_all_rows_share(G, dtype, top, N):
+    """Under a mean all picks weigh the same: whatever that is, its rounding is no common factor of the gradients."""
+    t = TYPES[dtype]
+    for seed, share in enumerate((1 / N, 1 / 7373, 1 / 3, 0.7)):
+        X, W, _, idx, _, _ = inputs(N, 104, 20000, top, t, False, False, seed=seed)
+        dloss = torch.full((N,), share, device="cuda")
+        (_, _, dx, dw, _), _ = reference(X.cpu(), W.cpu(), None, idx.cpu(), None, dloss.cpu())
+        got = G.cross_entropy_gradients(X, W, idx, dloss=dloss, want_db=False)
+        for a, w in ((got[2], dx), (got[3], dw)):
+            # The outputs' own rounding, and G's: a pick's entry 2^11 (1 - p) is off by half a step below 2^11, u / 2 (u
+            # half a step above), u / 2 / sqrt 3 in the root mean square; the other entries' squares sum to exp(2^2) /
+            # 20000 of a pick's for logits of deviation 2, times 7 picks at most: 0.02 u^2 / 3. Together 0.30 u. 1.1 for
+            # the fluctuation of a norm over 520 entries.
+            u = torch.finfo(t).eps / 2
+            rounded = float((w.to(t).double() - w).norm() / w.norm())
+            off = float((a.cpu().double() - w).norm() / w.norm())
+            assert off <= 1.1 * (rounded ** 2 + (0.31 * u) ** 2) ** 0.5, (seed, share, off, rounded)
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
