@@ -34,7 +34,7 @@ constexpr int kNormKeep = 16;
 inline NormShape norm_shape(int64_t D, int e) {
   const int v = 16 / e;
   const int64_t pieces = (D + v - 1) / v;
-  for (int g : {8, 16})
+  for (int g : {4, 8, 16, 32})
     if (pieces <= g) return {g, 1};
   for (int c = 1; c * v <= kNormKeep; c *= 2)
     if (pieces <= 64 * c) return {64, c};

@@ -368,7 +368,7 @@ void with_norm_shape(NormShape s, int D, F&& f3) {
   using std::integral_constant;
   auto f = [&](auto g, auto c) {
     if (D % V == 0) return f3(g, c, integral_constant<int, kWhole>{});
-    if constexpr (decltype(g)::value == 8)
+    if constexpr (decltype(g)::value == 4)
       if (D < V) return f3(g, c, integral_constant<int, kTiny>{});
     f3(g, c, integral_constant<int, kMoved>{});
   };
@@ -380,8 +380,10 @@ void with_norm_shape(NormShape s, int D, F&& f3) {
     if constexpr (kMost >= 4) f(g, integral_constant<int, 4>{});
   };
   constexpr integral_constant<int, kNormKeep / V> few{};
+  if (s.group == 4) return f(integral_constant<int, 4>{}, integral_constant<int, 1>{});
   if (s.group == 8) return f(integral_constant<int, 8>{}, integral_constant<int, 1>{});
   if (s.group == 16) return f(integral_constant<int, 16>{}, integral_constant<int, 1>{});
+  if (s.group == 32) return f(integral_constant<int, 32>{}, integral_constant<int, 1>{});
   if (s.group == 64) return pieces(integral_constant<int, 64>{}, few);
   if (s.group == 256) return pieces(integral_constant<int, 256>{}, few);
   if (s.group == 512) return f(integral_constant<int, 512>{}, few);

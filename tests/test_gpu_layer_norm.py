@@ -15,7 +15,7 @@ TYPES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
 COMBOS = [("f32", "f32", "f32"), ("f16", "f16", "f16"), ("bf16", "bf16", "f32"), ("f32", "bf16", "f32"),
           ("f32", "f16", "f16"), ("bf16", "bf16", "bf16")]
 # A sum over a row runs over at most 64 elements in a thread, 6 steps over a wave and 16 waves, that over the rows over
-# at most N in a thread, a block's 32 groups, 16 slices of at most 64 parts: 96 and N + 160 additions at most, each off
+# at most N in a thread, a block's 64 groups, 16 slices of at most 64 parts: 96 and N + 160 additions at most, each off
 # by 2^-24 of a partial sum. U is a rounding.
 ROW, COLUMN, U = 96, 160, 2.0 ** -24
 
@@ -74,7 +74,7 @@ def compare(got, want, bound, what):
 
 
 # one element, the pieces of every group of threads, one more and one less, and the widest
-WIDTHS = [1, 2, 7, 8, 9, 31, 33, 64, 65, 96, 129, 255, 256, 512, 513, 777, 1024, 1025, 2048, 2050, 4096, 5000, 8192,
+WIDTHS = [1, 2, 7, 8, 9, 16, 17, 31, 32, 33, 64, 65, 96, 128, 129, 200, 255, 256, 257, 512, 513, 777, 1024, 1025, 2048, 2050, 4096, 5000, 8192,
           8193, 16384, 16390, 30000, 32768, 65535, 65536]
 
 
