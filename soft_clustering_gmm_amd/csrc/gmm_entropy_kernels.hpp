@@ -43,15 +43,15 @@ __device__ __forceinline__ bool has_gradient(const RowPicks& picks, const float*
 // us each in launches of their own. Of up to kOwnPrepRows rows that need no
 // padded copies the loss kernel does the same beside its work.
 // ---------------------------------------------------------------------------
-template <typename T, int THREADS = 64>
+template <typename T, int THREADS>
 __device__ __forceinline__ void copy_row(const T* from, T* to, int n, int64_t ld, int t) {
   constexpr int V = Frag<T>::kPer;
   for (int64_t c = t * V; c < ld; c += THREADS * V) *reinterpret_cast<u32x4*>(to + c) = load_frag<T>(from + c, (int)(n - c));
 }
 
-template <typename T>
+template <typename T, int L>
 __global__ void __launch_bounds__(256) entropy_prep_kernel(const EntropyPrep p) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, t = threadIdx.x % L;
   int block = blockIdx.x, blocks = gridDim.x;
   if (p.all_rows) {  // the largest finite |dloss w|, in parts
     if (block < kEntropyRange) {
@@ -72,17 +72,18 @@ __global__ void __launch_bounds__(256) entropy_prep_kernel(const EntropyPrep p) 
     blocks -= kEntropyRange;
   }
   const int64_t jobs = p.rows + (p.w ? p.V : 0);
-  for (int64_t i = block * 4ll + wave; i < jobs; i += blocks * 4ll) {
+  constexpr int64_t kRows = 256 / L;
+  for (int64_t i = block * kRows + threadIdx.x / L; i < jobs; i += blocks * kRows) {
     if (i >= p.rows) {
       const int64_t r = i - p.rows;
-      copy_row<T>(static_cast<const T*>(p.W) + r * p.d_in, static_cast<T*>(p.w) + r * p.ld, p.d_in, p.ld, lane);
+      copy_row<T, L>(static_cast<const T*>(p.W) + r * p.d_in, static_cast<T*>(p.w) + r * p.ld, p.d_in, p.ld, t);
       continue;
     }
     const T* x = static_cast<const T*>(p.X) + i * p.d_in;
-    if (p.x) copy_row<T>(x, static_cast<T*>(p.x) + i * p.ld, p.d_in, p.ld, lane);
+    if (p.x) copy_row<T, L>(x, static_cast<T*>(p.x) + i * p.ld, p.d_in, p.ld, t);
     if (p.clean) {
       const bool on = has_gradient(p.picks, p.dloss, p.first + i, p.V);
-      copy_row<T>(x, static_cast<T*>(p.clean) + i * p.ld, on ? p.d_in : 0, p.ld, lane);
+      copy_row<T, L>(x, static_cast<T*>(p.clean) + i * p.ld, on ? p.d_in : 0, p.ld, t);
     }
   }
 }
@@ -129,7 +130,7 @@ __global__ void __launch_bounds__(THREADS > 256 ? THREADS : 256) entropy_loss_ke
   const int t = threadIdx.x % THREADS, lane = threadIdx.x & 63;
   const float scale = p.coef && p.range ? gradient_scale(p) : 1.f;
   const int64_t row = blockIdx.x * (int64_t)kRows + threadIdx.x / THREADS;
-  if (row >= p.rows) return;  // whole waves, and only where a row is one wave's
+  if (row >= p.rows) return;  // whole rows, and only where no barrier follows
   if (p.clean)
     copy_row<T, THREADS>(static_cast<const T*>(p.X) + row * p.d_in, static_cast<T*>(p.clean) + row * p.ldx,
                          has_gradient(p.picks, p.dloss, row, p.V) ? p.d_in : 0, p.ldx, t);
@@ -155,8 +156,9 @@ __global__ void __launch_bounds__(THREADS > 256 ? THREADS : 256) entropy_loss_ke
       sum = join(sum, LogSum{m, s});
     }
   }
+  constexpr int kLanes = THREADS < 64 ? THREADS : 64;  // of a row in a wave
 #pragma unroll
-  for (int o = 32; o; o >>= 1) sum = join(sum, LogSum{__shfl_xor(sum.m, o), __shfl_xor(sum.s, o)});
+  for (int o = kLanes / 2; o; o >>= 1) sum = join(sum, LogSum{__shfl_xor(sum.m, o), __shfl_xor(sum.s, o)});
   // this wave's part of x W_j
   auto dot = [&](int v) {
     constexpr int V = Frag<T>::kPer;
@@ -171,7 +173,7 @@ __global__ void __launch_bounds__(THREADS > 256 ? THREADS : 256) entropy_loss_ke
       for (int i = 0; i < V; ++i) of = fmaf(a[i], b[i], of);
     }
 #pragma unroll
-    for (int o = 32; o; o >>= 1) of += __shfl_xor(of, o);
+    for (int o = kLanes / 2; o; o >>= 1) of += __shfl_xor(of, o);
     return of;
   };
   if constexpr (THREADS > 64) {
@@ -187,14 +189,14 @@ __global__ void __launch_bounds__(THREADS > 256 ? THREADS : 256) entropy_loss_ke
     sum = red[0];
     for (int w = 1; w < kWaves; ++w) sum = join(sum, red[w]);
   }
-  // one wave goes on
+  // one wave goes on, or the row's part of one
   const float log_sum = logf(sum.s);
   float loss = 0.f, share = 0.f;
   RowCoef c{};
   c.v0 = c.v1 = -1;
   for (int j = 0; j < p.picks.top; ++j) {
     const Pick k = pick_of(p.picks, row, j, p.V);
-    if (k.w == 0.f) continue;  // the same for the whole wave
+    if (k.w == 0.f) continue;  // the same for the row
     float of = 0.f;
     if (z) {
       of = z[k.v];
@@ -216,7 +218,7 @@ __global__ void __launch_bounds__(THREADS > 256 ? THREADS : 256) entropy_loss_ke
       c.all = 1;
     loss = fmaf(k.w, log_sum + (sum.m - of), loss);
   }
-  if (lane == 0) {
+  if (t == 0) {
     p.loss[row] = loss;
     if (p.lse) p.lse[row] = sum.m == -kInf ? sum.s == 0.f ? -kInf : sum.s : sum.m + log_sum;
     if (p.coef) {
@@ -301,10 +303,16 @@ __global__ void __launch_bounds__(256) entropy_gradient_kernel(const EntropyArgs
 
 template <typename T>
 hipError_t launch_entropy_prep(const EntropyPrep& p, hipStream_t s) {
-  const int64_t jobs = p.rows + (p.w ? p.V : 0), blocks = (jobs + 3) / 4;
-  const unsigned grid = (unsigned)(blocks < 8192 ? blocks : 8192) + (p.all_rows ? kEntropyRange : 0);
-  if (grid) entropy_prep_kernel<T><<<grid, 256, 0, s>>>(p);
-  return hipGetLastError();
+  auto go = [&](auto lanes) {
+    constexpr int L = decltype(lanes)::value, kRows = 256 / L;
+    const int64_t jobs = p.rows + (p.w ? p.V : 0), blocks = (jobs + kRows - 1) / kRows;
+    const unsigned grid = (unsigned)(blocks < 8192 ? blocks : 8192) + (p.all_rows ? kEntropyRange : 0);
+    if (grid) entropy_prep_kernel<T, L><<<grid, 256, 0, s>>>(p);
+    return hipGetLastError();
+  };
+  // short rows share a wave (16384 x 128 in float: 6.1 us, one a wave 9.2)
+  if (p.ld * sizeof(T) <= 512) return go(std::integral_constant<int, 16>{});
+  return go(std::integral_constant<int, 64>{});
 }
 
 template <typename T>
@@ -312,7 +320,10 @@ hipError_t launch_entropy_loss(const EntropyArgs& p, hipStream_t s) {
   const int parts = p.stats ? p.groups : p.V / 4;
   // a wave a row where the rows fill the device (8 rows of 4096 features, 1024 parts: 9.8 us, by 256 threads 5.8)
   const int threads = p.rows >= 1024 ? (parts <= 2048 ? 64 : 1024) : parts <= 128 ? 64 : parts <= 4096 ? 256 : 1024;
-  if (threads == 64)
+  // and four rows a wave where they are many and have little each (16384 rows of 16 parts: 6.1 us, one a wave 13.4)
+  if (p.rows >= 4096 && parts <= 32 && (p.Z || p.d_in <= 512))
+    entropy_loss_kernel<T, 16><<<(unsigned)((p.rows + 15) / 16), 256, 0, s>>>(p);
+  else if (threads == 64)
     entropy_loss_kernel<T, 64><<<(unsigned)((p.rows + 3) / 4), 256, 0, s>>>(p);
   else if (threads == 256)
     entropy_loss_kernel<T, 256><<<(unsigned)p.rows, 256, 0, s>>>(p);

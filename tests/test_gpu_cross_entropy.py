@@ -130,7 +130,8 @@ def test_against_64_bits(G, monkeypatch, i, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("N,d,V", [(4090, 520, 8190), (4090, 200, 8190), (8200, 1000, 2050), (2040, 136, 33001), (4090, 72, 4101)])
+@pytest.mark.parametrize("N,d,V", [(4090, 520, 8190), (4090, 200, 8190), (8200, 1000, 2050), (2040, 136, 33001), (4090, 72, 4101),
+                                   (5001, 100, 90), (4999, 700, 300)])
 def test_large_tiles(G, monkeypatch, N, d, V, dtype):
     monkeypatch.setattr(oracle, "ON", "cuda")
     t = TYPES[dtype]
@@ -143,6 +144,10 @@ def test_large_tiles(G, monkeypatch, N, d, V, dtype):
         # the bounds are those of the worst signs; in the 2-norm two roundings remain, G's and the output's
         off = float((a.double() - w).norm() / w.norm())
         assert off <= (1e-5 if a.dtype == torch.float32 else 2 * oracle.EPS[t] / 2), (what, off)
+    for part in ("dx", "dw", "db"):  # each alone is the same
+        asked = {f"want_{n}": n == part for n in ("dx", "dw", "db")}
+        one = G.cross_entropy_gradients(X, W, idx, dloss=dloss, wts=wts, bias=b, **asked)
+        assert all(o is None or torch.equal(a, o) for a, o in zip(got, one))
     loss, lse = G.cross_entropy(X, W, idx, wts=wts, bias=b)
     compare(loss, want[0], bounds[0], "loss")
     compare(lse, want[1], bounds[1], "lse")
