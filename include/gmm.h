@@ -472,9 +472,10 @@ int gmm_cross_entropy(const void* X, int32_t x_dtype, int64_t N, int32_t d_in, c
  * lse is. A row of no picks, or whose dloss is 0, has no part in the gradients,
  * whatever its X holds. G and, where the features are many, the logits pass through
  * the workspace in pieces of rows, of at most 2^29 logits (256 rows at least). lse
- * and loss come from the float logits; for G of 2-byte operands a logit may have been
- * kept in half, as its difference from the largest z of its row and of the 32 or 64
- * columns around it, so that a p is off by 2^-11 of that difference. The products take G rounded to
+ * and loss come from the float logits; for G of 2-byte operands p may have been kept
+ * in half, as its quotient by the largest of its row and of the 32 or 64 columns around
+ * it, so that it is off by 2^-12 of itself, and below 2^-29 of that largest by 2^-40 of
+ * it. The products take G rounded to
  * x_dtype, as the matrix instructions do, and accumulate in float; 2-byte operands
  * take it scaled so that the largest |dloss_n w_nj| becomes 2^11, which is
  * taken back from the sums, so that half keeps its 11 bits down to 2^-25 of

@@ -27,7 +27,7 @@ struct EntropyArgs {
   int groups, columns;   // of a group
   const float* Z;        // [rows][ldz] logits, or null: the picks' are computed from X and W
   void* G;               // [rows][ldz] their gradient in the operands' type; in its place
-                         // before, where Z is null, the logits' differences from their group's largest in half
+                         // before, where Z is null, the logits' exponentials over their group's largest in half
   int64_t ldz;           // a multiple of 8
   RowCoef* coef;         // [rows], or null: no gradient
   float* range;          // [kEntropyRange] and G's scale's inverse behind; null: no scale
@@ -67,7 +67,7 @@ hipError_t launch_entropy_prep(const EntropyPrep& p, hipStream_t s);
 // Loss, lse and coef of every row.
 template <typename T>
 hipError_t launch_entropy_loss(const EntropyArgs& p, hipStream_t s);
-// G and its column sums from Z, or the differences, and coef.
+// G and its column sums from Z, or the exponentials, and coef.
 template <typename T>
 hipError_t launch_entropy_gradient(const EntropyArgs& p, hipStream_t s);
 

@@ -236,10 +236,11 @@ __global__ void __launch_bounds__(THREADS > 256 ? THREADS : 256) entropy_loss_ke
 // The logits' gradient and its column sums (of the rounded values, in float,
 // without the scale). A wave takes a row's columns of its block, 16 bytes of G a
 // lane, so what belongs to the row is scalar; a block takes a chunk of rows.
-// HBM bounds it. GROUPED: 2-byte operands' logits lie in G's place as differences
-// from the largest z of their row and group of columns, in half: a probability is
-// off by 2^-11 of its distance to that, so the large ones least (8192 x 65536:
-// 401 us, against 600 from floats, which the product took 240 us more to write).
+// HBM bounds it. GROUPED: 2-byte operands' logits lie in G's place as exp(z - the
+// largest z of their row and group of columns), in half: a probability is off by
+// 2^-12 of itself, no more than G's rounding puts it off by, and below 2^-29 of the
+// largest of its group by 2^-40 of that (8192 x 65536: 401 us, against 600 from
+// floats, which the product took 240 us more to write).
 // ---------------------------------------------------------------------------
 template <typename T, bool GROUPED>
 __global__ void __launch_bounds__(256) entropy_gradient_kernel(const EntropyArgs p, int across) {
@@ -278,11 +279,9 @@ __global__ void __launch_bounds__(256) entropy_gradient_kernel(const EntropyArgs
       float g[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) z[i] = (float)raw[u].e[i];
-      if (GROUPED) {  // exp(z + most - base), most -infinity where all of the group are
-        c[u].up = most[u] == -__builtin_inff() ? 0.f : c[u].up * exp_of(most[u] - c[u].base);
-        c[u].base = 0.f;
-      }
-      logit_gradient<V>(c[u], p.picks, row, col, p.V, z, g);
+      if (GROUPED)  // most is -infinity where all of the group are
+        c[u].up = most[u] == -__builtin_inff() ? 0.f : c[u].up * exp_of(most[u] - c[u].base) * (1.f / kKeptOne);
+      logit_gradient<V, GROUPED>(c[u], p.picks, row, col, p.V, z, g);
       if (mine) {
         store_as<T, V>(static_cast<T*>(p.G) + row * p.ldz + col, V, g);
         if (p.parts)

@@ -77,10 +77,14 @@ enum { kTile256 = 0, kTile128 = 1, kTile64 = 2, kTileVariants = 3 };
 constexpr int kTileRows[kTileVariants] = {256, 128, 64};
 constexpr int kStepBytes = 128;  // bytes of k per step and operand row
 // In the place of an activation: statistics of the rows instead of C, or beside
-// it (of 2-byte operands C is then z - the largest z of its row and group, in
-// half); the gradient of a cross entropy whose logits z are.
+// it (of 2-byte operands C is then kKeptOne exp(z - the largest z of its row and
+// group), in half); the gradient of a cross entropy whose logits z are.
 constexpr int kRowStats = 6, kStatsToo = 7, kLogitGradient = 8;
-
+// What 1 is kept as: half's 11 bits reach down to 2^-29 of it. (The differences
+// z - largest themselves, in half, are as many bytes and put an entry off by
+// 2^-11 of them, so by 2^-8 of itself at a distance of 8 and more; the gradients
+// of half operands are rounded to 2^-12.)
+constexpr float kKeptOne = 32768.f;
 
 // Groups of columns whose statistics such a product of N columns writes:
 // those of a wave, 4 in a tile, or 2 where its waves are 2 x 2.

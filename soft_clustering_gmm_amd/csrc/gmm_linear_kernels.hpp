@@ -284,9 +284,9 @@ __global__ void __launch_bounds__(256) column_sums_kernel(const ProductArgs p) {
 }
 
 // The statistics of a wave's TI x NI tiles, straight from the registers: a lane
-// has 4 NI columns of a row, which 4 lanes share. SHIFT: acc becomes z - the
-// largest of its row.
-template <typename T, int TI, int NI, bool SHIFT, typename F>
+// has 4 NI columns of a row, which 4 lanes share. KEEP: acc becomes kKeptOne
+// exp(z - the largest of its row).
+template <typename T, int TI, int NI, bool KEEP, typename F>
 __device__ __forceinline__ void row_stats(const ProductArgs& p, f32x4 (*acc)[NI], F&& first_row, int n0, int group,
                                           int groups, int lane) {
   constexpr float kInf = __builtin_inff();
@@ -320,9 +320,9 @@ __device__ __forceinline__ void row_stats(const ProductArgs& p, f32x4 (*acc)[NI]
     for (int j = 0; j < NI; ++j)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        z[j][q] -= base;
-        sum += exp_of(z[j][q]);
-        if (SHIFT) acc[i][j][q] = z[j][q];
+        const float e = exp_of(z[j][q] - base);
+        sum += e;
+        if (KEEP) acc[i][j][q] = kKeptOne * e;
       }
     sum += __shfl_xor(sum, 16);
     sum += __shfl_xor(sum, 32);
@@ -335,9 +335,9 @@ __device__ __forceinline__ void row_stats(const ProductArgs& p, f32x4 (*acc)[NI]
   }
 }
 
-// Logits that leave as differences from their row's largest, in half.
+// Logits that leave as their exponentials over their row's largest, in half.
 template <typename T, int ACT>
-constexpr bool kShifted = ACT == kStatsToo && sizeof(T) == 2;
+constexpr bool kKept = ACT == kStatsToo && sizeof(T) == 2;
 
 // Products that may be unscaled: the gradients' of 2-byte operands (B k-strided).
 template <typename T, bool BS>
@@ -434,7 +434,7 @@ product_kernel(const ProductArgs p) {
   }
   step_barrier<0>(lds);  // nobody reads the slots, and nothing arrives in them any more
   if constexpr (ACT == kRowStats || ACT == kStatsToo)
-    row_stats<T, 2 * MI, NI, kShifted<T, ACT>>(p, acc[0], [&](int i) { return at.m0 + i / MI * HM + wm * TM + 16 * (i % MI); },
+    row_stats<T, 2 * MI, NI, kKept<T, ACT>>(p, acc[0], [&](int i) { return at.m0 + i / MI * HM + wm * TM + 16 * (i % MI); },
                              at.n0 + wn * TN, at.n0 / BN * WN + wn, p.tiles_n * WN, lane);
   if constexpr (ACT == kRowStats) return;
 
@@ -454,7 +454,7 @@ product_kernel(const ProductArgs p) {
   float bias[W];
 #pragma unroll
   for (int i = 0; i < W; ++i) bias[i] = 0.f;
-  if (whole && p.bias && n < p.N && !kShifted<T, ACT>) load_as<T, W>(static_cast<const T*>(p.bias) + n, p.N - n, bias);
+  if (whole && p.bias && n < p.N && !kKept<T, ACT>) load_as<T, W>(static_cast<const T*>(p.bias) + n, p.N - n, bias);
   // The next 16 rows' residual is on its way while these are finished: C may be
   // the residual, so the compiler keeps a load behind the stores before it.
   constexpr int R = ACT == kLogitGradient ? sizeof(RowCoef) / 4 : W;  // or the row's coefficients in its place
@@ -498,7 +498,7 @@ product_kernel(const ProductArgs p) {
         for (int k = 0; k < W; ++k) z[k] *= unscale;
       const int64_t m = row_of(i, q);
       if (m < p.M && n < p.N) {
-        if constexpr (kShifted<T, ACT>) {
+        if constexpr (kKept<T, ACT>) {
           store_as<_Float16, W>(static_cast<_Float16*>(p.C) + m * p.ldc + n, p.N - n, z);
         } else if (whole) {
           finish_row<T, ACT, W>(p, m, n, z, bias, res[i & 1][q]);

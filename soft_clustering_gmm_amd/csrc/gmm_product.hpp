@@ -348,11 +348,11 @@ __device__ __forceinline__ Pick pick_of(const RowPicks& p, int64_t row, int j, i
   return {is ? v : -1, !is ? 0.f : p.wts ? p.wts[at] : 1.f};
 }
 
-// The gradients of W logits z of a row, from column `col` of V on; 0 behind the
-// last. What few pieces have, picks and the last column, is behind branches: with
+// The gradients of W logits of a row, from column `col` of V on; 0 behind the
+// last. z are the logits, or (KEPT) numbers that c.up makes their s p. What few pieces have, picks and the last column, is behind branches: with
 // a comparison for each entry the products that end in this (8192 x 64 to 32768
 // classes) took 271 us, so 222.
-template <int W>
+template <int W, bool KEPT = false>
 __device__ __forceinline__ void logit_gradient(const RowCoef& c, const RowPicks& picks, int64_t row, int col, int V,
                                                const float* z, float* g) {
   if (c.d == 0.f) {
@@ -361,7 +361,7 @@ __device__ __forceinline__ void logit_gradient(const RowCoef& c, const RowPicks&
     return;
   }
 #pragma unroll
-  for (int i = 0; i < W; ++i) g[i] = c.up * exp_of(z[i] - c.base);
+  for (int i = 0; i < W; ++i) g[i] = c.up * (KEPT ? z[i] : exp_of(z[i] - c.base));
   if (col + W > V)
 #pragma unroll
     for (int i = 0; i < W; ++i)

@@ -110,8 +110,8 @@ struct EntropyBackPlan {
 
   // Tiles of the logits' product: whole sums where it is not written.
   Cut logits(int64_t rows, int V, int d_in, int e) const { return choose_cut(rows, V, d_in, e, twice ? 1 : 256); }
-  // Whether they are kept as half differences from their group's largest, in the place of their gradient.
-  bool shifted(int64_t rows, int V, int d_in, int e) const {
+  // Whether they are kept as exponentials over their group's largest, in half, in the place of their gradient.
+  bool kept(int64_t rows, int V, int d_in, int e) const {
     return !few && !twice && e == 2 && logits(rows, V, d_in, e).splits == 1;
   }
   // Sums of a column that a piece's gradient leaves, and what is kept of them: those of many tiles are added up first.
@@ -149,8 +149,8 @@ static EntropyBackPlan entropy_back_plan(int64_t N, int d_in, int V, int e) {
   size_t z = 0, g = 0;
   for (int64_t rows : {l.piece, N % l.piece})
     if (rows) {
-      const bool shifted = l.shifted(rows, V, d_in, e);
-      if (!l.twice && !shifted) z = std::max(z, (size_t)rows * l.ldz * sizeof(float));
+      const bool kept = l.kept(rows, V, d_in, e);
+      if (!l.twice && !kept) z = std::max(z, (size_t)rows * l.ldz * sizeof(float));
       g = std::max(g, (size_t)rows * l.ldz * e);
       if (!l.few) {
         const Cut c = l.logits(rows, V, d_in, e);
@@ -287,11 +287,11 @@ static hipError_t entropy_gradients(EntropyArgs a, int64_t N, T* dX, T* dW, T* d
         a.groups = stat_groups(c.variant, sizeof(T), a.V);
         a.columns = stat_columns(c.variant, sizeof(T));
       }
-      const bool shifted = l.shifted(rows, a.V, a.d_in, sizeof(T));
-      a.Z = l.twice || shifted ? nullptr : reinterpret_cast<float*>(ws + l.o_z);
-      p.C = shifted ? a.G : const_cast<float*>(a.Z);
+      const bool kept = l.kept(rows, a.V, a.d_in, sizeof(T));
+      a.Z = l.twice || kept ? nullptr : reinterpret_cast<float*>(ws + l.o_z);
+      p.C = kept ? a.G : const_cast<float*>(a.Z);
       p.ldc = l.ldz;
-      p.c_f32 = !shifted;
+      p.c_f32 = !kept;
       e = run_product<T>(c, false, false, l.twice ? kRowStats : a.stats ? kStatsToo : (int)GMM_ACT_NONE, p, s, false);
       if (e == hipSuccess && l.twice) e = launch_entropy_loss<T>(a, s);
       if (e == hipSuccess && l.twice && (dX || dW || db)) {  // again, for their gradient
