@@ -453,7 +453,8 @@ size_t gmm_layer_norm_workspace_bytes(int64_t N, int32_t D, int32_t x_dtype);
  * counts for nothing; a row may pick a class more than once, and a row of no
  * picks has a loss of 0. loss and lse (nullable) receive N floats. The logits
  * are not written to memory: the tiles of the product leave the largest and the
- * sum of each row's columns.
+ * sum of each row's columns, and the picks' logits. All three come from one float
+ * sum, so a loss of weights above 0 is not below 0.
  * Products and sums are float. A bias of -infinity takes a class out. A logit that is NaN or
  * +infinity, or only -infinity, make the row's lse and loss NaN (lse -infinity in
  * the last case).

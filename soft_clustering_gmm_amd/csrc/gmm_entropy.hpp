@@ -9,7 +9,6 @@
 
 namespace gmm {
 
-constexpr int kMaxPicksRow = 8;        // picks of a row
 constexpr int64_t kMaxClasses = 1 << 20;
 constexpr int kEntropyRange = 256;     // parts of the largest gradient of a row
 
@@ -25,7 +24,8 @@ struct EntropyArgs {
   float *loss, *lse;     // [rows], lse nullable
   const float* stats;    // [rows][groups][2] of the logits' product, or null: from the logits
   int groups, columns;   // of a group
-  const float* Z;        // [rows][ldz] logits, or null: the picks' are computed from X and W
+  const float* picked;   // [rows][picks.top] the picks' logits of that product, or null: from the logits
+  const float* Z;        // [rows][ldz] logits, or null: not written
   void* G;               // [rows][ldz] their gradient in the operands' type; in its place
                          // before, where Z is null, the logits' exponentials over their group's largest in half
   int64_t ldz;           // a multiple of 8

@@ -117,16 +117,18 @@ __device__ __forceinline__ float gradient_scale(const EntropyArgs& p) {
 // A row's loss from its log-sum, in parts from the product's tiles (`stats`) or
 // from its logits, by THREADS threads:
 //   loss = sum_j w_j (log s + (m - z_j)),  lse = m + log s
-// m - z_j first, so that a loss near 0 keeps its digits. The picks' logits are
-// read, or where they are nowhere computed, by the threads of the row: they are
-// few. Latency bounds it, so few rows take more threads each.
+// z_j is the logit that m and s were taken of, and m - z_j is formed first: both
+// terms are at least 0, and a loss near 0 is as exact as the logits' differences,
+// down to the half rounding of s next to 1. (With z_j as a sum of its own, in
+// another order than the product's, a third of the losses of rows that are sure
+// of their pick came out below 0, by 1e-5 to 1e-4.) Latency bounds it, so few
+// rows take more threads each.
 // ---------------------------------------------------------------------------
 template <typename T, int THREADS>
 __global__ void __launch_bounds__(THREADS > 256 ? THREADS : 256) entropy_loss_kernel(const EntropyArgs p) {
   constexpr float kInf = __builtin_inff();
   constexpr int kThreads = THREADS > 256 ? THREADS : 256, kRows = kThreads / THREADS, kWaves = (THREADS + 63) / 64;
   __shared__ LogSum red[kWaves];
-  __shared__ float dots[kWaves][kMaxPicksRow];
   const int t = threadIdx.x % THREADS, lane = threadIdx.x & 63;
   const float scale = p.coef && p.range ? gradient_scale(p) : 1.f;
   const int64_t row = blockIdx.x * (int64_t)kRows + threadIdx.x / THREADS;
@@ -159,31 +161,8 @@ __global__ void __launch_bounds__(THREADS > 256 ? THREADS : 256) entropy_loss_ke
   constexpr int kLanes = THREADS < 64 ? THREADS : 64;  // of a row in a wave
 #pragma unroll
   for (int o = kLanes / 2; o; o >>= 1) sum = join(sum, LogSum{__shfl_xor(sum.m, o), __shfl_xor(sum.s, o)});
-  // this wave's part of x W_j
-  auto dot = [&](int v) {
-    constexpr int V = Frag<T>::kPer;
-    const T *x = static_cast<const T*>(p.X) + row * p.d_in, *w = static_cast<const T*>(p.W) + (int64_t)v * p.d_in;
-    float of = 0.f;
-#pragma unroll 2
-    for (int c = t * V; c < p.d_in; c += THREADS * V) {
-      float a[V], b[V];
-      load_as<T, V>(x + c, p.d_in - c, a);
-      load_as<T, V>(w + c, p.d_in - c, b);
-#pragma unroll
-      for (int i = 0; i < V; ++i) of = fmaf(a[i], b[i], of);
-    }
-#pragma unroll
-    for (int o = kLanes / 2; o; o >>= 1) of += __shfl_xor(of, o);
-    return of;
-  };
   if constexpr (THREADS > 64) {
     if (lane == 0) red[threadIdx.x / 64] = sum;
-    if (!z)
-      for (int j = 0; j < p.picks.top; ++j) {
-        const Pick k = pick_of(p.picks, row, j, p.V);
-        const float of = k.w == 0.f ? 0.f : dot(k.v);
-        if (lane == 0) dots[threadIdx.x / 64][j] = of;
-      }
     __syncthreads();
     if (threadIdx.x >= 64) return;
     sum = red[0];
@@ -197,18 +176,7 @@ __global__ void __launch_bounds__(THREADS > 256 ? THREADS : 256) entropy_loss_ke
   for (int j = 0; j < p.picks.top; ++j) {
     const Pick k = pick_of(p.picks, row, j, p.V);
     if (k.w == 0.f) continue;  // the same for the row
-    float of = 0.f;
-    if (z) {
-      of = z[k.v];
-    } else {
-      if constexpr (THREADS > 64) {
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) of += dots[w][j];
-      } else {
-        of = dot(k.v);
-      }
-      if (p.bias) of += (float)static_cast<const T*>(p.bias)[k.v];
-    }
+    const float of = p.picked ? p.picked[row * p.picks.top + j] : z[k.v];
     share += k.w;
     if (c.v0 < 0 || c.v0 == k.v)
       c.v0 = k.v, c.c0 += k.w;
@@ -320,7 +288,7 @@ hipError_t launch_entropy_loss(const EntropyArgs& p, hipStream_t s) {
   // a wave a row where the rows fill the device (8 rows of 4096 features, 1024 parts: 9.8 us, by 256 threads 5.8)
   const int threads = p.rows >= 1024 ? (parts <= 2048 ? 64 : 1024) : parts <= 128 ? 64 : parts <= 4096 ? 256 : 1024;
   // and four rows a wave where they are many and have little each (16384 rows of 16 parts: 6.1 us, one a wave 13.4)
-  if (p.rows >= 4096 && parts <= 32 && (p.Z || p.d_in <= 512))
+  if (p.rows >= 4096 && parts <= 32)
     entropy_loss_kernel<T, 16><<<(unsigned)((p.rows + 15) / 16), 256, 0, s>>>(p);
   else if (threads == 64)
     entropy_loss_kernel<T, 64><<<(unsigned)((p.rows + 3) / 4), 256, 0, s>>>(p);

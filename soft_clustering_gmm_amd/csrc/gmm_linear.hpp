@@ -16,6 +16,7 @@ struct RowCoef {
   int all;
 };
 static_assert(sizeof(RowCoef) == 32, "two loads of 16 bytes");
+constexpr int kMaxPicksRow = 8;
 struct RowPicks {
   const int32_t* idx;  // [rows][top]
   const float* wts;    // [rows][top] or null: 1
@@ -55,11 +56,13 @@ struct ProductArgs {
   // act kRowStats and kStatsToo: the largest z of each row and group of columns and
   // the sum of exp(z - it): [M][groups][2], groups as stat_groups() says
   float* stats;
+  // and, where not null, the z of the rows' picks that are classes: [M][picks.top]
+  float* picked;
+  RowPicks picks;
   // act kLogitGradient: of the rows of C, which has the operands' type and zeros
   // from N to the end of its last 16 bytes; column sums of the rounded C times
   // *parts_unscale (null: 1), two for each tile's rows: [2 tiles_m][N], or null
   const RowCoef* coef;
-  RowPicks picks;
   float* parts;
   const float* parts_unscale;
   const float* unscale;  // C = *unscale times the product, where not null (gradients of 2-byte operands)
@@ -110,7 +113,10 @@ struct FewArgs {
   void* pre;
   int c_f32;
   int64_t ldc;
-  float* stats;  // act kRowStats, as in ProductArgs: groups of 16 few_tiles() columns
+  // act kRowStats, as in ProductArgs: groups of 16 few_tiles() columns
+  float* stats;
+  float* picked;
+  RowPicks picks;
 };
 // Tiles of 16 rows of B a block. More than two blocks a CU: two, which halves
 // what is read of A; a single row is one address for all lanes and costs little.

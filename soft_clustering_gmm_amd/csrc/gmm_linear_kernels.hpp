@@ -283,12 +283,50 @@ __global__ void __launch_bounds__(256) column_sums_kernel(const ProductArgs p) {
   column_sums<T>(p, blockIdx.x, red);
 }
 
+// The logits of the rows' picks in a wave's TI x NI tiles: whichever lane has one
+// writes it. The same float that the statistics are taken of, so that no pick's
+// lies above its row's largest. `mine` are the picks of the tile's rows from m0 on.
+// Most waves have none, so all rows are looked at first.
+template <int TI, int NI, typename F>
+__device__ __forceinline__ void store_picks(const ProductArgs& p, const f32x4 (*acc)[NI], const float (*bias)[4],
+                                            F&& first_row, const int* mine, int64_t m0, int n0, int lane) {
+  const int top = p.picks.top, n = n0 + 4 * (lane >> 4);  // this lane's columns are n + 16 j + q
+  for (int k = 0; k < top; ++k) {
+    bool some = false;
+#pragma unroll
+    for (int r = 0; r < 16 * TI; r += 64) {
+      const int i = r / 16 + lane / 16;
+      if (i < TI) {
+        const int v = mine[((int)(first_row(i) - m0) + (lane & 15)) * top + k];
+        some |= v >= n0 && v < min(p.N, n0 + 16 * NI);
+      }
+    }
+    if (!__any(some)) continue;
+    int v[TI];
+#pragma unroll
+    for (int i = 0; i < TI; ++i) v[i] = mine[((int)(first_row(i) - m0) + (lane & 15)) * top + k];
+#pragma unroll
+    for (int i = 0; i < TI; ++i) {
+      const int d = v[i] - n;
+      if (v[i] < p.N && (unsigned)d < 16u * NI && (d & 12) == 0) {
+        float z = 0.f;
+#pragma unroll
+        for (int j = 0; j < NI; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (d == 16 * j + q) z = acc[i][j][q] + bias[j][q];
+        p.picked[(first_row(i) + (lane & 15)) * top + k] = z;
+      }
+    }
+  }
+}
+
 // The statistics of a wave's TI x NI tiles, straight from the registers: a lane
 // has 4 NI columns of a row, which 4 lanes share. KEEP: acc becomes kKeptOne
 // exp(z - the largest of its row).
-template <typename T, int TI, int NI, bool KEEP, typename F>
-__device__ __forceinline__ void row_stats(const ProductArgs& p, f32x4 (*acc)[NI], F&& first_row, int n0, int group,
-                                          int groups, int lane) {
+template <typename T, int TI, int NI, bool KEEP, bool PICKS, typename F>
+__device__ __forceinline__ void row_stats(const ProductArgs& p, f32x4 (*acc)[NI], F&& first_row, const int* picks,
+                                          int64_t m0, int n0, int group, int groups, int lane) {
   constexpr float kInf = __builtin_inff();
   float bias[NI][4];
 #pragma unroll
@@ -303,6 +341,7 @@ __device__ __forceinline__ void row_stats(const ProductArgs& p, f32x4 (*acc)[NI]
     for (int q = 0; q < 4; ++q)
       if (n + q >= p.N) bias[j][q] = -kInf;  // the products there are 0
   }
+  if (PICKS && p.picked) store_picks<TI, NI>(p, acc, bias, first_row, picks, m0, n0, lane);
 #pragma unroll
   for (int i = 0; i < TI; ++i) {
     float most = -kInf, z[NI][4], sum = 0.f;
@@ -351,6 +390,8 @@ product_kernel(const ProductArgs p) {
   using OB = Operand<T, BN, NW, BS>;
   constexpr int kSlot = 2 * OA::kBytes + OB::kBytes, kPending = 2 * OA::kLoads + OB::kLoads;
   __shared__ __align__(1024) char lds[2 * kSlot];
+  constexpr bool kPicks = ACT == kRowStats || kKept<T, ACT>;  // float logits in memory hold them
+  __shared__ int picks[kPicks ? BM * kMaxPicksRow : 1];
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN;
@@ -407,6 +448,15 @@ product_kernel(const ProductArgs p) {
     }
     __builtin_amdgcn_sched_barrier(0);
   };
+  // the rows' picks, for the end (asked for there, a tile of 256 rows took 1.1 us more)
+  constexpr int kPickLoads = kPicks ? BM * kMaxPicksRow / (64 * NW) : 1;
+  int pick[kPickLoads];
+  if (kPicks && p.picked)
+#pragma unroll
+    for (int u = 0; u < kPickLoads; ++u) {
+      const int i = u * 64 * NW + threadIdx.x;
+      pick[u] = i < BM * p.picks.top && at.m0 * p.picks.top + i < p.M * p.picks.top ? p.picks.idx[at.m0 * p.picks.top + i] : -1;
+    }
   load_a(0, 0), load_b(0), load_a(0, 1);
   load_a(1, 0), load_b(1), load_a(1, 1);
   step_barrier<kPending + OA::kLoads>(lds);
@@ -432,10 +482,14 @@ product_kernel(const ProductArgs p) {
     read_b(s + 1, 0);
     multiply(1, 1, std::true_type{});
   }
+  if (kPicks && p.picked)
+#pragma unroll
+    for (int u = 0; u < kPickLoads; ++u)
+      if (u * 64 * NW + (int)threadIdx.x < BM * p.picks.top) picks[u * 64 * NW + threadIdx.x] = pick[u];
   step_barrier<0>(lds);  // nobody reads the slots, and nothing arrives in them any more
   if constexpr (ACT == kRowStats || ACT == kStatsToo)
-    row_stats<T, 2 * MI, NI, kKept<T, ACT>>(p, acc[0], [&](int i) { return at.m0 + i / MI * HM + wm * TM + 16 * (i % MI); },
-                             at.n0 + wn * TN, at.n0 / BN * WN + wn, p.tiles_n * WN, lane);
+    row_stats<T, 2 * MI, NI, kKept<T, ACT>, kPicks>(p, acc[0], [&](int i) { return at.m0 + i / MI * HM + wm * TM + 16 * (i % MI); }, picks,
+                             at.m0, at.n0 + wn * TN, at.n0 / BN * WN + wn, p.tiles_n * WN, lane);
   if constexpr (ACT == kRowStats) return;
 
   // The results go through LDS, 16 rows of m at a time in memory of the wave's
@@ -602,6 +656,9 @@ __global__ void __launch_bounds__(64 * NW) few_kernel(const FewArgs p) {
 #pragma unroll
         for (int w = 0; w < NW; ++w) z += red[w][m][n];
         if (p.bias) z += (float)static_cast<const T*>(p.bias)[n0 + n];
+        if (m < p.M)
+          for (int k = 0; k < p.picks.top; ++k)
+            if (p.picks.idx[m * p.picks.top + k] == n0 + n) p.picked[m * p.picks.top + k] = z;
       }
       float most = z;
 #pragma unroll

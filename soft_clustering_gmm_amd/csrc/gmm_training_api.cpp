@@ -53,13 +53,14 @@ constexpr int64_t kStatPiece = 256ll << 20;   // bytes of a piece's statistics
 // eight).
 constexpr int64_t kLogitPiece = 2048ll << 20;
 
-// Workspace of the loss: [padded rows of X of a piece] [padded W] [statistics].
+// Workspace of the loss: [padded rows of X of a piece] [padded W] [statistics]
+// [the picks' logits].
 struct EntropyPlan {
   bool few, pad;
   int64_t lx, piece;
   int groups;
   Cut cut;
-  size_t o_x, o_w, o_stats, bytes;
+  size_t o_x, o_w, o_stats, o_picked, bytes;
 };
 
 static EntropyPlan entropy_plan(int64_t N, int d_in, int V, int e) {
@@ -84,6 +85,7 @@ static EntropyPlan entropy_plan(int64_t N, int d_in, int V, int e) {
   l.o_x = take(l.pad ? (size_t)l.piece * l.lx * e : 0);
   l.o_w = take(l.pad ? (size_t)V * l.lx * e : 0);
   l.o_stats = take((size_t)l.piece * l.groups * 2 * sizeof(float));
+  l.o_picked = take((size_t)l.piece * kMaxPicksRow * sizeof(float));
   l.bytes = off;
   return l;
 }
@@ -100,13 +102,13 @@ constexpr int64_t kTwiceBytes = 32ll << 20;
 
 // Workspace of the gradients, for a piece of rows: [padded X] [X without the
 // rows that have no gradient] [padded W] [logits] [their gradient] [statistics]
-// [coefficients] [dW so far] [partial sums of the products] [column sums of the
+// [the picks' logits] [coefficients] [dW so far] [partial sums of the products] [column sums of the
 // tiles] [column sums] [range and scale].
 struct EntropyBackPlan {
   bool few, pad;
   bool twice;  // the logits are computed twice and not written
   int64_t lx, ldz, piece, chunk, chunks;  // chunks: of all rows
-  size_t o_x, o_clean, o_w, o_z, o_g, o_stats, o_coef, o_acc, o_part, o_fold, o_db, o_range, bytes;
+  size_t o_x, o_clean, o_w, o_z, o_g, o_stats, o_picked, o_coef, o_acc, o_part, o_fold, o_db, o_range, bytes;
 
   // Tiles of the logits' product: whole sums where it is not written.
   Cut logits(int64_t rows, int V, int d_in, int e) const { return choose_cut(rows, V, d_in, e, twice ? 1 : 256); }
@@ -167,6 +169,7 @@ static EntropyBackPlan entropy_back_plan(int64_t N, int d_in, int V, int e) {
   l.o_z = take(z);
   l.o_g = take(g);
   l.o_stats = take(stats);
+  l.o_picked = take(l.few ? 0 : (size_t)l.piece * kMaxPicksRow * sizeof(float));
   l.o_coef = take((size_t)l.piece * sizeof(RowCoef));
   l.o_acc = take(l.piece < N && e == 2 ? (size_t)V * d_in * sizeof(float) : 0);
   l.o_part = take(part);
@@ -207,8 +210,10 @@ static hipError_t entropy_forward(EntropyArgs a, int64_t N, char* ws, hipStream_
     a.loss = row_at(all.loss, r, 1);
     a.lse = row_at(all.lse, r, 1);
     a.stats = p.stats = reinterpret_cast<float*>(ws + l.o_stats);
+    a.picked = p.picked = reinterpret_cast<float*>(ws + l.o_picked);
+    p.picks = a.picks;
     if (l.few) {
-      const FewArgs f{a.X, a.W, (int)N, a.V, a.d_in, a.bias, nullptr, nullptr, nullptr, 1, 0, p.stats};
+      const FewArgs f{a.X, a.W, (int)N, a.V, a.d_in, a.bias, nullptr, nullptr, nullptr, 1, 0, p.stats, p.picked, p.picks};
       a.groups = l.groups;
       if ((e = launch_few<T>(kRowStats, f, s)) != hipSuccess) return e;
       return launch_entropy_loss<T>(a, s);
@@ -272,9 +277,9 @@ static hipError_t entropy_gradients(EntropyArgs a, int64_t N, T* dX, T* dW, T* d
     p.partial = reinterpret_cast<float*>(ws + l.o_part);
     // the logits, through the caches, which the next kernel finds them in (2048 x 1024 to 32768 classes: 580 us against
     // 598 past them)
-    a.stats = nullptr;
+    a.stats = a.picked = nullptr;
     if (l.few) {
-      const FewArgs f{a.X, a.W, (int)N, a.V, a.d_in, a.bias, nullptr, const_cast<float*>(a.Z), nullptr, 1, l.ldz, nullptr};
+      const FewArgs f{a.X, a.W, (int)N, a.V, a.d_in, a.bias, nullptr, const_cast<float*>(a.Z), nullptr, 1, l.ldz};
       e = launch_few<T>(GMM_ACT_NONE, f, s);
     } else {
       p.A = pad_x ? ws + l.o_x : a.X;
@@ -289,6 +294,8 @@ static hipError_t entropy_gradients(EntropyArgs a, int64_t N, T* dX, T* dW, T* d
       }
       const bool kept = l.kept(rows, a.V, a.d_in, sizeof(T));
       a.Z = l.twice || kept ? nullptr : reinterpret_cast<float*>(ws + l.o_z);
+      p.picks = a.picks;
+      if (!a.Z) a.picked = p.picked = reinterpret_cast<float*>(ws + l.o_picked);
       p.C = kept ? a.G : const_cast<float*>(a.Z);
       p.ldc = l.ldz;
       p.c_f32 = !kept;
@@ -296,7 +303,6 @@ static hipError_t entropy_gradients(EntropyArgs a, int64_t N, T* dX, T* dW, T* d
       if (e == hipSuccess && l.twice) e = launch_entropy_loss<T>(a, s);
       if (e == hipSuccess && l.twice && (dX || dW || db)) {  // again, for their gradient
         p.coef = a.coef;
-        p.picks = a.picks;
         const bool folds = db && l.folds(rows, a.V, a.d_in, sizeof(T));
         p.parts = folds ? reinterpret_cast<float*>(ws + l.o_fold) : a.parts;
         p.parts_unscale = scaled ? a.range + kEntropyRange : nullptr;
