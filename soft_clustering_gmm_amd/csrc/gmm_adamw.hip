@@ -53,7 +53,7 @@ __device__ __forceinline__ void from_f8(uint32_t c, float* out) {
 
 // A step's numbers that are the same for all elements.
 struct AdamStep {
-  float beta1, beta2, rest1, rest2, scale_g, keep, rate, root, eps;
+  float beta1, beta2, rest1, rest2, scale_g, shrink, rate, root, eps;
   uint32_t n;
 };
 
@@ -138,7 +138,8 @@ struct AdamLane {
       v[k] = s.beta2 * v[k] + s.rest2 * x * x;
       const float r = sqrtf(v[k]);  // the instruction alone would take a denormal v for 0
       const float old = MASTER ? master[k] : (float)p[k];
-      master[k] = fmaf(s.keep, old, -(s.rate * m[k] * __builtin_amdgcn_rcpf(fmaf(r, s.root, s.eps))));
+      // lr decay stays a small number of its own: in 1 - lr decay it would be a multiple of 2^-24, for all elements alike
+      master[k] = old - fmaf(s.shrink, old, s.rate * m[k] * __builtin_amdgcn_rcpf(fmaf(r, s.root, s.eps)));
       p[k] = (TP)master[k];
       if (F8) v[k] = r;
     }
@@ -216,7 +217,7 @@ __global__ void __launch_bounds__(64 * kAdamWaves) adamw_kernel(const AdamArgs a
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const float lr = a.lr * (a.lr_factor ? *a.lr_factor : 1.f);
     const double c1 = -expm1((double)n * a.log_beta1), c2 = -expm1((double)n * a.log_beta2);
-    const AdamStep s{a.beta1, a.beta2, a.rest1, a.rest2, a.grad_factor ? *a.grad_factor : 1.f, 1.f - lr * a.decay,
+    const AdamStep s{a.beta1, a.beta2, a.rest1, a.rest2, a.grad_factor ? *a.grad_factor : 1.f, lr * a.decay,
                      (float)(lr / c1), (float)(1. / sqrt(c2)), a.eps, (uint32_t)n};
     const int64_t blocks = (t.n + kStateBlock - 1) / kStateBlock, b0 = (int64_t)(block - a.first[i]) * a.chunk;
     const int64_t b1 = b0 + a.chunk < blocks ? b0 + a.chunk : blocks;
