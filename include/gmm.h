@@ -524,7 +524,8 @@ size_t gmm_cross_entropy_workspace_bytes(int64_t N, int32_t d_in, int32_t V, int
  * step (device, 2 int64, 8-byte aligned) holds the number of steps done, which the
  * call counts up by one, and a word for the library's own use that has to be 0 between calls. All
  * arithmetic is float, the powers of beta double. m, v and master are 16-byte
- * aligned. beta1 and beta2 from 0 to below 1, eps > 0, lr and weight_decay >= 0.
+ * aligned. beta1 and beta2 from 0 to below 1, lr and weight_decay >= 0, eps at least
+ * 1.17549435e-38 (a normal float), all of them finite as floats.
  * No parameter may overlap another tensor of the call. */
 int gmm_adamw_step(int32_t count, const int64_t* sizes, void* const* params, int32_t p_dtype,
                    const void* const* grads, int32_t g_dtype, float* master, void* m, void* v, int32_t state_bits,

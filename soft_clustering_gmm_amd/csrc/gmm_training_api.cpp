@@ -3,6 +3,7 @@
 // the host before anything is enqueued.
 #include "../../include/gmm.h"
 
+#include <float.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -40,6 +41,8 @@ static size_t norm_bytes(int64_t N, int D, int e) {
 }
 
 static bool factor_ok(double beta) { return beta >= 0. && beta < 1.; }
+// A size that is a finite float, too.
+static bool size_ok(double x) { return x >= 0. && x <= (double)FLT_MAX; }
 
 // The rows of a piece: what the call keeps of a row (`bytes`) within `most`, in
 // whole tiles.
@@ -484,8 +487,9 @@ int gmm_adamw_step(int32_t count, const int64_t* sizes, void* const* params, int
                    double weight_decay, const float* lr_factor, const float* grad_factor, void* stream) {
   if (!dtype_ok(p_dtype) || (g_dtype != p_dtype && g_dtype != GMM_F32)) return GMM_EINVAL;
   if (state_bits != 32 && state_bits != 8) return GMM_EINVAL;
-  if (!factor_ok(beta1) || !factor_ok(beta2) || !((float)eps > 0.f) || !isfinite(eps)) return GMM_EINVAL;
-  if (!(lr >= 0.) || !isfinite(lr) || !(weight_decay >= 0.) || !isfinite(weight_decay)) return GMM_EINVAL;
+  if (!factor_ok(beta1) || !factor_ok(beta2) || !size_ok(lr) || !size_ok(weight_decay)) return GMM_EINVAL;
+  // the device's reciprocal takes a denormal number for 0
+  if (!size_ok(eps) || (float)eps < FLT_MIN) return GMM_EINVAL;
   const int64_t total = gmm_adamw_state_elements(count, sizes);
   if (total < 0 || !step || reinterpret_cast<uintptr_t>(step) % 8 || (count > 0 && (!params || !grads)))
     return GMM_EINVAL;
