@@ -71,10 +71,10 @@ hipError_t launch_entropy_loss(const EntropyArgs& p, hipStream_t s);
 template <typename T>
 hipError_t launch_entropy_gradient(const EntropyArgs& p, hipStream_t s);
 
-// `count` rows of V column sums to kFoldedSums or fewer: those of each group of
-// fold_rows(count) added up.
+// `count` rows of V column sums to `most` or fewer: those of each group of
+// fold_rows(count, most) added up. To one row, it may be one of them.
 constexpr int kFoldedSums = 256;
-inline int64_t fold_rows(int64_t count) { return (count + kFoldedSums - 1) / kFoldedSums; }
-hipError_t launch_entropy_fold(const float* parts, int64_t count, int V, float* out, hipStream_t s);
+inline int64_t fold_rows(int64_t count, int64_t most) { return (count + most - 1) / most; }
+hipError_t launch_entropy_fold(const float* parts, int64_t count, int64_t most, int V, float* out, hipStream_t s);
 
 }  // namespace gmm

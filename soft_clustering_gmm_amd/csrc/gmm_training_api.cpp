@@ -106,13 +106,15 @@ constexpr int64_t kTwiceBytes = 32ll << 20;
 // Workspace of the gradients, for a piece of rows: [padded X] [X without the
 // rows that have no gradient] [padded W] [logits] [their gradient] [statistics]
 // [the picks' logits] [coefficients] [dW so far] [partial sums of the products] [column sums of the
-// tiles] [column sums] [range and scale].
+// tiles] [column sums, those of the pieces before first] [range and scale].
 struct EntropyBackPlan {
   bool few, pad;
   bool twice;  // the logits are computed twice and not written
-  int64_t lx, ldz, piece, chunk, chunks;  // chunks: of all rows
+  int64_t lx, ldz, piece, chunk;
   size_t o_x, o_clean, o_w, o_z, o_g, o_stats, o_picked, o_coef, o_acc, o_part, o_fold, o_db, o_range, bytes;
 
+  // Rows of column sums that a piece finds of those before.
+  int64_t carries(int64_t N) const { return piece < N ? 1 : 0; }
   // Tiles of the logits' product: whole sums where it is not written.
   Cut logits(int64_t rows, int V, int d_in, int e) const { return choose_cut(rows, V, d_in, e, twice ? 1 : 256); }
   // Whether they are kept as exponentials over their group's largest, in half, in the place of their gradient.
@@ -126,7 +128,7 @@ struct EntropyBackPlan {
   bool folds(int64_t rows, int V, int d_in, int e) const { return twice && tile_sums(rows, V, d_in, e) > kFoldedSums; }
   int64_t sums(int64_t rows, int V, int d_in, int e) const {
     const int64_t n = tile_sums(rows, V, d_in, e);
-    return folds(rows, V, d_in, e) ? ceil_div(n, fold_rows(n)) : n;
+    return folds(rows, V, d_in, e) ? ceil_div(n, fold_rows(n, kFoldedSums)) : n;
   }
 };
 
@@ -139,13 +141,12 @@ static EntropyBackPlan entropy_back_plan(int64_t N, int d_in, int V, int e) {
   l.piece = piece_rows(N, l.ldz * (int64_t)sizeof(float), kLogitPiece);
   l.twice = !l.few && d_in <= (e == 2 ? kTwice : kTwiceF32) && l.piece * l.ldz * (int64_t)sizeof(float) > kTwiceBytes;
   // Rows of a block that has columns of G: 16 at least (of 1001 rows and 7777 classes in half 64 make a block a CU, 17.9
-  // us, and 16 take 10.4), more while 2048 blocks are left, then as many as leave 1024 sums of a column, 8192 at most.
+  // us, and 16 take 10.4), more while 2048 blocks are left, then as many as leave 1024 sums of a column.
   const int64_t across = ceil_div(l.ldz, 64 * (16 / e));
   l.chunk = std::max<int64_t>(16, std::min<int64_t>(64, l.piece * across / 2048 / 16 * 16));
-  l.chunk = std::max(l.chunk, std::min<int64_t>(8192, ceil_div(ceil_div(N, 1024), 16) * 16));
+  l.chunk = std::max(l.chunk, ceil_div(ceil_div(l.piece, 1024), 16) * 16);
   l.chunk = std::min(l.piece, l.chunk);
-  l.chunks = l.sums(l.piece, V, d_in, e) * (N / l.piece) + (N % l.piece ? l.sums(N % l.piece, V, d_in, e) : 0);
-  size_t off = 0, part = 0, stats = 0, fold = 0;
+  size_t off = 0, part = 0, stats = 0, fold = 0, sums = 0;
   auto take = [&](size_t bytes) {
     const size_t o = off;
     off = align_up(off + bytes, 256);
@@ -165,6 +166,7 @@ static EntropyBackPlan entropy_back_plan(int64_t N, int d_in, int V, int e) {
       part = std::max(part, partial_bytes(choose_cut(rows, d_in, V, e), rows, d_in));
       part = std::max(part, partial_bytes(choose_cut(V, d_in, rows, e), V, d_in));
       if (l.folds(rows, V, d_in, e)) fold = std::max(fold, (size_t)l.tile_sums(rows, V, d_in, e) * V * sizeof(float));
+      sums = std::max(sums, (size_t)(l.sums(rows, V, d_in, e) + l.carries(N)) * V * sizeof(float));
     }
   l.o_x = take(l.pad && !l.few ? (size_t)l.piece * l.lx * e : 0);
   l.o_clean = take((size_t)l.piece * l.lx * e);
@@ -177,7 +179,7 @@ static EntropyBackPlan entropy_back_plan(int64_t N, int d_in, int V, int e) {
   l.o_acc = take(l.piece < N && e == 2 ? (size_t)V * d_in * sizeof(float) : 0);
   l.o_part = take(part);
   l.o_fold = take(fold);
-  l.o_db = take((size_t)l.chunks * V * sizeof(float));
+  l.o_db = take(sums);
   l.o_range = take((kEntropyRange + 1) * sizeof(float));
   l.bytes = off;
   return l;
@@ -250,7 +252,7 @@ static hipError_t entropy_gradients(EntropyArgs a, int64_t N, T* dX, T* dW, T* d
   a.coef = reinterpret_cast<RowCoef*>(ws + l.o_coef);
   a.chunk = l.chunk;
   float* sums = reinterpret_cast<float*>(ws + l.o_db);
-  a.parts = db ? sums : nullptr;
+  a.parts = db ? sums + l.carries(N) * a.V : nullptr;
   const bool pad_w = l.pad && (dX || !l.few), pad_x = l.pad && !l.few;
   const void* W = pad_w ? ws + l.o_w : a.W;
   for (int64_t r = 0; r < N; r += l.piece) {
@@ -313,14 +315,16 @@ static hipError_t entropy_gradients(EntropyArgs a, int64_t N, T* dX, T* dW, T* d
         p.c_f32 = sizeof(T) == 4;
         e = run_product<T>(c, false, false, kLogitGradient, p, s, false);
         if (e == hipSuccess && folds)
-          e = launch_entropy_fold(p.parts, l.tile_sums(rows, a.V, a.d_in, sizeof(T)), a.V, a.parts, s);
+          e = launch_entropy_fold(p.parts, l.tile_sums(rows, a.V, a.d_in, sizeof(T)), kFoldedSums, a.V, a.parts, s);
       }
     }
     if (e != hipSuccess) return e;
     if (!l.twice && (e = launch_entropy_loss<T>(a, s)) != hipSuccess) return e;
     if (!dX && !dW && !db) continue;
     if (!l.twice && (e = launch_entropy_gradient<T>(a, s)) != hipSuccess) return e;
-    if (db) a.parts += l.sums(rows, a.V, a.d_in, sizeof(T)) * a.V;
+    // the column sums of this piece, and of those before in front of them
+    const int64_t first = r ? 0 : l.carries(N), count = l.carries(N) + l.sums(rows, a.V, a.d_in, sizeof(T)) - first;
+    if (db && !last && (e = launch_entropy_fold(sums + first * a.V, count, 1, a.V, sums, s)) != hipSuccess) return e;
     p = ProductArgs{};
     p.partial = reinterpret_cast<float*>(ws + l.o_part);
     p.N = a.d_in;
@@ -328,9 +332,9 @@ static hipError_t entropy_gradients(EntropyArgs a, int64_t N, T* dX, T* dW, T* d
     p.ldb = l.lx;
     p.unscale = scaled ? a.range + kEntropyRange : nullptr;
     if (db && last) {  // summed beside the next product
-      p.sums = sums;
+      p.sums = sums + first * a.V;
       p.sums_out = db;
-      p.sums_rows = l.chunks;
+      p.sums_rows = count;
       p.sums_cols = a.V;
       p.sum_blocks = (int)ceil_div(a.V, kSumCols);
       if (!dX && !dW) return launch_column_sums<T>(p, s);
