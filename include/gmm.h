@@ -475,7 +475,7 @@ int gmm_cross_entropy(const void* X, int32_t x_dtype, int64_t N, int32_t d_in, c
  * the workspace in pieces of rows, of at most 2^29 logits (256 rows at least). lse
  * and loss come from the float logits; for G of 2-byte operands p may have been kept
  * in half, as its quotient by the largest of its row and of the 32 or 64 columns around
- * it, so that it is off by 2^-12 of itself, and below 2^-29 of that largest by 2^-40 of
+ * it, so that it is off by 2^-11 of itself, and below 2^-29 of that largest by 2^-40 of
  * it. The products take G rounded to
  * x_dtype, as the matrix instructions do, and accumulate in float; 2-byte operands
  * take it scaled so that the largest |dloss_n w_nj| becomes 2^11, which is

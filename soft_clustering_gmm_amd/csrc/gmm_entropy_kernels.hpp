@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(THREADS > 256 ? THREADS : 256) entropy_loss_ke
 // lane, so what belongs to the row is scalar; a block takes a chunk of rows.
 // HBM bounds it. GROUPED: 2-byte operands' logits lie in G's place as exp(z - the
 // largest z of their row and group of columns), in half: a probability is off by
-// 2^-12 of itself, no more than G's rounding puts it off by, and below 2^-29 of the
+// 2^-11 of itself, no more than G's rounding puts it off by, and below 2^-29 of the
 // largest of its group by 2^-40 of that (8192 x 65536: 401 us, against 600 from
 // floats, which the product took 240 us more to write).
 // ---------------------------------------------------------------------------

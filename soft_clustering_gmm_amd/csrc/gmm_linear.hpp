@@ -86,7 +86,7 @@ constexpr int kRowStats = 6, kStatsToo = 7, kLogitGradient = 8;
 // What 1 is kept as: half's 11 bits reach down to 2^-29 of it. (The differences
 // z - largest themselves, in half, are as many bytes and put an entry off by
 // 2^-11 of them, so by 2^-8 of itself at a distance of 8 and more; the gradients
-// of half operands are rounded to 2^-12.)
+// of half operands are rounded to 2^-11.)
 constexpr float kKeptOne = 32768.f;
 
 // Groups of columns whose statistics such a product of N columns writes:
