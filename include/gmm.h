@@ -423,9 +423,9 @@ size_t gmm_expert_workspace_bytes(int64_t N, int32_t D, int32_t K, int32_t F, in
  * bfloat16 products). gamma and beta (D) have type w_dtype, which is y_dtype or
  * GMM_F32; each is nullable (1 and 0). stats (nullable, N x 2 float) receives
  * mean and rstd, which the backward call needs. eps > 0. Arithmetic is float
- * (the squares of a row's deviations have to sum to less than 3.4e38), rounded
- * once per output; rows may start at any element. What is not finite in a row
- * reaches that row alone. Y may be X itself where their types agree. */
+ * (a row's values, and the squares of their deviations from its mean, which is off by
+ * up to 2^-17 of the largest value, have to sum to less than 3.4e38), rounded once per
+ * output; rows may start at any element. What is not finite in a row reaches that row alone. Y may be X itself where their types agree. */
 int gmm_layer_norm(const void* X, int32_t x_dtype, int64_t N, int32_t D, const void* gamma, const void* beta,
                    int32_t w_dtype, float eps, void* Y, int32_t y_dtype, float* stats, void* stream);
 

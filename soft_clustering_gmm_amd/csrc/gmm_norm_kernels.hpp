@@ -228,11 +228,13 @@ __global__ void __launch_bounds__(norm_threads(G)) norm_backward_kernel(const No
       const auto own = span(c);
       if (!kKeep) piece(row, c, now.e[0]);
       if (!kGamma) own.template weights<TY>(p.gamma, p.w_f32, 1.f, gamma[0]);
+      // beyond the row x is 0, and (0 - mean) rstd may be beyond float
+      const float rstd = LIE == kWhole && own.skip ? 0.f : now.rstd;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         // what is another's counts as 0; beyond the row dY is
         const float dy = LIE != kMoved || own.mine(i) ? (float)now.e[w].y[i] : 0.f;
-        const float h = ((float)now.e[w].x[i] - now.mean) * now.rstd;
+        const float h = LIE == kTiny && !own.mine(i) ? 0.f : ((float)now.e[w].x[i] - now.mean) * rstd;
         if (kKeep) {
           dg[w][i] = fmaf(dy, h, dg[w][i]);
           db[w][i] += dy;
