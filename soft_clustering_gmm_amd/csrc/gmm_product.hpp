@@ -301,17 +301,16 @@ __device__ __forceinline__ void store_row(void* p, int64_t at, int n, bool is_f3
     store_as<T, W, STREAM>(static_cast<T*>(p) + at, n, v);
 }
 
-// Sums (or largest) of K values over the G threads of a row, in every thread and
-// in a fixed order. Rows of several waves meet in LDS: `red` has two halves that
-// calls take in turn, so one barrier a call is enough (who writes a half again
-// has passed the barrier that all pass after reading it).
-template <int G, int K, bool MOST>
-__device__ __forceinline__ void row_reduce(float* v, float (*red)[G > 64 ? G / 64 : 1][2], int& turn) {
-  auto join = [](float a, float b) { return MOST ? fmaxf(a, b) : a + b; };
+// Sums of K values over the G threads of a row, in every thread and in a fixed
+// order. Rows of several waves meet in LDS: `red` has two halves that calls take
+// in turn, so one barrier a call is enough (who writes a half again has passed
+// the barrier that all pass after reading it).
+template <int G, int K>
+__device__ __forceinline__ void row_sum(float* v, float (*red)[G > 64 ? G / 64 : 1][2], int& turn) {
 #pragma unroll
   for (int o = (G < 64 ? G : 64) / 2; o; o >>= 1)
 #pragma unroll
-    for (int k = 0; k < K; ++k) v[k] = join(v[k], __shfl_xor(v[k], o));
+    for (int k = 0; k < K; ++k) v[k] += __shfl_xor(v[k], o);
   if constexpr (G > 64) {
     const int wave = threadIdx.x / 64;
     if (threadIdx.x % 64 == 0)
@@ -320,17 +319,12 @@ __device__ __forceinline__ void row_reduce(float* v, float (*red)[G > 64 ? G / 6
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      v[k] = MOST ? -__builtin_inff() : 0.f;
+      v[k] = 0.f;
 #pragma unroll
-      for (int w = 0; w < G / 64; ++w) v[k] = join(v[k], red[turn][w][k]);
+      for (int w = 0; w < G / 64; ++w) v[k] += red[turn][w][k];
     }
     turn ^= 1;
   }
-}
-
-template <int G, int K>
-__device__ __forceinline__ void row_sum(float* v, float (*red)[G > 64 ? G / 64 : 1][2], int& turn) {
-  row_reduce<G, K, false>(v, red, turn);
 }
 
 // exp(x), x <= 0 or so: the error is that of x log2(e) in float, |x| 2^-23.
