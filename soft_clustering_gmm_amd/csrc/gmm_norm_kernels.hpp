@@ -172,7 +172,12 @@ __global__ void __launch_bounds__(norm_threads(G)) norm_kernel(const NormArgs p)
 // One read of X and dY (two of rows of more than 16384 elements, the second from
 // the caches): a thread keeps its columns' sums over the rows that its
 // block takes; they go to `partial` and are added in a fixed order. HBM bounds
-// it (16384 x 2048, float X and bfloat16 dY: 62 us, 5.4 TB/s).
+// it (16384 x 2048, float X and bfloat16 dY: 62 us, 5.4 TB/s). 1024 threads have
+// 128 registers each, and rows of 8193 to 16384 elements want more: gamma is read
+// again, and up to 54 of the registers are kept in memory where X is float and dY
+// is not or the pieces are moved (4096 x 16384: float 182 us, bfloat16 114, float
+// to bfloat16 158; x 16382: 237, 170 and 265). Wider rows are read by the columns'
+// kernel and then twice here (2048 x 32768: 339, 221 and 294 us).
 // ---------------------------------------------------------------------------
 template <typename TX, typename TY, int G, int C, int LIE>
 __global__ void __launch_bounds__(norm_threads(G)) norm_backward_kernel(const NormArgs p) {
@@ -180,7 +185,7 @@ __global__ void __launch_bounds__(norm_threads(G)) norm_backward_kernel(const No
   constexpr bool kKeep = C * V <= kNormKeep;
   constexpr bool kAhead = kKeep && G <= 512;  // the next row is on its way while one is finished
   constexpr int kHeld = kKeep ? C : 1, kUnroll = kKeep ? C : 1;
-  constexpr bool kGamma = kKeep && G <= 512;  // gamma, too (of 1024 threads it would spill)
+  constexpr bool kGamma = kKeep && G <= 512;  // gamma, too (1024 threads have no room for it)
   __shared__ float red[2][G > 64 ? G / 64 : 1][2];
   __shared__ float sums[kKeep && kRows > 1 ? kRows : 1][kKeep && kRows > 1 ? G * C * V : 1];
   int turn = 0;
@@ -228,8 +233,12 @@ __global__ void __launch_bounds__(norm_threads(G)) norm_backward_kernel(const No
       const auto own = span(c);
       if (!kKeep) piece(row, c, now.e[0]);
       if (!kGamma) own.template weights<TY>(p.gamma, p.w_f32, 1.f, gamma[0]);
-      // beyond the row x is 0, and (0 - mean) rstd may be beyond float
-      const float rstd = LIE == kWhole && own.skip ? 0.f : now.rstd;
+      // Beyond the row x is 0, and (0 - mean) rstd may be beyond float, and no number times dY's 0. 1024 threads have no
+      // register left for it, and pass over such pieces (4096 x 16384, float to bfloat16: 158 us, 223 with a rstd of 0
+      // there); in the others a branch costs more (16384 x 2048, float to bfloat16: 83, with it 69).
+      const bool none = LIE == kWhole && own.skip;
+      if (G == 1024 && none) continue;
+      const float rstd = none ? 0.f : now.rstd;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         // what is another's counts as 0; beyond the row dY is

@@ -40,3 +40,28 @@ def test_constant_rows(G, t, D):
     bound = 100 * 2.0 ** -24 * stats[:4, 1:].double() * (k.abs() + k.abs().mean(1, keepdim=True))
     assert ((dx[:4].double() - want).abs() <= bound + oracle.rounding(want.abs() + bound, t)).all()
     assert dx.isfinite().all() and dgamma.isfinite().all() and dbeta.isfinite().all()
+
+
+# pieces for some of the threads of every number of threads that share a row
+@pytest.mark.parametrize("x,y", [("f32", "f32"), ("f32", "bf16"), ("bf16", "bf16"), ("f16", "f16")])
+@pytest.mark.parametrize("D", [3, 12, 24, 25, 72, 136, 300, 520, 1000, 1032, 2056, 2504, 4104, 6000, 9000, 12000, 17000, 40000])
+def test_given_statistics(G, x, y, D):
+    """Rows of one value, which is their mean, under statistics that the caller gives: dX = rstd (k - mean k)."""
+    t = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+    g = torch.Generator(device="cuda").manual_seed(D)
+    top = 2.0 ** 110 if x != "f16" else 2.0 ** 15
+    X = torch.full((5, D), top, device="cuda", dtype=t[x])
+    X[1::2] = -top
+    dY = torch.randn(5, D, generator=g, device="cuda").to(t[y])
+    gamma = (1 + 0.2 * torch.randn(D, generator=g, device="cuda")).to(t[y])
+    rstd = 2.0 ** 20 if x != "f16" else 2.0 ** 114  # top times rstd is beyond float
+    if x == "f16":
+        dY.zero_()  # 2^114 times anything else is beyond half
+    stats = torch.tensor([top, rstd], device="cuda").expand(5, 2).contiguous()
+    stats[1::2, 0] = -top
+    dx, dgamma, dbeta = G.layer_norm_backward(dY, X, stats, gamma)
+    k = dY.double() * gamma.double()
+    want = rstd * (k - k.mean(1, keepdim=True))
+    bound = 100 * 2.0 ** -24 * rstd * (k.abs() + k.abs().mean(1, keepdim=True))
+    assert ((dx.double() - want).abs() <= bound + oracle.rounding(want.abs() + bound, t[x])).all()
+    assert (dgamma == 0).all() and dbeta.isfinite().all()
