@@ -39,9 +39,10 @@ struct EntropyArgs {
   int64_t ldx;
   int own_range;
 };
-// (16 rows of 512 features to 300 classes: 34.5 us for the call, with a launch
-// before 36.9; 300 rows, whose picks every wave then reads: 37.6 and 36.7.)
-constexpr int64_t kOwnPrepRows = 64;
+// Every wave reads all picks then (512 features to 300 classes, with a launch
+// before and so: 16 rows 28.0 us and 25.7, 512 36.2 and 33.4, 1024 39.1 and 38.6,
+// 2048 41.6 and 45.9; 512 rows of 8 picks 46.8 and 51.6).
+constexpr int64_t kOwnPrepPicks = 512;
 
 // Work before the products, in one launch: copies of rows of whole pieces of
 // 16 bytes of X and of W (no rows: none), a copy of X with zeros for the rows

@@ -40,8 +40,8 @@ __device__ __forceinline__ bool has_gradient(const RowPicks& picks, const float*
 // or its loss is not asked for; what is not finite in such a row of X would
 // reach dW as 0 times it, so dW's product takes a copy with zeros there.
 // One launch: of 1001 rows the copies, the clean rows and the range took 4 to 6
-// us each in launches of their own. Of up to kOwnPrepRows rows that need no
-// padded copies the loss kernel does the same beside its work.
+// us each in launches of their own. Of up to kOwnPrepPicks picks of rows that need
+// no padded copies the loss kernel does the same beside its work.
 // ---------------------------------------------------------------------------
 template <typename T, int THREADS>
 __device__ __forceinline__ void copy_row(const T* from, T* to, int n, int64_t ld, int t) {
@@ -285,9 +285,10 @@ hipError_t launch_entropy_prep(const EntropyPrep& p, hipStream_t s) {
 template <typename T>
 hipError_t launch_entropy_loss(const EntropyArgs& p, hipStream_t s) {
   const int parts = p.stats ? p.groups : p.V / 4;
-  // a wave a row where the rows fill the device (8 rows of 4096 features, 1024 parts: 9.8 us, by 256 threads 5.8)
+  // a wave a row where the rows fill the device (8 rows of 1024 parts: 54.1 us for the call, by 256 threads 53.4)
   const int threads = p.rows >= 1024 ? (parts <= 2048 ? 64 : 1024) : parts <= 128 ? 64 : parts <= 4096 ? 256 : 1024;
-  // and four rows a wave where they are many and have little each (16384 rows of 16 parts: 6.1 us, one a wave 13.4)
+  // and four rows a wave where they are many and have little each (16384 rows of 16 parts: 21.1 us for the call, one a
+  // wave 24.6)
   if (p.rows >= 4096 && parts <= 32)
     entropy_loss_kernel<T, 16><<<(unsigned)((p.rows + 15) / 16), 256, 0, s>>>(p);
   else if (threads == 64)

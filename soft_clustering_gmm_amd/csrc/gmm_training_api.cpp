@@ -52,7 +52,7 @@ static int64_t piece_rows(int64_t N, int64_t bytes, int64_t most) {
 }
 constexpr int64_t kStatPiece = 256ll << 20;   // bytes of a piece's statistics
 // Bytes of a piece's logits, were they float: dW is read and written once for
-// each (8192 x 2048 to 65536 classes: 6062 us in one piece, 6884 in four, 8009 in
+// each (8192 x 2048 to 65536 classes: 5815 us in one piece, 6543 in four, 7617 in
 // eight).
 constexpr int64_t kLogitPiece = 2048ll << 20;
 
@@ -96,11 +96,11 @@ static EntropyPlan entropy_plan(int64_t N, int d_in, int V, int e) {
 // Up to so many features, and where the logits are more than the caches keep at
 // hand, they are computed twice, once for the loss and once for their gradient,
 // and not written to memory (8192 rows to 32768 classes in bfloat16, against
-// once: 64 features 731 us and 815, 256 922 and 931, 512 1206 and 1142; to 8192 in
-// float: 64 features 416 and 469, 128 646 and 637; 4096 rows to 4096 classes in
-// bfloat16, 64 MiB of float: 64 features 72 and 80; 1000 rows to 8000, 32 MiB: 512
-// features 90 and 88; 8192 to 1024 in float: 91 and 84).
-constexpr int kTwice = 256, kTwiceF32 = 96;
+// once: 64 features 726 us and 753, 96 755 and 747, 256 912 and 881; to 8192 in
+// float: 64 features 433 and 440, 128 669 and 608; 4096 rows to 4096 classes in
+// bfloat16, 64 MiB of float: 64 features 74 and 75; 8192 to 1024 in float, 32 MiB:
+// 84 and 79).
+constexpr int kTwice = 64;
 constexpr int64_t kTwiceBytes = 32ll << 20;
 
 // Workspace of the gradients, for a piece of rows: [padded X] [X without the
@@ -139,9 +139,9 @@ static EntropyBackPlan entropy_back_plan(int64_t N, int d_in, int V, int e) {
   l.pad = l.lx != d_in;
   l.ldz = ceil_div(V, 8) * 8;
   l.piece = piece_rows(N, l.ldz * (int64_t)sizeof(float), kLogitPiece);
-  l.twice = !l.few && d_in <= (e == 2 ? kTwice : kTwiceF32) && l.piece * l.ldz * (int64_t)sizeof(float) > kTwiceBytes;
-  // Rows of a block that has columns of G: 16 at least (of 1001 rows and 7777 classes in half 64 make a block a CU, 17.9
-  // us, and 16 take 10.4), more while 2048 blocks are left, then as many as leave 1024 sums of a column.
+  l.twice = !l.few && d_in <= kTwice && l.piece * l.ldz * (int64_t)sizeof(float) > kTwiceBytes;
+  // Rows of a block that has columns of G: 16 at least (of 1001 rows and 7777 classes in half 64 make a block a CU, and
+  // the call 103.6 us, 16 98), more while 2048 blocks are left, then as many as leave 1024 sums of a column.
   const int64_t across = ceil_div(l.ldz, 64 * (16 / e));
   l.chunk = std::max<int64_t>(16, std::min<int64_t>(64, l.piece * across / 2048 / 16 * 16));
   l.chunk = std::max(l.chunk, ceil_div(ceil_div(l.piece, 1024), 16) * 16);
@@ -264,8 +264,8 @@ static hipError_t entropy_gradients(EntropyArgs a, int64_t N, T* dX, T* dW, T* d
     a.dloss = row_at(all.dloss, r, 1);
     a.loss = row_at(all.loss, r, 1);
     a.lse = row_at(all.lse, r, 1);
-    // few rows in their place: the loss kernel does the rest
-    const bool alone = N <= kOwnPrepRows && !pad_x && !pad_w;
+    // few picks, and rows in their place: the loss kernel does the rest
+    const bool alone = N * a.picks.top <= kOwnPrepPicks && !pad_x && !pad_w;
     a.own_range = alone;
     a.clean = alone && dW ? ws + l.o_clean : nullptr;
     a.ldx = l.lx;
@@ -280,8 +280,8 @@ static hipError_t entropy_gradients(EntropyArgs a, int64_t N, T* dX, T* dW, T* d
     if (!alone && (e = launch_entropy_prep<T>(b, s)) != hipSuccess) return e;
     ProductArgs p{};
     p.partial = reinterpret_cast<float*>(ws + l.o_part);
-    // the logits, through the caches, which the next kernel finds them in (2048 x 1024 to 32768 classes: 580 us against
-    // 598 past them)
+    // the logits, through the caches, which the next kernel finds them in (16384 x 128 to 1024 classes in float: 170 us
+    // for the call, past them 172; 2048 x 128 to 32768, 256 MiB: 612 and 605; 2-byte operands within 1 us)
     a.stats = a.picked = nullptr;
     if (l.few) {
       const FewArgs f{a.X, a.W, (int)N, a.V, a.d_in, a.bias, nullptr, const_cast<float*>(a.Z), nullptr, 1, l.ldz};
