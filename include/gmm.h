@@ -466,13 +466,14 @@ int gmm_cross_entropy(const void* X, int32_t x_dtype, int64_t N, int32_t d_in, c
                       void* workspace, size_t ws_bytes, void* stream);
 
 /* The same with the gradients of sum_n dloss_n loss_n (dloss nullable: 1) in one
- * call, each logit computed once. With p = exp(z - lse) and s_n = sum_j w_nj:
+ * call. With p = exp(z - lse) and s_n = sum_j w_nj:
  *   G_nv = dloss_n (s_n p_nv - sum_j w_nj [idx_nj = v]),
  *   dX = G W,  dW = G^T X,  db = sum_n G_n
  * dX (N x d_in), dW (V x d_in) and db (V) have type x_dtype; each is nullable, as
  * lse is. A row of no picks, or whose dloss is 0, has no part in the gradients,
- * whatever its X holds. G and, where the features are many, the logits pass through
- * the workspace in pieces of rows, of at most 2^29 logits (256 rows at least). lse
+ * whatever its X holds. The logits are computed once, and pass through the workspace
+ * as G does, in pieces of rows of at most 2^29 logits (256 rows at least); or twice,
+ * where the features are few, and only G is written. lse
  * and loss come from the float logits; for G of 2-byte operands p may have been kept
  * in half, as its quotient by the largest of its row and of the 32 or 64 columns around
  * it, so that it is off by 2^-11 of itself, and below 2^-29 of that largest by 2^-40 of
@@ -519,7 +520,8 @@ size_t gmm_cross_entropy_workspace_bytes(int64_t N, int32_t d_in, int32_t V, int
  * x = (x ^ x >> 16) * 0x7FEB352D, x = (x ^ x >> 15) * 0x846CA68B, x ^= x >> 16;
  * the low half is m's, the high half v's, and the larger neighbour is taken where
  * the half / 65536 and the share beyond the smaller come to 1 or more. The step
- * itself is taken from the unrounded m and v.
+ * itself is taken from the unrounded m and v. (The hash's shifts and factors: C. Wellons,
+ * "Prospecting for Hash Functions", 2018.)
  *
  * step (device, 2 int64, 8-byte aligned) holds the number of steps done, which the
  * call counts up by one, and a word for the library's own use that has to be 0 between calls. All

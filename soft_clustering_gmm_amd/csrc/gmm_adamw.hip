@@ -11,7 +11,10 @@ constexpr int kAdamWaves = 4;
 constexpr float kF8Most = 448.f;  // the largest e4m3 value
 
 // 32 bits for an element of the state at a step: what decides how its 8-bit
-// states are rounded. A multiply-xorshift hash; the states repeat exactly.
+// states are rounded; the states repeat exactly. A multiply-xorshift hash with the
+// shifts and factors that C. Wellons' search for such hashes of least bias
+// published ("Prospecting for Hash Functions", 2018); the step's factor is 2^32
+// over the golden ratio.
 __device__ __forceinline__ uint32_t chance(uint32_t place, uint32_t step) {
   uint32_t x = place ^ (step * 0x9E3779B1u);
   x = (x ^ (x >> 16)) * 0x7FEB352Du;
@@ -198,9 +201,9 @@ struct AdamLane {
 // g once. A wave takes 256 elements (a block of the state) at a time, 4
 // consecutive ones a lane, with 4 blocks in flight. The tensors come in the
 // kernel's arguments, so that a launch needs no table in memory. 268M bfloat16
-// parameters with float copies and states: 1335 us, 5.6 TB/s; with one block in
+// parameters with float copies and states: 1340 us, 5.6 TB/s; with one block in
 // flight 1346, through the caches 1435, with 512 blocks of the state a thread
-// block 1436. The same with 8 bits: 811 us, 5.3 TB/s, and 841, 847, 869.
+// block 1436. The same with 8 bits: 804 us, 5.3 TB/s, and 841, 847, 869.
 // 8 bits: m and sqrt(v) as e4m3 with a scale for each 256 elements, its largest
 // finite value / 448; sqrt(v) because its range is half as wide.
 // ---------------------------------------------------------------------------

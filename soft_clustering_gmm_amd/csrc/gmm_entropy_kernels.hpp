@@ -91,10 +91,12 @@ __global__ void __launch_bounds__(256) entropy_prep_kernel(const EntropyPrep p) 
 // The scale of G: the largest |dloss w| becomes 2^11 (no entry passes 16 times
 // that, 8 picks and the probability's share of as many), and the products take it
 // back. So half's range is kept, and where all picks weigh the same, as under a
-// mean over labelled rows, their entries dloss (p - 1) lie next to 2^11, not next
-// to a number whose rounding all rows share: in bfloat16 the gradients of 8192
-// rows were off by 0.0029 without (1 / 7373 is 0.0024 from its neighbour), and are
-// by 0.0017, their own rounding. In every thread of a wave.
+// mean over labelled rows, the entries dloss (p - 1) of picks of p near 0 lie next
+// to 2^11, not next to a number whose rounding all rows share: in bfloat16 the
+// gradients of 8192 rows were off by 0.0029 without (1 / 7373 is 0.0024 from its
+// neighbour), and are by 0.0017, as by one rounding at the end. Entries of picks
+// of any p are rounded on their own besides: 0.0023 at a mean p of one half. In
+// every thread of a wave.
 __device__ __forceinline__ float gradient_scale(const EntropyArgs& p) {
   float most = 0.f;
   if (p.own_range) {
@@ -207,8 +209,8 @@ __global__ void __launch_bounds__(THREADS > 256 ? THREADS : 256) entropy_loss_ke
 // HBM bounds it. GROUPED: 2-byte operands' logits lie in G's place as exp(z - the
 // largest z of their row and group of columns), in half: a probability is off by
 // 2^-11 of itself, no more than G's rounding puts it off by, and below 2^-29 of the
-// largest of its group by 2^-40 of that (8192 x 65536: 401 us, against 600 from
-// floats, which the product took 240 us more to write).
+// largest of its group by 2^-40 of that (8192 x 65536: 394 us, 5.4 TB/s; from
+// floats 600, which the product took 240 us more to write).
 // ---------------------------------------------------------------------------
 template <typename T, bool GROUPED>
 __global__ void __launch_bounds__(256) entropy_gradient_kernel(const EntropyArgs p, int across) {

@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(norm_threads(G)) norm_kernel(const NormArgs p)
 // One read of X and dY (two of rows of more than 16384 elements, the second from
 // the caches): a thread keeps its columns' sums over the rows that its
 // block takes; they go to `partial` and are added in a fixed order. HBM bounds
-// it (16384 x 2048, float X and bfloat16 dY: 62 us, 5.4 TB/s). 1024 threads have
+// it (16384 x 2048, float X and bfloat16 dY: 60 us, 5.6 TB/s). 1024 threads have
 // 128 registers each, and rows of 8193 to 16384 elements want more: gamma is read
 // again, and up to 54 of the registers are kept in memory where X is float and dY
 // is not or the pieces are moved (4096 x 16384: float 182 us, bfloat16 114, float

@@ -841,7 +841,7 @@ def cross_entropy(X, W, idx, *, wts=None, bias=None, ws=None):
     None) are those of assign_top2 or kmeans_assign, or any other labels; a pick outside [0, V) counts for nothing. loss
     carries gradients to X, W and bias (first derivatives; lse carries none), for which the logits are computed again. A
     training step that knows its loss's gradients beforehand (a mean over the rows) calls cross_entropy_gradients, under
-    torch.no_grad(), and computes them once; so does a captured step."""
+    torch.no_grad(), and saves that; so does a captured step."""
     if _tracked(X, W, bias, wts):
         return _CrossEntropy.apply(X, W, bias, idx, wts, ws)
     N, d_in, V, top, dev, xt = _entropy_args(X, W, bias, idx, wts)
