@@ -425,7 +425,8 @@ size_t gmm_expert_workspace_bytes(int64_t N, int32_t D, int32_t K, int32_t F, in
  * mean and rstd, which the backward call needs. eps > 0. Arithmetic is float
  * (a row's values, and the squares of their deviations from its mean, which is off by
  * up to 2^-17 of the largest value, have to sum to less than 3.4e38), rounded once per
- * output; rows may start at any element. What is not finite in a row reaches that row alone. Y may be X itself where their types agree. */
+ * output; rows may start at any element. What is not finite in a row reaches that row
+ * alone. Y may be X itself where their types agree. */
 int gmm_layer_norm(const void* X, int32_t x_dtype, int64_t N, int32_t D, const void* gamma, const void* beta,
                    int32_t w_dtype, float eps, void* Y, int32_t y_dtype, float* stats, void* stream);
 
@@ -473,11 +474,10 @@ int gmm_cross_entropy(const void* X, int32_t x_dtype, int64_t N, int32_t d_in, c
  * lse is. A row of no picks, or whose dloss is 0, has no part in the gradients,
  * whatever its X holds. The logits are computed once, and pass through the workspace
  * as G does, in pieces of rows of at most 2^29 logits (256 rows at least); or twice,
- * where the features are few, and only G is written. lse
- * and loss come from the float logits; for G of 2-byte operands p may have been kept
- * in half, as its quotient by the largest of its row and of the 32 or 64 columns around
- * it, so that it is off by 2^-11 of itself, and below 2^-29 of that largest by 2^-40 of
- * it. The products take G rounded to
+ * where the features are few, and only G is written. lse and loss come from the float
+ * logits; for G of 2-byte operands p may have been kept in half, as its quotient by the
+ * largest of its row and of the 32 or 64 columns around it, so that it is off by 2^-11 of
+ * itself, and below 2^-29 of that largest by 2^-40 of it. The products take G rounded to
  * x_dtype, as the matrix instructions do, and accumulate in float; 2-byte operands
  * take it scaled so that the largest |dloss_n w_nj| becomes 2^11, which is
  * taken back from the sums, so that half keeps its 11 bits down to 2^-25 of
@@ -528,7 +528,7 @@ size_t gmm_cross_entropy_workspace_bytes(int64_t N, int32_t d_in, int32_t V, int
  * arithmetic is float, the powers of beta double. m, v and master are 16-byte
  * aligned. beta1 and beta2 from 0 to below 1, lr and weight_decay >= 0, eps at least
  * 1.17549435e-38 (a normal float), all of them finite as floats.
- * No parameter may overlap another tensor of the call. */
+ * No parameter may overlap another tensor of the call, nor may two of the state's. */
 int gmm_adamw_step(int32_t count, const int64_t* sizes, void* const* params, int32_t p_dtype,
                    const void* const* grads, int32_t g_dtype, float* master, void* m, void* v, int32_t state_bits,
                    float* m_scale, float* v_scale, int64_t* step, double lr, double beta1, double beta2, double eps,

@@ -455,7 +455,8 @@ product_kernel(const ProductArgs p) {
 #pragma unroll
     for (int u = 0; u < kPickLoads; ++u) {
       const int i = u * 64 * NW + threadIdx.x;
-      pick[u] = i < BM * p.picks.top && at.m0 * p.picks.top + i < p.M * p.picks.top ? p.picks.idx[at.m0 * p.picks.top + i] : -1;
+      const int64_t in = at.m0 * p.picks.top + i;
+      pick[u] = i < BM * p.picks.top && in < p.M * p.picks.top ? p.picks.idx[in] : -1;
     }
   load_a(0, 0), load_b(0), load_a(0, 1);
   load_a(1, 0), load_b(1), load_a(1, 1);
@@ -488,8 +489,9 @@ product_kernel(const ProductArgs p) {
       if (u * 64 * NW + (int)threadIdx.x < BM * p.picks.top) picks[u * 64 * NW + threadIdx.x] = pick[u];
   step_barrier<0>(lds);  // nobody reads the slots, and nothing arrives in them any more
   if constexpr (ACT == kRowStats || ACT == kStatsToo)
-    row_stats<T, 2 * MI, NI, kKept<T, ACT>, kPicks>(p, acc[0], [&](int i) { return at.m0 + i / MI * HM + wm * TM + 16 * (i % MI); }, picks,
-                             at.m0, at.n0 + wn * TN, at.n0 / BN * WN + wn, p.tiles_n * WN, lane);
+    row_stats<T, 2 * MI, NI, kKept<T, ACT>, kPicks>(
+        p, acc[0], [&](int i) { return at.m0 + i / MI * HM + wm * TM + 16 * (i % MI); }, picks, at.m0, at.n0 + wn * TN,
+        at.n0 / BN * WN + wn, p.tiles_n * WN, lane);
   if constexpr (ACT == kRowStats) return;
 
   // The results go through LDS, 16 rows of m at a time in memory of the wave's

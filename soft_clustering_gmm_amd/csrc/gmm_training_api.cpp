@@ -105,8 +105,9 @@ constexpr int64_t kTwiceBytes = 32ll << 20;
 
 // Workspace of the gradients, for a piece of rows: [padded X] [X without the
 // rows that have no gradient] [padded W] [logits] [their gradient] [statistics]
-// [the picks' logits] [coefficients] [dW so far] [partial sums of the products] [column sums of the
-// tiles] [column sums, those of the pieces before first] [range and scale].
+// [the picks' logits] [coefficients] [dW so far] [partial sums of the products]
+// [column sums of the tiles] [column sums, those of the pieces before first]
+// [range and scale].
 struct EntropyBackPlan {
   bool few, pad;
   bool twice;  // the logits are computed twice and not written
